@@ -12,6 +12,10 @@ Attention" (sections 4-5); API shape from the HPC-Ops pull request
     counters = torch.zeros(counter_bytes, dtype=torch.uint8, device="cuda")
     workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
     topk(logits, ke, output, num_valid_rows, top_k, counters, workspace)
+
+The operators around the selection in a sparse-attention step (an 8-bit paged
+cache, page scores, attention over the cache or its selected pages) are bound
+in ``cache.py`` and offered here too.
 """
 
 from __future__ import annotations
@@ -26,6 +30,8 @@ __all__ = [
     "library", "library_path", "query_device", "make_plan", "workspace_size", "topk", "run",
     "error_string", "version", "stream_floor", "FAMILY_AUTO", "FAMILY_PERSISTENT_SAMPLED", "FAMILY_KV_SPLIT",
     "FAMILY_ROW_LOCAL_EXACT", "FAMILY_CLUSTER_SPLIT", "TRACE_FIELDS", "ROUTES", "EXPORTED_SYMBOLS",
+    "KVCache", "SequenceBatch", "AttentionPlan", "CacheAttention", "SparseAttention", "cache_write",
+    "cache_read", "block_scores", "make_attention_plan", "CACHE_SYMBOLS",
 ]
 
 FAMILY_AUTO = 0
@@ -296,3 +302,7 @@ class ExactTopK:
                               device=self.device)
         return run(self.plan, logits, ke, out, num_valid_rows, self.counters, self.workspace,
                    prev_topk=prev_topk, trace=trace, stream=stream)
+
+
+from .cache import (CACHE_SYMBOLS, AttentionPlan, CacheAttention, KVCache, SequenceBatch,  # noqa: E402
+                    SparseAttention, block_scores, cache_read, cache_write, make_attention_plan)

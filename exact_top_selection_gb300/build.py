@@ -1,6 +1,6 @@
 """Builds libexact_topk.so in-tree for sm_103a (nvcc + g++, no CMake).
 
-The CUDA translation unit and the host planner compile in parallel; the shared
+The CUDA translation units and the host sources compile in parallel; the shared
 library links the CUDA runtime dynamically so that it shares one runtime (and
 its streams) with PyTorch in the same process.
 """
@@ -21,8 +21,11 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(BUILD_DIR, "libexact_topk.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["topk_kernels.cu", "exact_topk_api.cpp"]
-HEADERS = ["etk_internal.h"]
+CUDA_SOURCES = ["topk_kernels.cu", "cache_kernels.cu", "score_kernels.cu",
+                "attention_kernels.cu"]
+HOST_SOURCES = ["exact_topk_api.cpp", "cache_api.cpp"]
+HEADERS = ["etk_internal.h", "cache_internal.h", "cache_device.cuh"]
+PUBLIC_HEADERS = ["exact_topk.h", "exact_topk_cache.h"]
 
 
 def cuda_home() -> str:
@@ -36,8 +39,8 @@ def cuda_home() -> str:
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-    files.append(os.path.join(INCLUDE, "exact_topk.h"))
+    files = [os.path.join(CSRC, s) for s in CUDA_SOURCES + HOST_SOURCES + HEADERS]
+    files += [os.path.join(INCLUDE, h) for h in PUBLIC_HEADERS]
     files.append(os.path.abspath(__file__))
     return files
 
@@ -67,25 +70,27 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not os.path.exists(nvcc):
         nvcc = "nvcc"
     inc = ["-I", INCLUDE, "-I", CSRC]
-    obj_cu = os.path.join(BUILD_DIR, "topk_kernels.o")
-    obj_api = os.path.join(BUILD_DIR, "exact_topk_api.o")
     cu_cmd = [nvcc, *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
-              "--expt-relaxed-constexpr", *inc, "-c", os.path.join(CSRC, "topk_kernels.cu"),
-              "-o", obj_cu]
+              "--expt-relaxed-constexpr", *inc]
     if verbose_ptxas:
         cu_cmd.insert(1, "-Xptxas=-v")
-    api_cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", *inc,
-               "-I", os.path.join(home, "include"), "-c",
-               os.path.join(CSRC, "exact_topk_api.cpp"), "-o", obj_api]
-    with ThreadPoolExecutor(2) as ex:
-        outs = list(ex.map(_run, [cu_cmd, api_cmd]))
+    host_cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", *inc,
+                "-I", os.path.join(home, "include")]
+    cmds, objects = [], []
+    for cmd, sources in ((cu_cmd, CUDA_SOURCES), (host_cmd, HOST_SOURCES)):
+        for source in sources:
+            obj = os.path.join(BUILD_DIR, os.path.splitext(source)[0] + ".o")
+            cmds.append([*cmd, "-c", os.path.join(CSRC, source), "-o", obj])
+            objects.append(obj)
+    with ThreadPoolExecutor(len(cmds)) as ex:
+        outs = list(ex.map(_run, cmds))
     tmp = LIBRARY + f".tmp{os.getpid()}"
     libdir = os.path.join(home, "lib64")
-    _run([nvcc, *ARCH_FLAGS, "-shared", "-cudart", "shared", obj_cu, obj_api, "-o", tmp,
+    _run([nvcc, *ARCH_FLAGS, "-shared", "-cudart", "shared", *objects, "-o", tmp,
           "-Xlinker", f"-rpath={libdir}"])
     os.replace(tmp, LIBRARY)
     if verbose_ptxas:
-        sys.stdout.write(outs[0])
+        sys.stdout.write("".join(outs))
     return LIBRARY
 
 

@@ -1,0 +1,73 @@
+// Internal interface between the host checks of the cache operators
+// (cache_api.cpp) and their kernels (cache_kernels.cu, score_kernels.cu,
+// attention_kernels.cu).  Not installed.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime_api.h>
+
+#include "exact_topk_cache.h"
+
+namespace etk {
+
+// The arguments of a checked call as the kernels take them.
+struct CacheArgs {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  void* bounds;
+  int num_pages, heads, page, page_shift, dim, fp16;
+};
+
+struct BatchArgs {
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* q_start;  // NULL: one row for each sequence
+  int64_t table_pitch;
+  int64_t num_tokens;
+  int num_seqs, width;
+};
+
+struct RowArgs {
+  void* data;
+  int64_t token_stride, head_stride;
+};
+
+struct ScoreArgs {
+  RowArgs q;
+  float* scores;
+  int32_t* ke;
+  int32_t* num_valid_rows;
+  int64_t row_pitch;
+  int group, keep_first, keep_last;
+};
+
+struct AttentionArgs {
+  RowArgs q, out;
+  const int32_t* blocks;  // NULL: the whole cache
+  int32_t* counters;      // [workers] arrivals at the tile a worker starts and does not finish
+  float* partial;         // [workers][2] partial tiles (partial_floats each)
+  float scale_log2;       // softmax scale * log2(e)
+  int num_blocks, group, columns, tile_tokens, tile_heads, workers, min_units;
+};
+
+// Floats of one partial tile: running maxima and sums (a pair for each of 4
+// lanes' two columns of every 8, kept for all 32 lanes) and the outputs.
+constexpr int64_t partial_floats(int columns, int dim) {
+  return (int64_t)columns / 8 * 32 * 4 + (int64_t)columns * dim;
+}
+
+// Resident CTAs that the attention kernels are built for.
+constexpr int attention_ctas_per_sm(int columns) { return columns == 8 ? 3 : 2; }
+
+int launch_cache_write(const CacheArgs&, const BatchArgs&, const RowArgs& k, const RowArgs& v,
+                       cudaStream_t);
+int launch_cache_read(const CacheArgs&, const BatchArgs&, const RowArgs& k, const RowArgs& v,
+                      cudaStream_t);
+int launch_block_scores(const CacheArgs&, const BatchArgs&, const ScoreArgs&, cudaStream_t);
+int launch_attention(const CacheArgs&, const BatchArgs&, const AttentionArgs&, cudaStream_t);
+
+}  // namespace etk

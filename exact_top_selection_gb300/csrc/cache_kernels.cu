@@ -1,0 +1,310 @@
+// Writing rows into the paged 8-bit cache and reading them back
+// (exact_topk_cache_write, exact_topk_cache_read).
+//
+// Both move bytes and are bound by HBM.  A CTA takes the part of one page that
+// a sequence's rows reach: its codes are contiguous, its rows whole channels of
+// one head, so every access is a full line.  The CTAs are laid over the pages
+// without any host knowledge of lengths (first_slot).
+
+#include "cache_device.cuh"
+
+namespace etk {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+
+// The part of a page that a slot's sequence reaches with its rows.
+struct PagePart {
+  SeqRows rows;
+  int seq, block, first, end;  // offsets [first, end) of page `block` of the sequence
+  int index;                   // 0: the sequence's first part
+};
+
+// False where the slot has no part (first == end may still hold for index 0).
+__device__ __forceinline__ bool page_part(const BatchArgs& b, int page_shift, int64_t slot,
+                                          PagePart* part) {
+  const int P = 1 << page_shift;
+  part->seq = sequence_of_slot(b, slot, P, 2);
+  part->rows = sequence_rows(b, page_shift, part->seq);
+  part->index = (int)(slot - first_slot(b, part->seq, P, 2));
+  const int begin = part->rows.pos0 > 0 ? part->rows.pos0 : 0;
+  part->block = (begin >> page_shift) + part->index;
+  const int64_t base = (int64_t)part->block << page_shift;
+  const int64_t left = (int64_t)part->rows.len - base;
+  part->first = part->index == 0 ? begin & (P - 1) : 0;
+  part->end = left < P ? (int)left : P;
+  return part->index >= 0 && part->rows.count > 0 && part->end > part->first;
+}
+
+// 2^e with the smallest e in range for which amax <= 448 * 2^e.  448 = 1.75 * 2^8,
+// so a magnitude 1.m * 2^x needs e = x - 8, one more where 1.m > 1.75.
+__device__ __forceinline__ float scale_for(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  e = e < EXACT_TOPK_SCALE_MIN_EXP ? EXACT_TOPK_SCALE_MIN_EXP : e;
+  e = e > EXACT_TOPK_SCALE_MAX_EXP ? EXACT_TOPK_SCALE_MAX_EXP : e;
+  return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Two numbers as codes.  y + 0 * y is y, and NaN for an infinity, which the
+// saturating conversion would otherwise turn into 448.
+__device__ __forceinline__ uint32_t encode2(float x, float y) {
+  const float2 v = make_float2(fmaf(x, 0.f, x), fmaf(y, 0.f, y));
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float finite_magnitude(float x) {
+  const float a = fabsf(x);
+  return a < __uint_as_float(0x7F800000u) ? a : 0.f;
+}
+
+// One pass over the rows: a page's part is held in registers (8 channels a thread
+// and row, P * D / 1024 rows of the page), its largest magnitude found across
+// the CTA, then coded and stored.  Keys and values are separate CTAs (blockIdx.z).
+// Scales are powers of two: e4m3 is a floating format, so a finer scale would only
+// move the borders of its exponents, and with powers of two every division here and
+// every product on reading is exact.
+template <bool kFp16, int D, int P>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs c, BatchArgs b,
+                                                               RowArgs krows, RowArgs vrows) {
+  constexpr int kLanes = D / 8;               // threads on a row
+  constexpr int kRows = kThreads / kLanes;    // rows of a pass
+  constexpr int kPasses = P / kRows > 0 ? P / kRows : 1;
+  constexpr int kShift = P == 16 ? 4 : (P == 32 ? 5 : (P == 64 ? 6 : 7));
+  __shared__ float s_max[kWarps];
+  __shared__ float s_hi[kWarps][D], s_lo[kWarps][D];
+
+  PagePart part;
+  if (!page_part(b, kShift, blockIdx.x, &part)) return;
+  const int page = page_of(c, b, part.seq, part.block);
+  if (page < 0) return;
+  const bool keys = blockIdx.z == 0;
+  const RowArgs src = keys ? krows : vrows;
+  uint8_t* const codes = keys ? c.k : c.v;
+  float* const scales = keys ? c.k_scale : c.v_scale;
+  const bool bounds = keys && c.bounds != nullptr;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunk = tid % kLanes, row0 = tid / kLanes;
+  const int64_t row_base = part.rows.begin + (((int64_t)part.block << kShift) - part.rows.pos0);
+  const uint16_t* const rows = static_cast<const uint16_t*>(src.data);
+
+  for (int h = blockIdx.y; h < c.heads; h += gridDim.y) {
+    uint4 x[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int o = row0 + i * kRows;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (o >= part.first && o < part.end)
+        x[i] = *reinterpret_cast<const uint4*>(rows + (row_base + o) * src.token_stride +
+                                               h * src.head_stride + chunk * 8);
+    }
+    float amax = 0.f;
+    float hi[8], lo[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      hi[j] = -__uint_as_float(0x7F800000u);
+      lo[j] = __uint_as_float(0x7F800000u);
+    }
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int o = row0 + i * kRows;
+      if (o < part.first || o >= part.end) continue;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<kFp16>(w[j]);
+        amax = fmaxf(amax, fmaxf(finite_magnitude(f.x), finite_magnitude(f.y)));
+        if (bounds) {
+          const float most = kFp16 ? 65504.f : __uint_as_float(0x7F7F0000u);
+          const float u = f.x == f.x ? fminf(fmaxf(f.x, -most), most) : 0.f;
+          const float v = f.y == f.y ? fminf(fmaxf(f.y, -most), most) : 0.f;
+          hi[2 * j] = fmaxf(hi[2 * j], u);
+          lo[2 * j] = fminf(lo[2 * j], u);
+          hi[2 * j + 1] = fmaxf(hi[2 * j + 1], v);
+          lo[2 * j + 1] = fminf(lo[2 * j + 1], v);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+    if (bounds) {
+#pragma unroll
+      for (int o = 16; o >= kLanes; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          hi[j] = fmaxf(hi[j], __shfl_xor_sync(~0u, hi[j], o));
+          lo[j] = fminf(lo[j], __shfl_xor_sync(~0u, lo[j], o));
+        }
+      if (lane < kLanes)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s_hi[warp][chunk * 8 + j] = hi[j];
+          s_lo[warp][chunk * 8 + j] = lo[j];
+        }
+    }
+    if (lane == 0) s_max[warp] = amax;
+    const int64_t tile = (int64_t)page * c.heads + h;
+    const float held = part.first > 0 ? scales[tile] : 0.f;  // read before it is replaced
+    __syncthreads();
+    amax = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    const float scale = fmaxf(scale_for(amax), held);
+    uint8_t* const out = codes + tile * (P * D);
+    const float inverse = 1.f / scale;  // exact: the scale is a power of two
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int o = row0 + i * kRows;
+      if (o < part.first || o >= part.end) continue;
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = unpack2<kFp16>(w[j]);
+        q[j] = encode2(f.x * inverse, f.y * inverse);
+      }
+      *reinterpret_cast<uint2*>(out + o * D + chunk * 8) =
+          make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+    }
+    if (part.first > 0 && scale != held) {
+      const float ratio = held / scale;
+      for (int o = row0; o < part.first; o += kRows) {
+        uint2* const at = reinterpret_cast<uint2*>(out + o * D + chunk * 8);
+        const uint2 was = *at;
+        const uint32_t w[2] = {was.x, was.y};
+        uint32_t q[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 f0 = codes_to_float2((uint16_t)w[j]);
+          const float2 f1 = codes_to_float2((uint16_t)(w[j] >> 16));
+          q[j] = encode2(f0.x * ratio, f0.y * ratio) | encode2(f1.x * ratio, f1.y * ratio) << 16;
+        }
+        *at = make_uint2(q[0], q[1]);
+      }
+    }
+    if (bounds && tid < D) {
+      float u = fmaxf(fmaxf(s_hi[0][tid], s_hi[1][tid]), fmaxf(s_hi[2][tid], s_hi[3][tid]));
+      float v = fminf(fminf(s_lo[0][tid], s_lo[1][tid]), fminf(s_lo[2][tid], s_lo[3][tid]));
+      uint16_t* const at = static_cast<uint16_t*>(c.bounds) + tile * (2 * D) + tid;
+      if (part.first > 0) {
+        u = fmaxf(u, unpack2<kFp16>(at[0]).x);
+        v = fminf(v, unpack2<kFp16>(at[D]).x);
+      }
+      at[0] = (uint16_t)pack2<kFp16>(u, 0.f);
+      at[D] = (uint16_t)pack2<kFp16>(v, 0.f);
+    }
+    if (tid == 0) scales[tile] = scale;
+    __syncthreads();  // the shared maxima are free for the next head
+  }
+}
+
+// 16 codes a thread and step: one 16-byte load, two 16-byte stores.
+template <bool kFp16>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs c, BatchArgs b,
+                                                              RowArgs krows, RowArgs vrows) {
+  const int P = c.page, D = c.dim;
+  PagePart part;
+  const bool any = page_part(b, c.page_shift, blockIdx.x, &part);
+  const bool keys = blockIdx.z == 0;
+  const RowArgs dst = keys ? krows : vrows;
+  uint16_t* const rows = static_cast<uint16_t*>(dst.data);
+  const int lanes = D / 16, lane_shift = D == 128 ? 3 : 2;
+  const int heads = (c.heads - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
+
+  // rows ahead of the sequence's first token
+  if (part.index == 0 && part.rows.pos0 < 0) {
+    const int none = part.rows.count < -part.rows.pos0 ? part.rows.count : -part.rows.pos0;
+    for (int64_t i = threadIdx.x; i < (int64_t)none * heads * lanes; i += kThreads) {
+      const int64_t r = i / lanes;
+      uint4* const at = reinterpret_cast<uint4*>(
+          rows + (part.rows.begin + r / heads) * dst.token_stride +
+          ((int64_t)blockIdx.y + (r % heads) * gridDim.y) * dst.head_stride + (i % lanes) * 16);
+      at[0] = at[1] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
+  if (!any) return;
+  const int page = page_of(c, b, part.seq, part.block);
+  const int64_t row_base =
+      part.rows.begin + (((int64_t)part.block << c.page_shift) - part.rows.pos0);
+  const uint8_t* const codes = keys ? c.k : c.v;
+  const float* const scales = keys ? c.k_scale : c.v_scale;
+  const int steps = heads << (c.page_shift + lane_shift);
+#pragma unroll 4
+  for (int i = threadIdx.x; i < steps; i += kThreads) {
+    const int chunk = i & (lanes - 1), o = (i >> lane_shift) & (P - 1);
+    const int h = (int)blockIdx.y + (i >> (c.page_shift + lane_shift)) * (int)gridDim.y;
+    if (o < part.first || o >= part.end) continue;
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    float scale = 0.f;
+    if (page >= 0) {
+      const int64_t tile = (int64_t)page * c.heads + h;
+      x = *reinterpret_cast<const uint4*>(codes + (tile * P + o) * D + chunk * 16);
+      scale = scales[tile];
+    }
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f0 = codes_to_float2((uint16_t)w[j]);
+      const float2 f1 = codes_to_float2((uint16_t)(w[j] >> 16));
+      y[2 * j] = pack2<kFp16>(f0.x * scale, f0.y * scale);
+      y[2 * j + 1] = pack2<kFp16>(f1.x * scale, f1.y * scale);
+    }
+    uint4* const at = reinterpret_cast<uint4*>(rows + (row_base + o) * dst.token_stride +
+                                               h * dst.head_stride + chunk * 16);
+    at[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    at[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  }
+}
+
+// Heads are spread over CTAs (blockIdx.y) until there are a few waves of them;
+// beyond that a CTA takes several, so that small pages do not become CTAs of a
+// kilobyte each.
+dim3 page_grid(const CacheArgs& c, const BatchArgs& b) {
+  const int64_t slots = slot_count(b, c.page, 2);
+  int y = c.heads;
+  while (y > 1 && slots * y > 4096 && c.heads / y * c.page * c.dim < 16384) y = (y + 1) / 2;
+  return dim3((unsigned)slots, (unsigned)y, 2u);
+}
+
+template <bool kFp16, int D>
+void write_page(const CacheArgs& c, const BatchArgs& b, const RowArgs& k, const RowArgs& v,
+                cudaStream_t stream) {
+  const dim3 grid = page_grid(c, b);
+  switch (c.page) {
+    case 16:
+      cache_write_kernel<kFp16, D, 16><<<grid, kThreads, 0, stream>>>(c, b, k, v);
+      break;
+    case 32:
+      cache_write_kernel<kFp16, D, 32><<<grid, kThreads, 0, stream>>>(c, b, k, v);
+      break;
+    case 64:
+      cache_write_kernel<kFp16, D, 64><<<grid, kThreads, 0, stream>>>(c, b, k, v);
+      break;
+    default:
+      cache_write_kernel<kFp16, D, 128><<<grid, kThreads, 0, stream>>>(c, b, k, v);
+      break;
+  }
+}
+
+}  // namespace
+
+int launch_cache_write(const CacheArgs& c, const BatchArgs& b, const RowArgs& k, const RowArgs& v,
+                       cudaStream_t stream) {
+  if (c.dim == 128)
+    c.fp16 ? write_page<true, 128>(c, b, k, v, stream) : write_page<false, 128>(c, b, k, v, stream);
+  else
+    c.fp16 ? write_page<true, 64>(c, b, k, v, stream) : write_page<false, 64>(c, b, k, v, stream);
+  return launch_status();
+}
+
+int launch_cache_read(const CacheArgs& c, const BatchArgs& b, const RowArgs& k, const RowArgs& v,
+                      cudaStream_t stream) {
+  const dim3 grid = page_grid(c, b);
+  if (c.fp16)
+    cache_read_kernel<true><<<grid, kThreads, 0, stream>>>(c, b, k, v);
+  else
+    cache_read_kernel<false><<<grid, kThreads, 0, stream>>>(c, b, k, v);
+  return launch_status();
+}
+
+}  // namespace etk

@@ -111,6 +111,14 @@ const char* exact_topk_error_string(int status) {
       return "plan field out of range or inconsistent";
     case EXACT_TOPK_ERR_CUDA:
       return "CUDA runtime call failed";
+    case EXACT_TOPK_ERR_BAD_CACHE:
+      return "bad cache: need pages of 16, 32, 64 or 128 tokens, head_dim 64 or 128, 1 <= kv_heads "
+             "<= 1024, type bf16 or fp16";
+    case EXACT_TOPK_ERR_BAD_BATCH:
+      return "bad batch: need 1 <= num_seqs <= 4096, table_width * page_size <= 2^30, num_tokens == "
+             "num_seqs without q_start, table_width <= 131072 with a page list";
+    case EXACT_TOPK_ERR_BAD_HEADS:
+      return "bad heads: need q_heads a multiple of kv_heads, at most 65536";
     default:
       return "unknown exact_topk status";
   }

@@ -62,7 +62,11 @@ typedef enum exact_topk_status {
   EXACT_TOPK_ERR_MISALIGNED = -6,       /* logits/ke/out/counters/workspace not 4-byte aligned
                                            (counters and workspace must be 16-byte aligned) */
   EXACT_TOPK_ERR_BAD_PLAN = -7,         /* a plan field is out of range or inconsistent */
-  EXACT_TOPK_ERR_CUDA = -8              /* a CUDA runtime call failed (device query or launch) */
+  EXACT_TOPK_ERR_CUDA = -8,             /* a CUDA runtime call failed (device query or launch) */
+  /* the cache operators of exact_topk_cache.h */
+  EXACT_TOPK_ERR_BAD_CACHE = -9,        /* a cache field is out of range or of no supported size */
+  EXACT_TOPK_ERR_BAD_BATCH = -10,       /* a batch field is out of range or does not fit the call */
+  EXACT_TOPK_ERR_BAD_HEADS = -11        /* q_heads < 1, too large or no multiple of kv_heads */
 } exact_topk_status;
 
 #define EXACT_TOPK_MAX_K 16384
