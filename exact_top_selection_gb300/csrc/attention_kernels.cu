@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 512;   // pages whose ids are held in shared memory at a time
+constexpr int kChunk = 128;   // pages whose ids are held in shared memory at a time
 constexpr int kStep = 16;     // tokens of a matrix instruction
 // The running maximum is raised only when a score is more than this above it (in
 // powers of two): probabilities then reach 2^8, and the sums are rescaled a few
@@ -70,18 +70,20 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 r;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-      : "l"(p));
-  return r;
+// 16 bytes to shared memory, asynchronously; zeros where !there.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+               "r"(there ? 16 : 0)
+               : "memory");
 }
 
-__device__ __forceinline__ uint2 load8(const void* p) {
-  uint2 r;
-  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
@@ -112,28 +114,29 @@ __device__ __forceinline__ void tile_shape(const AttentionArgs& a, const CacheAr
   *units = n > 0 ? n : 1;
 }
 
+// Steps of 16 tokens that a warp holds in shared memory, all but one of them on their
+// way.
+constexpr int ring_steps(int dim, int tiles) {
+  return (tiles == 1 ? 3 : 5) * (dim == 64 ? 2 : 1);
+}
+
 template <int D, int NT>
-struct alignas(16) Shared {
+struct alignas(128) Shared {
   static constexpr int kRegs = D / 16 * NT * 4;  // output registers of a lane
   static constexpr int kRow = D + 8;             // halves of a query row, padded by 16 bytes
-  float out[kWarps][kRegs][32];
+  static constexpr int kRing = ring_steps(D, NT);
+  union {
+    uint8_t ring[kWarps][kRing][2][kStep * D];  // codes of keys and values
+    float out[kWarps][kRegs][32];               // after the last step
+  };
   float stat[kWarps][NT * 4][32];  // m and l of a lane's two columns of every 8
   __half q[NT * 8][kRow];
   float factor[NT * 8];
   int page[kChunk];
   uint32_t entry[kChunk];          // place in the sequence | members << 24
+  float2 scale[kChunk];            // of keys and values
   int scan[kWarps];
   int last;
-};
-
-// The 16 tokens of a step in a lane's registers.
-template <int D>
-struct Step {
-  uint4 k[2][D / 64];   // rows lane / 4 and lane / 4 + 8: chunks of 16 channels
-  uint4 v[4];           // tokens 2c, 2c+1, 2c+8, 2c+9 (c = lane % 4): D / 8 channels
-  float k_scale, v_scale;
-  int pos;              // first token's position
-  uint32_t members;     // tokens of the tile that take the page; 0: nothing to do
 };
 
 template <int D, int NT>
@@ -340,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8))
     const uint32_t everyone = (1u << t.tokens) - 1u;
     float unit = 1.f;  // the values' scale that o is held in
 
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0][0]);
     // steps of 16 tokens: a warp takes two in a row (a page of 16 has one)
     const int pair_shift = c.page >= 32 ? 1 : 0;
     const int sub_shift = c.page_shift - 4 - pair_shift;  // log2 of (pairs of) steps a page
@@ -356,17 +360,21 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8))
           for (int k = 0; k < 4; ++k) {
             const uint32_t who = w >> (8 * k) & 255u;
             if (who == 0u) continue;
-            if (at >= chunk0 && at < chunk0 + entries) {
+            if (at >= chunk0 && at < chunk0 + entries)
               sm.entry[at - chunk0] = (uint32_t)(i * 4 + k) | who << 24;
-              sm.page[at - chunk0] = page_of(c, b, t.seq, i * 4 + k);
-            }
             ++at;
           }
         }
-      } else {
-        for (int i = tid; i < entries; i += kThreads) {
-          sm.entry[i] = (uint32_t)(chunk0 + i);
-          sm.page[i] = page_of(c, b, t.seq, chunk0 + i);
+        __syncthreads();
+      }
+      for (int i = tid; i < entries; i += kThreads) {
+        const int place = listed ? (int)(sm.entry[i] & 0xFFFFFFu) : chunk0 + i;
+        const int page = page_of(c, b, t.seq, place);
+        sm.page[i] = page;
+        if (!listed) sm.entry[i] = (uint32_t)place;
+        if (page >= 0) {
+          const int64_t tile = (int64_t)page * c.heads + t.head;
+          sm.scale[i] = make_float2(__ldg(c.k_scale + tile), __ldg(c.v_scale + tile));
         }
       }
       __syncthreads();
@@ -374,214 +382,280 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8))
       const int subs = entries << sub_shift;
       const int steps = warp < subs ? ((subs - warp + kWarps - 1) / kWarps) << pair_shift : 0;
 
-      auto fetch = [&](int i, Step<D>& s) {
-        s.members = 0u;
-        if (i >= steps) return;
+      // Step i of this warp: its entry, and its first row in the page.
+      const auto find = [&](int i, int* e, int* row0) {
         const int sub = warp + (i >> pair_shift) * kWarps;
-        const int e = sub >> sub_shift;
-        const int row0 = ((sub & ((1 << sub_shift) - 1)) << (4 + pair_shift)) +
-                         ((i & ((1 << pair_shift) - 1)) << 4);
-        const uint32_t entry = sm.entry[e];
-        const int page = sm.page[e];
-        const int place = listed ? (int)(entry & 0xFFFFFFu) : (int)entry;
-        s.pos = (place << c.page_shift) + row0;
-        const int rows = most - s.pos;  // tokens that anyone sees
-        if (page < 0 || rows <= 0) return;
-        s.members = listed ? entry >> 24 : everyone;
-        const int64_t tile = (int64_t)page * c.heads + t.head;
-        const int64_t at = (tile * c.page + row0) * D;
-        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int p = 0; p < kHalf; ++p)
-            s.k[r][p] = g + 8 * r < rows
-                            ? load16(c.k + at + (g + 8 * r) * D + p * 64 + q4 * 16)
-                            : none;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int row = q4 * 2 + (r & 1) + (r >> 1) * 8;
-          s.v[r] = none;
-          if (row < rows) {
-            if (D == 128) {
-              s.v[r] = load16(c.v + at + row * D + g * 16);
-            } else {
-              const uint2 half = load8(c.v + at + row * D + g * 8);
-              s.v[r].x = half.x;
-              s.v[r].y = half.y;
-            }
-          }
-        }
-        s.k_scale = __ldg(c.k_scale + tile);
-        s.v_scale = __ldg(c.v_scale + tile);
+        *e = sub >> sub_shift;
+        *row0 = ((sub & ((1 << sub_shift) - 1)) << (4 + pair_shift)) +
+                ((i & ((1 << pair_shift) - 1)) << 4);
+      };
+      const auto position = [&](int e, int row0) {
+        const int place = listed ? (int)(sm.entry[e] & 0xFFFFFFu) : (int)sm.entry[e];
+        return (place << c.page_shift) + row0;
       };
 
-      auto compute = [&](const Step<D>& s) {
-        if (s.members == 0u) return;
-        // S^T
-        float x[NT][4];
+      // Codes of step i into its place of the ring. A step is contiguous in memory. In
+      // shared memory its 16-byte pieces are exchanged within lines of 128 bytes so
+      // that the reads below touch every bank once.
+      const auto fetch = [&](int i) {
+        if (i < steps) {
+          int e, row0;
+          find(i, &e, &row0);
+          const int page = sm.page[e];
+          const int rows = most - position(e, row0);  // tokens that anyone sees
+          if (page >= 0 && rows > 0) {
+            const int64_t at =
+                (((int64_t)page * c.heads + t.head) * c.page + row0) * D + lane * 16;
+            const uint32_t to = ring + (i % Smem::kRing) * (2 * kStep * D);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) x[n][r] = 0.f;
-#pragma unroll
-        for (int p = 0; p < kHalf; ++p)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t w0 = word(s.k[0][p], i), w1 = word(s.k[1][p], i);
-            const uint32_t a0 = codes_to_half2((uint16_t)w0);
-            const uint32_t a2 = codes_to_half2((uint16_t)(w0 >> 16));
-            const uint32_t a1 = codes_to_half2((uint16_t)w1);
-            const uint32_t a3 = codes_to_half2((uint16_t)(w1 >> 16));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              if (NT > 1 && (s.members & have[n]) == 0u) continue;
-              uint4 q;  // channels of steps i and i ^ 1
-              if (kHoldQ)
-                q = held[n][p][i >> 1];
-              else
-                q = *reinterpret_cast<const uint4*>(
-                    &sm.q[n * 8 + g][p * 64 + q4 * 16 + (i >> 1) * 8]);
-              mma(x[n], a0, a1, a2, a3, i & 1 ? q.z : q.x, i & 1 ? q.w : q.y);
+            for (int j = 0; j < D / 32; ++j) {
+              const int piece = lane + 32 * j, line = piece >> 3, p = piece & 7;
+              const bool there = (D == 128 ? line : piece >> 2) < rows;
+              const int pk = D == 128 ? p ^ ((line & 1) << 2) : p;
+              const int pv = D == 128 ? p ^ ((line >> 1 & 3) << 1) : p ^ ((line & 3) << 1);
+              copy16(to + line * 128 + pk * 16, c.k + at + j * 512, there);
+              copy16(to + kStep * D + line * 128 + pv * 16, c.v + at + j * 512, there);
             }
-          }
-        const bool masked = s.pos + kStep > least || s.members != everyone;
-        bool raise = false;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = r & 1;
-            x[n][r] *= sm.factor[n * 8 + q4 * 2 + j] * s.k_scale;
-            if (masked) {
-              const int pos = s.pos + g + (r >> 1) * 8;
-              if (pos > t.pos0 + (int)shift[n][j] || (s.members >> shift[n][j] & 1u) == 0u)
-                x[n][r] = -infinity();
-            }
-            raise |= x[n][r] > m[n][j] + kSlack;
-          }
-        if (__any_sync(~0u, raise)) {
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            float by[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float top = fmaxf(fmaxf(x[n][j], x[n][j + 2]), m[n][j]);
-#pragma unroll
-              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-              by[j] = m[n][j] == -infinity() ? 0.f : exp2_fast(m[n][j] - top);
-              m[n][j] = top;
-              l[n][j] *= by[j];
-            }
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) o[i][n][r] *= by[r & 1];
           }
         }
-        if (s.v_scale != unit) {
-          const float by = unit / s.v_scale;
-          unit = s.v_scale;
+        copy_commit();
+      };
+
+      const auto compute = [&](int i) {
+        int e, row0;
+        find(i, &e, &row0);
+        const int pos = position(e, row0);
+        if (sm.page[e] < 0 || pos >= most) return;
+        const uint32_t members = listed ? sm.entry[e] >> 24 : everyone;
+        const float2 scale = sm.scale[e];
+        const uint8_t* const codes = &sm.ring[warp][i % Smem::kRing][0][0];
+        // Eight columns of which no token takes the page are left out. Where some do and
+        // some do not, or the step ends beyond a token, scores are masked.
+        bool takes[NT];
+        bool masked = pos + kStep > least;
 #pragma unroll
-          for (int i = 0; i < kTiles; ++i)
+        for (int n = 0; n < NT; ++n) {
+          takes[n] = NT == 1 || (members & have[n]) != 0u;
+          masked |= takes[n] && (members & have[n]) != have[n];
+        }
+
+        // ---- S^T ----
+        float x[NT][4];
+        {
+          uint32_t a[D / 16][4];
+#pragma unroll
+          for (int p = 0; p < kHalf; ++p) {
+            uint4 w[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int row = g + 8 * r;
+              w[r] = *reinterpret_cast<const uint4*>(
+                  codes + row * D + (D == 128 ? (p * 4 + q4) ^ ((row & 1) << 2) : q4) * 16);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t w0 = word(w[0], k), w1 = word(w[1], k);
+              a[p * 4 + k][0] = codes_to_half2((uint16_t)w0);
+              a[p * 4 + k][2] = codes_to_half2((uint16_t)(w0 >> 16));
+              a[p * 4 + k][1] = codes_to_half2((uint16_t)w1);
+              a[p * 4 + k][3] = codes_to_half2((uint16_t)(w1 >> 16));
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (!takes[n]) continue;
+            float other[4] = {0.f, 0.f, 0.f, 0.f};  // two sums, for shorter chains
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[n][r] = 0.f;
+#pragma unroll
+            for (int p = 0; p < kHalf; ++p)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint4 q;
+                if (kHoldQ)
+                  q = held[n][p][k];
+                else
+                  q = *reinterpret_cast<const uint4*>(
+                      &sm.q[n * 8 + g][p * 64 + q4 * 16 + k * 8]);
+                const uint32_t(&a0)[4] = a[p * 4 + k * 2];
+                const uint32_t(&a1)[4] = a[p * 4 + k * 2 + 1];
+                mma(x[n], a0[0], a0[1], a0[2], a0[3], q.x, q.y);
+                mma(other, a1[0], a1[1], a1[2], a1[3], q.z, q.w);
+              }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[n][r] += other[r];
+          }
+        }
+
+        // ---- probabilities ----
+        if (scale.y != unit) {
+          const float by = unit / scale.y;
+          unit = scale.y;
+#pragma unroll
+          for (int k = 0; k < kTiles; ++k)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) o[i][n][r] *= by;
+              for (int r = 0; r < 4; ++r) o[k][n][r] *= by;
         }
         uint32_t pt[NT][2];
+        uint32_t seen = 0u;  // 4 bits for each 8 columns: this lane's scores that count
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float p[4];
+          if (!takes[n]) continue;
+          const float2 factor = *reinterpret_cast<const float2*>(&sm.factor[n * 8 + q4 * 2]);
+          float y[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int j = r & 1;
-            // a column that has seen nothing yet has every x at -inf
-            p[r] = exp2_fast(x[n][r] - (m[n][j] == -infinity() ? 0.f : m[n][j]));
-            l[n][j] += p[r];
+            x[n][r] *= (r & 1 ? factor.y : factor.x) * scale.x;
+            y[r] = x[n][r] - m[n][r & 1];
           }
-          pt[n][0] = transpose8(pack2<true>(p[0], p[1]));
-          pt[n][1] = transpose8(pack2<true>(p[2], p[3]));
+          if (masked) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t token = shift[n][r & 1];
+              if (pos + g + (r >> 1) * 8 > t.pos0 + (int)token || (members >> token & 1u) == 0u)
+                x[n][r] = y[r] = -infinity();
+              else
+                seen |= 1u << (n * 4 + r);
+            }
+          }
+          const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+          if (__any_sync(~0u, top > kSlack)) {
+            float by[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float high = fmaxf(fmaxf(x[n][j], x[n][j + 2]), m[n][j]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1)
+                high = fmaxf(high, __shfl_xor_sync(~0u, high, d));
+              by[j] = m[n][j] == -infinity() ? 0.f : exp2_fast(m[n][j] - high);
+              m[n][j] = high;
+              l[n][j] *= by[j];
+            }
+#pragma unroll
+            for (int k = 0; k < kTiles; ++k)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) o[k][n][r] *= by[r & 1];
+            // a masked score stays -inf, also where its column has seen nothing yet
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              y[r] = x[n][r] == -infinity() ? x[n][r] : x[n][r] - m[n][r & 1];
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            y[r] = exp2_fast(y[r]);
+            l[n][r & 1] += y[r];
+          }
+          pt[n][0] = transpose8(pack2<true>(y[0], y[1]));
+          pt[n][1] = transpose8(pack2<true>(y[2], y[3]));
+        }
+
+        // ---- values: tokens 2c, 2c+1, 2c+8, 2c+9 of 16 (8) channels ----
+        uint4 v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int row = q4 * 2 + (r & 1) + (r >> 1) * 8;
+          const uint8_t* const at = codes + kStep * D;
+          if (D == 128) {
+            v[r] = *reinterpret_cast<const uint4*>(at + row * 128 +
+                                                   (g ^ ((row >> 1 & 3) << 1)) * 16);
+          } else {
+            const int line = row >> 1, p = (row & 1) * 4 + (g >> 1);
+            const uint2 half = *reinterpret_cast<const uint2*>(
+                at + line * 128 + (p ^ ((line & 3) << 1)) * 16 + (g & 1) * 8);
+            v[r] = make_uint4(half.x, half.y, 0u, 0u);
+          }
         }
         // A value that is NaN makes NaN of the columns that see its token, and of no
         // other: where not every column sees every token, such values are taken out
         // of the product, and a product of ones marks the outputs that they reach.
-        uint4 v[4] = {s.v[0], s.v[1], s.v[2], s.v[3]};
         if (masked) {
           uint32_t bad = 0u;
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) bad |= nan_codes(word(s.v[r], i));
+            for (int k = 0; k < D / 32; ++k) bad |= nan_codes(word(v[r], k));
           if (__any_sync(~0u, bad != 0u)) {
-            uint32_t sees[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              sees[n][0] = transpose8(pack2<true>(x[n][0] != -infinity() ? 1.f : 0.f,
-                                                  x[n][1] != -infinity() ? 1.f : 0.f));
-              sees[n][1] = transpose8(pack2<true>(x[n][2] != -infinity() ? 1.f : 0.f,
-                                                  x[n][3] != -infinity() ? 1.f : 0.f));
-            }
+              if (!takes[n]) continue;
+              const uint32_t bits = seen >> (n * 4);
+              const uint32_t s0 = transpose8((bits & 1u ? 0x3C00u : 0u) |
+                                             (bits & 2u ? 0x3C000000u : 0u));
+              const uint32_t s1 = transpose8((bits & 4u ? 0x3C00u : 0u) |
+                                             (bits & 8u ? 0x3C000000u : 0u));
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-              uint32_t one[4];
+              for (int k = 0; k < kTiles; ++k) {
+                uint32_t one[4];
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {  // r: channel 2i + (r & 1), token pair r >> 1
-                const int byte = (i & 1) * 2 + (r & 1);
-                const uint32_t w0 = word(s.v[(r >> 1) * 2], i >> 1) >> (8 * byte);
-                const uint32_t w1 = word(s.v[(r >> 1) * 2 + 1], i >> 1) >> (8 * byte);
-                one[r] = ((w0 & 0x7Fu) == 0x7Fu ? 0x3C00u : 0u) |
-                         ((w1 & 0x7Fu) == 0x7Fu ? 0x3C000000u : 0u);
-              }
-#pragma unroll
-              for (int n = 0; n < NT; ++n) {
+                for (int r = 0; r < 4; ++r) {  // channel 2k + (r & 1), token pair r >> 1
+                  const int byte = (k & 1) * 2 + (r & 1);
+                  const uint32_t w0 = word(v[(r >> 1) * 2], k >> 1) >> (8 * byte);
+                  const uint32_t w1 = word(v[(r >> 1) * 2 + 1], k >> 1) >> (8 * byte);
+                  one[r] = ((w0 & 0x7Fu) == 0x7Fu ? 0x3C00u : 0u) |
+                           ((w1 & 0x7Fu) == 0x7Fu ? 0x3C000000u : 0u);
+                }
                 float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                mma(hit, one[0], one[1], one[2], one[3], sees[n][0], sees[n][1]);
+                mma(hit, one[0], one[1], one[2], one[3], s0, s1);
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                  if (hit[r] > 0.f) o[i][n][r] = __uint_as_float(0x7FFFFFFFu);
+                  if (hit[r] > 0.f) o[k][n][r] = __uint_as_float(0x7FFFFFFFu);
               }
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              uint32_t w[4] = {s.v[r].x, s.v[r].y, s.v[r].z, s.v[r].w};
+              uint32_t w[4] = {v[r].x, v[r].y, v[r].z, v[r].w};
 #pragma unroll
-              for (int i = 0; i < D / 32; ++i) {
-                const uint32_t nan = nan_codes(w[i]) >> 7;  // 1 in each byte that is NaN
-                w[i] &= ~(nan * 255u);
+              for (int k = 0; k < D / 32; ++k) {
+                const uint32_t nan = nan_codes(w[k]) >> 7;  // 1 in each byte that is NaN
+                w[k] &= ~(nan * 255u);
               }
               v[r] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
         }
-        // O^T
+
+        // ---- O^T, half of the channels at a time ----
+        constexpr int kPart = kTiles / 2;
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) {
-          const uint32_t w0 = __byte_perm(word(v[0], i >> 1), word(v[1], i >> 1),
-                                          i & 1 ? 0x7362 : 0x5140);
-          const uint32_t w1 = __byte_perm(word(v[2], i >> 1), word(v[3], i >> 1),
-                                          i & 1 ? 0x7362 : 0x5140);
-          const uint32_t a0 = codes_to_half2((uint16_t)w0);
-          const uint32_t a1 = codes_to_half2((uint16_t)(w0 >> 16));
-          const uint32_t a2 = codes_to_half2((uint16_t)w1);
-          const uint32_t a3 = codes_to_half2((uint16_t)(w1 >> 16));
+        for (int half = 0; half < 2; ++half) {
+          uint32_t a[kPart][4];
+#pragma unroll
+          for (int k = 0; k < kPart; ++k) {
+            const int tile = half * kPart + k;
+            const uint32_t w0 = __byte_perm(word(v[0], tile >> 1), word(v[1], tile >> 1),
+                                            tile & 1 ? 0x7362 : 0x5140);
+            const uint32_t w1 = __byte_perm(word(v[2], tile >> 1), word(v[3], tile >> 1),
+                                            tile & 1 ? 0x7362 : 0x5140);
+            a[k][0] = codes_to_half2((uint16_t)w0);
+            a[k][1] = codes_to_half2((uint16_t)(w0 >> 16));
+            a[k][2] = codes_to_half2((uint16_t)w1);
+            a[k][3] = codes_to_half2((uint16_t)(w1 >> 16));
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            if (NT > 1 && (s.members & have[n]) == 0u) continue;
-            mma(o[i][n], a0, a1, a2, a3, pt[n][0], pt[n][1]);
+            if (!takes[n]) continue;
+#pragma unroll
+            for (int k = 0; k < kPart; ++k)
+              mma(o[half * kPart + k][n], a[k][0], a[k][1], a[k][2], a[k][3], pt[n][0],
+                  pt[n][1]);
           }
         }
       };
 
-      Step<D> s0, s1;
-      fetch(0, s0);
-      for (int i = 0; i < steps; i += 2) {
-        fetch(i + 1, s1);
-        compute(s0);
-        fetch(i + 2, s0);
-        compute(s1);
+#pragma unroll
+      for (int i = 0; i < Smem::kRing - 1; ++i) fetch(i);
+      for (int i = 0; i < steps; ++i) {
+        copy_wait<Smem::kRing - 2>();
+        __syncwarp();
+        compute(i);
+        __syncwarp();
+        fetch(i + Smem::kRing - 1);
       }
+      copy_wait<0>();
     }
+    __syncthreads();  // the ring's memory is used for the outputs now
 
     // ---- join the warps ----
     // Each lane's sums cover its own tokens: add over the lanes of a column. Then
