@@ -117,11 +117,12 @@ def _rows(t, name, cache, heads, tokens=None):
         raise TypeError(f"{name} must be {cache.dtype}, got {t.dtype}")
     if t.device != cache.device:
         raise ValueError(f"{name} must be on {cache.device}, got {t.device}")
-    shape = t.shape
-    if len(shape) != 3 or shape[1] != heads or shape[2] != cache.head_dim or \
-            (tokens is not None and shape[0] != tokens):
-        raise ValueError(f"{name} must be [{'num_tokens' if tokens is None else tokens}, {heads}, "
-                         f"{cache.head_dim}], got {list(shape)}")
+    shape, dim = t.shape, cache.head_dim
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or (tokens is not None and shape[0] != tokens):
+        raise ValueError(f"{name} must be [{'num_tokens' if tokens is None else tokens}, {heads}, {dim}], "
+                         f"got {list(shape)}")
+    if t.is_contiguous():
+        return _Rows(t.data_ptr(), heads * dim, dim)
     token, head, channel = t.stride()
     if channel != 1:
         raise ValueError(f"{name} must have contiguous channels")
@@ -130,28 +131,29 @@ def _rows(t, name, cache, heads, tokens=None):
 
 
 def _span(t):
-    """Bytes from the first to behind the last element of rows."""
-    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()) if n > 1 and s > 0)
-    first = sum((n - 1) * s for n, s in zip(t.shape, t.stride()) if n > 1 and s < 0)
-    at, size = t.data_ptr(), t.element_size()
-    return at + first * size, at + (last + 1) * size
+    """Addresses of the first element of rows and behind the last one."""
+    at = t.data_ptr()
+    if t.is_contiguous():
+        return at, at + t.nbytes
+    ends = [(n - 1) * s * t.element_size() for n, s in zip(t.shape, t.stride())]
+    return at + sum(e for e in ends if e < 0), at + sum(e for e in ends if e > 0) + t.element_size()
 
 
-def _written(t, name, *read):
-    """An output's rows must share no memory with one another, nor with rows that are read."""
+def _written(t, name, other):
+    """An output's rows must share no memory with one another, nor with the rows `other`."""
     if t.numel() == 0:
         return
-    need = t.shape[2]  # elements that the dimensions so far span
-    for n, s in sorted(zip(t.shape[:2], map(abs, t.stride()[:2])), key=lambda x: x[1]):
-        if n > 1:
-            if s < need:
-                raise ValueError(f"the rows of {name} must not overlap")
-            need += (n - 1) * s
+    if not t.is_contiguous():
+        need = t.shape[2]  # elements that the dimensions so far span
+        for n, s in sorted(zip(t.shape[:2], map(abs, t.stride()[:2])), key=lambda x: x[1]):
+            if n > 1:
+                if s < need:
+                    raise ValueError(f"the rows of {name} must not overlap")
+                need += (n - 1) * s
     a, b = _span(t)
-    for r in read:
-        c, d = _span(r)
-        if a < d and c < b:
-            raise ValueError(f"{name} must not share memory with another row argument")
+    c, d = _span(other)
+    if a < d and c < b:
+        raise ValueError(f"{name} must not share memory with another row argument")
 
 
 class KVCache:
@@ -271,7 +273,7 @@ def cache_read(cache, batch, num_tokens=None, out=None, stream=None):
     k, v = out
     kr = _rows(k, "out[0]", cache, cache.kv_heads, num_tokens)
     vr = _rows(v, "out[1]", cache, cache.kv_heads, k.shape[0])
-    _written(k, "out[0]")
+    _written(k, "out[0]", v)
     _written(v, "out[1]", k)
     batch._check(cache, k.shape[0])
     _call(cache.device, stream, _lib().exact_topk_cache_read, cache._ref, batch._ref, k.shape[0], kr, vr)

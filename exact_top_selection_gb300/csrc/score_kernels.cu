@@ -12,6 +12,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int64_t kPromptColumns = 64;
 constexpr int kPages = 16;  // pages of a warp's step: the rows of one matrix instruction
 
 template <bool kFp16>
@@ -29,6 +30,13 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The larger one; NaN where either is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
 }
 
 // Both halves' positive or negative part; NaN stays NaN.
@@ -128,10 +136,7 @@ __global__ void __launch_bounds__(kThreads) score_step_kernel(CacheArgs c, Batch
       const int here = group - head0 < heads ? group - head0 : heads;
       if (group > 8) {  // one token a tile: its maximum goes from pass to pass
         if (lane < kPages)
-          for (int i = 0; i < here; ++i) {
-            const float v = s_out[warp][lane][i];
-            best = best != best || v <= best ? best : v;
-          }
+          for (int i = 0; i < here; ++i) best = max_nan(best, s_out[warp][lane][i]);
         if (head0 + heads < group) continue;
       }
       for (int i = lane; i < tokens * kPages; i += 32) {
@@ -142,10 +147,8 @@ __global__ void __launch_bounds__(kThreads) score_step_kernel(CacheArgs c, Batch
         float v = best;
         if (group <= 8) {
           v = s_out[warp][i % kPages][t * heads];
-          for (int k = 1; k < heads; ++k) {
-            const float u = s_out[warp][i % kPages][t * heads + k];
-            v = v != v || u <= v ? v : u;
-          }
+          for (int k = 1; k < heads; ++k)
+            v = max_nan(v, s_out[warp][i % kPages][t * heads + k]);
         }
         if (j < a.keep_first || j > newest - a.keep_last) v = __uint_as_float(0x7F800000u);
         if (page_of(c, b, seq, j) < 0) v = -__uint_as_float(0x7F800000u);
@@ -155,10 +158,360 @@ __global__ void __launch_bounds__(kThreads) score_step_kernel(CacheArgs c, Batch
   }
 }
 
+// ---- prompts ----
+//
+// Many columns against many pages: bound by the matrix products, so they run on the
+// fifth-generation tensor cores. A CTA keeps 256 columns (tokens x heads of one key
+// head, [relu(q) | min(q, 0)]) in shared memory and streams pages past them, 128 at a
+// time: D[128 pages][256 columns] in tensor memory, two of them, so that one is
+// read out while the next is computed. Pages are the accumulator's lanes: the largest over a
+// token's heads is a maximum over neighbouring columns of one lane, and a warp's 32 lanes
+// write 32 neighbouring scores.
+//
+// Page rows lie anywhere in memory, 2 D channels each: four warps gather them in pieces of 64
+// channels (one 128-byte line of the operand's layout) through a ring, one thread of a ninth warp
+// issues the products, and four more warps read the results out. Every wait is bounded; a CTA
+// whose wait ran out writes NaN for what it has not computed.
+constexpr int kGather = 128;             // threads that gather, and as many that read out
+constexpr int kPromptThreads = 2 * kGather + 32;
+constexpr int kColumns = 256;
+constexpr int kLanes = 128;              // pages of a tile
+constexpr int kLine = 64;                // channels of a line
+constexpr int kLineBytes = kLanes * kLine * 2;
+constexpr uint32_t kWaitLimit = 1u << 20;  // polls of a barrier, far beyond any real wait
+
+template <int D>
+struct PromptShared {
+  static constexpr int kChunks = 2 * D / kLine;
+  static constexpr int kStages = D == 128 ? 5 : 6;
+  uint8_t columns[kChunks][kColumns * kLine * 2];
+  uint8_t pages[kStages][kLineBytes];
+  uint64_t full[kStages], empty[kStages], done[2], free[2], drained;
+  uint32_t tensor;
+  int failed;
+};
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+__device__ __forceinline__ void barrier_init(uint64_t* b, int count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(shared_address(b)), "r"(count)
+               : "memory");
+}
+
+__device__ __forceinline__ void barrier_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_address(b)) : "memory");
+}
+
+// False when the barrier's phase did not complete in time, or another wait has given up.
+__device__ __forceinline__ bool barrier_wait(uint64_t* b, uint32_t parity, volatile int* failed) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done)
+        : "r"(shared_address(b)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if ((i & 255u) == 255u && *failed) return false;
+  }
+  *failed = 1;
+  return false;
+}
+
+// Operand in lines of 128 bytes, 8 of them to a swizzled block of 1024 bytes.
+__device__ __forceinline__ uint64_t operand(uint32_t address) {
+  return (uint64_t)((address & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ void tensor_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t kind,
+                                           bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+      : "memory");
+}
+
+// The barrier's phase completes when the products issued so far have.
+__device__ __forceinline__ void tensor_commit(uint64_t* b) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          shared_address(b))
+      : "memory");
+}
+
+__device__ __forceinline__ void tensor_load32(uint32_t address, float (&v)[32]) {
+  uint32_t* const r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(address));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// kPadded: the group's heads rounded up to a power of two, at most 32; a column beyond
+// the group repeats its last head, which leaves the maximum as it is.
+template <bool kFp16, int D, int kPadded>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    score_prompt_kernel(CacheArgs c, BatchArgs b, ScoreArgs a, int tiles_per_cta) {
+  using Smem = PromptShared<D>;
+  constexpr int kChunks = Smem::kChunks, kStages = Smem::kStages;
+  constexpr int kTileTokens = kColumns / kPadded;
+  extern __shared__ unsigned char raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(
+      raw + ((1024u - (shared_address(raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.z;
+  const int64_t slot = blockIdx.x;
+  if (a.num_valid_rows != nullptr && slot == 0 && blockIdx.y == 0 && h == 0 && tid == 0)
+    *a.num_valid_rows =
+        (int32_t)((b.q_start == nullptr ? b.num_seqs : clamp_row(b, b.num_seqs)) * c.heads);
+  const int seq = sequence_of_slot(b, slot, kTileTokens, 1);
+  const SeqRows rows = sequence_rows(b, c.page_shift, seq);
+  const int64_t index = slot - first_slot(b, seq, kTileTokens, 1);
+  const int64_t token0 = index * kTileTokens;
+  if (index < 0 || token0 >= rows.count) return;
+  const int tokens = rows.count - token0 < kTileTokens ? (int)(rows.count - token0) : kTileTokens;
+  const int64_t row0 = rows.begin + token0;
+  const int pos0 = rows.pos0 + (int)token0;
+  if (blockIdx.y == 0 && tid < tokens) {
+    const int pos = pos0 + tid;
+    a.ke[(row0 + tid) * c.heads + h] = pos < 0 ? 0 : (pos >> c.page_shift) + 1;
+  }
+  const int last = pos0 + tokens - 1;
+  const int seen = last < 0 ? 0 : (last >> c.page_shift) + 1;
+  const int first_page = (int)blockIdx.y * tiles_per_cta * kLanes;
+  if (first_page >= seen) return;
+  const int all = (seen - first_page + kLanes - 1) / kLanes;
+  const int tiles = all < tiles_per_cta ? all : tiles_per_cta;
+
+  if (tid == 0) {
+    sm.failed = 0;
+    for (int i = 0; i < kStages; ++i) {
+      barrier_init(&sm.full[i], kGather);
+      barrier_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      barrier_init(&sm.done[i], 1);
+      barrier_init(&sm.free[i], kGather);
+    }
+    barrier_init(&sm.drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     shared_address(&sm.tensor))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // columns: 8 channels at a time, the positive and the negative part to their lines
+  for (int i = tid; i < kColumns * (D / 8); i += kPromptThreads) {
+    const int col = i / (D / 8), piece = i % (D / 8);
+    const int token = col / kPadded;
+    const int head = col % kPadded < a.group ? col % kPadded : a.group - 1;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (token < tokens)
+      w = __ldg(reinterpret_cast<const uint4*>(
+          static_cast<const uint16_t*>(a.q.data) + (row0 + token) * a.q.token_stride +
+          ((int64_t)h * a.group + head) * a.q.head_stride + piece * 8));
+    const int at = col * (kLine * 2) + (((piece & 7) ^ (col & 7)) << 4);
+    *reinterpret_cast<uint4*>(&sm.columns[piece / 8][at]) =
+        make_uint4(clamp_sign<kFp16>(w.x, true), clamp_sign<kFp16>(w.y, true),
+                   clamp_sign<kFp16>(w.z, true), clamp_sign<kFp16>(w.w, true));
+    *reinterpret_cast<uint4*>(&sm.columns[kChunks / 2 + piece / 8][at]) =
+        make_uint4(clamp_sign<kFp16>(w.x, false), clamp_sign<kFp16>(w.y, false),
+                   clamp_sign<kFp16>(w.z, false), clamp_sign<kFp16>(w.w, false));
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tensor = sm.tensor;
+  volatile int* const failed = &sm.failed;
+
+  if (warp >= 4 && warp < 8) {
+    // ---- gather: thread i takes piece i % 8 of the lines of pages i / 8 + 16 k ----
+    constexpr int kRows = kLanes / (kGather / 8);
+    const int piece = tid & 7, line0 = (tid - kGather) >> 3;
+    const uint16_t* const bounds = static_cast<const uint16_t*>(c.bounds);
+    int step = 0;
+    bool ok = true;
+    const auto publish = [&](int s) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      barrier_arrive(&sm.full[s % kStages]);
+    };
+    for (int tile = 0; tile < tiles && ok; ++tile) {
+      int id[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int j = first_page + tile * kLanes + line0 + k * (kGather / 8);
+        id[k] = j < seen ? page_of(c, b, seq, j) : -1;
+      }
+      for (int chunk = 0; chunk < kChunks; ++chunk, ++step) {
+        const int s = step % kStages;
+        if (step >= kStages && !barrier_wait(&sm.empty[s], (step / kStages - 1) & 1, failed)) {
+          ok = false;
+          break;
+        }
+        const uint32_t to = shared_address(sm.pages[s]);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const int line = line0 + k * (kGather / 8);
+          const int64_t page = id[k] < 0 ? 0 : id[k];
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           to + line * (kLine * 2) + ((piece ^ (line & 7)) << 4)),
+                       "l"(bounds + (page * c.heads + h) * (2 * D) + chunk * kLine + piece * 8),
+                       "r"(id[k] < 0 ? 0 : 16)
+                       : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (step >= 2) {  // two more on their way
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+          publish(step - 2);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    if (ok)
+      for (int s = step < 2 ? 0 : step - 2; s < step; ++s) publish(s);
+  } else if (warp == 8) {
+    // ---- products, by one thread ----
+    if (lane == 0) {
+      constexpr uint32_t kType = kFp16 ? 0u : 1u;
+      constexpr uint32_t kind = 1u << 4 | kType << 7 | kType << 10 | (kColumns / 8) << 17 |
+                                (kLanes / 16) << 24;
+      int step = 0;
+      bool ok = true;
+      for (int tile = 0; tile < tiles && ok; ++tile) {
+        const int buffer = tile & 1;
+        if (tile >= 2) ok = barrier_wait(&sm.free[buffer], (tile / 2 - 1) & 1, failed);
+        for (int chunk = 0; chunk < kChunks && ok; ++chunk, ++step) {
+          const int s = step % kStages;
+          if (!barrier_wait(&sm.full[s], (step / kStages) & 1, failed)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t pages = operand(shared_address(sm.pages[s]));
+          const uint64_t columns = operand(shared_address(sm.columns[chunk]));
+#pragma unroll
+          for (int k = 0; k < kLine / 16; ++k)  // 32 bytes of a line each
+            tensor_mma(tensor + buffer * kColumns, pages + 2 * k, columns + 2 * k, kind,
+                       chunk > 0 || k > 0);
+          tensor_commit(&sm.empty[s]);
+        }
+        if (ok) tensor_commit(&sm.done[buffer]);
+      }
+      // what was issued ends before the shared memory and the tensor memory go
+      if (!ok) {
+        int none = 0;
+        tensor_commit(&sm.drained);
+        barrier_wait(&sm.drained, 0, &none);
+      }
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---- read out ----
+    constexpr int kEach = 32 / kPadded;  // tokens of 32 columns
+    bool ok = true;
+    for (int tile = 0; tile < tiles; ++tile) {
+      const int buffer = tile & 1;
+      const int j = first_page + tile * kLanes + warp * 32 + lane;
+      const bool there = j < seen && page_of(c, b, seq, j) >= 0;
+      if (ok) ok = barrier_wait(&sm.done[buffer], (tile / 2) & 1, failed);
+      ok = __all_sync(~0u, ok);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      for (int part = 0; part < kColumns / 32 && part * kEach < tokens; ++part) {
+        float v[32];
+        if (ok) {
+          tensor_load32(tensor + ((uint32_t)(warp * 32) << 16) + buffer * kColumns + part * 32, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(0x7FFFFFFFu);
+        }
+#pragma unroll
+        for (int t = 0; t < kEach; ++t) {
+          float best = v[t * kPadded];
+#pragma unroll
+          for (int k = 1; k < kPadded; ++k) best = max_nan(best, v[t * kPadded + k]);
+          const int token = part * kEach + t;
+          const int pos = pos0 + token;
+          const int newest = pos >> c.page_shift;
+          if (token >= tokens || pos < 0 || j > newest) continue;
+          if (j < a.keep_first || j > newest - a.keep_last) best = __uint_as_float(0x7F800000u);
+          if (!there) best = -__uint_as_float(0x7F800000u);
+          a.scores[((row0 + token) * c.heads + h) * a.row_pitch + j] = best;
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      barrier_arrive(&sm.free[buffer]);
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tensor)
+                 : "memory");
+}
+
+template <bool kFp16, int D, int kPadded>
+int launch_prompt(const CacheArgs& c, const BatchArgs& b, const ScoreArgs& a,
+                  cudaStream_t stream) {
+  constexpr size_t smem = sizeof(PromptShared<D>) + 1024;
+  const auto kernel = score_prompt_kernel<kFp16, D, kPadded>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return EXACT_TOPK_ERR_CUDA;
+  }
+  const int64_t slots = slot_count(b, kColumns / kPadded, 1);
+  const int64_t tiles = ((int64_t)b.width + kLanes - 1) / kLanes;
+  // A CTA's columns cost as much as about two tiles to bring in; seven waves of CTAs leave
+  // little of the last one idle.
+  int64_t each = slots * c.heads * tiles / (152 * 7);
+  each = each < 1 ? 1 : (each > 16 ? 16 : each);
+  const dim3 grid((unsigned)slots, (unsigned)((tiles + each - 1) / each), (unsigned)c.heads);
+  kernel<<<grid, kPromptThreads, smem, stream>>>(c, b, a, (int)each);
+  return launch_status();
+}
+
+template <bool kFp16, int D>
+int launch_prompt_group(const CacheArgs& c, const BatchArgs& b, const ScoreArgs& a,
+                        cudaStream_t stream) {
+  if (a.group == 1) return launch_prompt<kFp16, D, 1>(c, b, a, stream);
+  if (a.group == 2) return launch_prompt<kFp16, D, 2>(c, b, a, stream);
+  if (a.group <= 4) return launch_prompt<kFp16, D, 4>(c, b, a, stream);
+  if (a.group <= 8) return launch_prompt<kFp16, D, 8>(c, b, a, stream);
+  if (a.group <= 16) return launch_prompt<kFp16, D, 16>(c, b, a, stream);
+  return launch_prompt<kFp16, D, 32>(c, b, a, stream);
+}
+
 }  // namespace
 
 int launch_block_scores(const CacheArgs& c, const BatchArgs& b, const ScoreArgs& a,
                         cudaStream_t stream) {
+  // Rows of a sequence (their mean number) times its group's heads: from 64 columns on the
+  // tensor cores' tiles are filled well enough.
+  const int64_t mean = (b.num_tokens + b.num_seqs - 1) / b.num_seqs;
+  if (a.group <= 32 && mean * a.group >= kPromptColumns) {
+    if (c.dim == 128)
+      return c.fp16 ? launch_prompt_group<true, 128>(c, b, a, stream)
+                    : launch_prompt_group<false, 128>(c, b, a, stream);
+    return c.fp16 ? launch_prompt_group<true, 64>(c, b, a, stream)
+                  : launch_prompt_group<false, 64>(c, b, a, stream);
+  }
   const int tile_tokens = a.group >= 8 ? 1 : 8 / a.group;
   const int64_t slots = slot_count(b, tile_tokens, 1);
   const int steps = (b.width + kWarps * kPages - 1) / (kWarps * kPages);

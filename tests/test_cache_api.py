@@ -178,12 +178,12 @@ def test_binding_refuses_tensors_on_the_cpu_and_of_wrong_types():
 
 
 def test_outputs_that_overlap_are_refused():
-    x = torch.zeros(4 * 64 * 4, dtype=torch.bfloat16)
-    binding._written(x.view(4, 4, 64), "out")
-    binding._written(x.as_strided((4, 4, 64), (64, 256, 1)), "out")
+    x, apart = torch.zeros(4 * 64 * 4, dtype=torch.bfloat16), torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    binding._written(x.view(4, 4, 64), "out", apart)
+    binding._written(x.as_strided((4, 4, 64), (64, 256, 1)), "out", apart)
     for size, stride in (((4, 4, 64), (0, 64, 1)), ((4, 4, 64), (64, 64, 1)), ((4, 2, 64), (96, 64, 1)), ((4, 2, 64), (64, 32, 1))):
         with pytest.raises(ValueError):
-            binding._written(x.as_strided(size, stride), "out")
+            binding._written(x.as_strided(size, stride), "out", apart)
     with pytest.raises(ValueError):
         binding._written(x.view(4, 4, 64), "out", x.view(4, 4, 64)[1:])
     y = x.view(2, 2, 4, 64)
