@@ -39,6 +39,12 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   return r;
 }
 
+__device__ __forceinline__ float max_nan(float x, float y, float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 // Both halves' positive or negative part; NaN stays NaN.
 template <bool kFp16>
 __device__ __forceinline__ uint32_t clamp_sign(uint32_t w, bool positive) {
@@ -168,28 +174,75 @@ __global__ void __launch_bounds__(kThreads) score_step_kernel(CacheArgs c, Batch
 // token's heads is a maximum over neighbouring columns of one lane, and a warp's 32 lanes
 // write 32 neighbouring scores.
 //
-// Page rows lie anywhere in memory, 2 D channels each: four warps gather them in pieces of 64
-// channels (one 128-byte line of the operand's layout) through a ring, one thread of a ninth warp
-// issues the products, and four more warps read the results out. Every wait is bounded; a CTA
-// whose wait ran out writes NaN for what it has not computed.
-constexpr int kGather = 128;             // threads that gather, and as many that read out
-constexpr int kPromptThreads = 2 * kGather + 32;
+// One CTA an SM takes items (256 columns x a run of pages) in turn. Its warps keep to one
+// role each: four gather page rows, which lie anywhere in memory, in lines of 64
+// channels through a ring; eight bring the next item's columns, line by line as the products
+// let go of the old ones; one thread issues the products; four warps read the results
+// out. Every wait is bounded; a CTA whose wait ran out writes NaN for what it has not computed.
+constexpr int kReadOut = 128;            // threads of each role
+constexpr int kGather = 128;
+constexpr int kFill = 256;
+constexpr int kPromptThreads = kReadOut + kGather + kFill + 32;
+constexpr int kIssueWarp = (kPromptThreads - 32) / 32;
+constexpr int kSms = 152;                // one CTA on each
 constexpr int kColumns = 256;
 constexpr int kLanes = 128;              // pages of a tile
 constexpr int kLine = 64;                // channels of a line
 constexpr int kLineBytes = kLanes * kLine * 2;
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls of a barrier, far beyond any real wait
 
+// Lines are in the order hi, lo of channels 0-63, then hi, lo of channels 64-127.
 template <int D>
 struct PromptShared {
   static constexpr int kChunks = 2 * D / kLine;
   static constexpr int kStages = D == 128 ? 5 : 6;
   uint8_t columns[kChunks][kColumns * kLine * 2];
   uint8_t pages[kStages][kLineBytes];
-  uint64_t full[kStages], empty[kStages], done[2], free[2], drained;
+  uint64_t full[kStages], empty[kStages];       // page lines
+  uint64_t filled[kChunks], released[kChunks];  // column lines
+  uint64_t done[2], free[2];                    // accumulators
+  uint64_t drained;
   uint32_t tensor;
   int failed;
 };
+
+// An item: a column tile of a sequence and key head, and a run of page tiles.
+struct PromptItem {
+  int64_t row0;
+  int seq, head, pos0, tokens, seen, first_page, tiles;
+};
+
+struct PromptWork {
+  int64_t slots, items;
+  int groups, each;  // runs of page tiles, and the tiles of one
+};
+
+// False where there is nothing to score: no rows, or no pages left for the run.
+__device__ __forceinline__ bool prompt_item(const CacheArgs& c, const BatchArgs& b,
+                                            const PromptWork& w, int tile_tokens, int64_t i,
+                                            PromptItem* item) {
+  const int group = (int)(i % w.groups);
+  const int64_t rest = i / w.groups;
+  item->head = (int)(rest % c.heads);
+  const int64_t slot = rest / c.heads;
+  item->seq = sequence_of_slot(b, slot, tile_tokens, 1);
+  const SeqRows rows = sequence_rows(b, c.page_shift, item->seq);
+  const int64_t index = slot - first_slot(b, item->seq, tile_tokens, 1);
+  const int64_t token0 = index * tile_tokens;
+  item->tokens = 0;
+  item->tiles = 0;
+  if (index < 0 || token0 >= rows.count) return false;
+  item->tokens = rows.count - token0 < tile_tokens ? (int)(rows.count - token0) : tile_tokens;
+  item->row0 = rows.begin + token0;
+  item->pos0 = rows.pos0 + (int)token0;
+  const int last = item->pos0 + item->tokens - 1;
+  item->seen = last < 0 ? 0 : (last >> c.page_shift) + 1;
+  item->first_page = group * w.each * kLanes;
+  if (item->first_page >= item->seen) return false;
+  const int all = (item->seen - item->first_page + kLanes - 1) / kLanes;
+  item->tiles = all < w.each ? all : w.each;
+  return true;
+}
 
 __device__ __forceinline__ uint32_t shared_address(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -257,14 +310,26 @@ __device__ __forceinline__ void tensor_load32(uint32_t address, float (&v)[32]) 
         "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(address));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Loads issued so far are complete; v, which one of them filled, may be read from here on.
+__device__ __forceinline__ void tensor_wait(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+               "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+               "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+               "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+               "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
+               "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
 }
 
 // kPadded: the group's heads rounded up to a power of two, at most 32; a column beyond
 // the group repeats its last head, which leaves the maximum as it is.
 template <bool kFp16, int D, int kPadded>
 __global__ void __launch_bounds__(kPromptThreads, 1)
-    score_prompt_kernel(CacheArgs c, BatchArgs b, ScoreArgs a, int tiles_per_cta) {
+    score_prompt_kernel(CacheArgs c, BatchArgs b, ScoreArgs a, PromptWork work) {
   using Smem = PromptShared<D>;
   constexpr int kChunks = Smem::kChunks, kStages = Smem::kStages;
   constexpr int kTileTokens = kColumns / kPadded;
@@ -272,78 +337,112 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   Smem& sm = *reinterpret_cast<Smem*>(
       raw + ((1024u - (shared_address(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.z;
-  const int64_t slot = blockIdx.x;
-  if (a.num_valid_rows != nullptr && slot == 0 && blockIdx.y == 0 && h == 0 && tid == 0)
+  if (a.num_valid_rows != nullptr && blockIdx.x == 0 && tid == 0)
     *a.num_valid_rows =
         (int32_t)((b.q_start == nullptr ? b.num_seqs : clamp_row(b, b.num_seqs)) * c.heads);
-  const int seq = sequence_of_slot(b, slot, kTileTokens, 1);
-  const SeqRows rows = sequence_rows(b, c.page_shift, seq);
-  const int64_t index = slot - first_slot(b, seq, kTileTokens, 1);
-  const int64_t token0 = index * kTileTokens;
-  if (index < 0 || token0 >= rows.count) return;
-  const int tokens = rows.count - token0 < kTileTokens ? (int)(rows.count - token0) : kTileTokens;
-  const int64_t row0 = rows.begin + token0;
-  const int pos0 = rows.pos0 + (int)token0;
-  if (blockIdx.y == 0 && tid < tokens) {
-    const int pos = pos0 + tid;
-    a.ke[(row0 + tid) * c.heads + h] = pos < 0 ? 0 : (pos >> c.page_shift) + 1;
-  }
-  const int last = pos0 + tokens - 1;
-  const int seen = last < 0 ? 0 : (last >> c.page_shift) + 1;
-  const int first_page = (int)blockIdx.y * tiles_per_cta * kLanes;
-  if (first_page >= seen) return;
-  const int all = (seen - first_page + kLanes - 1) / kLanes;
-  const int tiles = all < tiles_per_cta ? all : tiles_per_cta;
-
   if (tid == 0) {
     sm.failed = 0;
     for (int i = 0; i < kStages; ++i) {
       barrier_init(&sm.full[i], kGather);
       barrier_init(&sm.empty[i], 1);
     }
+    for (int i = 0; i < kChunks; ++i) {
+      barrier_init(&sm.filled[i], kFill);
+      barrier_init(&sm.released[i], 1);
+    }
     for (int i = 0; i < 2; ++i) {
       barrier_init(&sm.done[i], 1);
-      barrier_init(&sm.free[i], kGather);
+      barrier_init(&sm.free[i], kReadOut);
     }
     barrier_init(&sm.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8) {
+  if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                      shared_address(&sm.tensor))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // columns: 8 channels at a time, the positive and the negative part to their lines
-  for (int i = tid; i < kColumns * (D / 8); i += kPromptThreads) {
-    const int col = i / (D / 8), piece = i % (D / 8);
-    const int token = col / kPadded;
-    const int head = col % kPadded < a.group ? col % kPadded : a.group - 1;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (token < tokens)
-      w = __ldg(reinterpret_cast<const uint4*>(
-          static_cast<const uint16_t*>(a.q.data) + (row0 + token) * a.q.token_stride +
-          ((int64_t)h * a.group + head) * a.q.head_stride + piece * 8));
-    const int at = col * (kLine * 2) + (((piece & 7) ^ (col & 7)) << 4);
-    *reinterpret_cast<uint4*>(&sm.columns[piece / 8][at]) =
-        make_uint4(clamp_sign<kFp16>(w.x, true), clamp_sign<kFp16>(w.y, true),
-                   clamp_sign<kFp16>(w.z, true), clamp_sign<kFp16>(w.w, true));
-    *reinterpret_cast<uint4*>(&sm.columns[kChunks / 2 + piece / 8][at]) =
-        make_uint4(clamp_sign<kFp16>(w.x, false), clamp_sign<kFp16>(w.y, false),
-                   clamp_sign<kFp16>(w.z, false), clamp_sign<kFp16>(w.w, false));
-  }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tensor = sm.tensor;
   volatile int* const failed = &sm.failed;
+  PromptItem item;
 
-  if (warp >= 4 && warp < 8) {
+  if (tid < kReadOut) {
+    // ---- read out ----
+    constexpr int kEach = 32 / kPadded;  // tokens of 32 columns
+    const int64_t row_step = (int64_t)c.heads * a.row_pitch;
+    bool ok = true;
+    int count = 0;  // tiles so far
+    for (int64_t i = blockIdx.x; i < work.items; i += gridDim.x) {
+      if (!prompt_item(c, b, work, kTileTokens, i, &item)) continue;
+      const int first_newest = item.pos0 >> c.page_shift;  // the first token's newest page
+      const int parts = (item.tokens + kEach - 1) / kEach;
+      int j0 = item.first_page + warp * 32;
+      bool there = j0 + lane < item.seen && page_of(c, b, item.seq, j0 + lane) >= 0;
+      for (int tile = 0; tile < item.tiles; ++tile, ++count, j0 += kLanes) {
+        const int buffer = count & 1, j = j0 + lane;
+        // all of the warp's pages are seen by every token, and scored
+        const bool plain = item.pos0 >= 0 && j0 >= a.keep_first &&
+                           j0 + 31 <= first_newest - a.keep_last && __all_sync(~0u, there);
+        float* at = a.scores + (item.row0 * c.heads + item.head) * a.row_pitch + j;
+        if (ok) ok = barrier_wait(&sm.done[buffer], (count >> 1) & 1, failed);
+        ok = __all_sync(~0u, ok);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t from = tensor + ((uint32_t)(warp * 32) << 16) + buffer * kColumns;
+        const auto largest = [&](const float (&v)[32], int t) {
+          float best = v[t * kPadded];
+          if (kPadded == 2) best = max_nan(best, v[t * kPadded + 1]);
+#pragma unroll
+          for (int k = 1; k + 1 < kPadded; k += 2)
+            best = max_nan(best, v[t * kPadded + k], v[t * kPadded + k + 1]);
+          if (kPadded > 2) best = max_nan(best, v[t * kPadded + kPadded - 1]);
+          return best;
+        };
+        const auto write = [&](int part, const float (&v)[32]) {
+          const int left = item.tokens - part * kEach;
+          if (plain && ok && left >= kEach) {
+#pragma unroll
+            for (int t = 0; t < kEach; ++t, at += row_step) *at = largest(v, t);
+            return;
+          }
+#pragma unroll
+          for (int t = 0; t < kEach; ++t, at += row_step) {
+            float best = ok ? largest(v, t) : __uint_as_float(0x7FFFFFFFu);
+            const int pos = item.pos0 + part * kEach + t;
+            const int newest = pos >> c.page_shift;
+            if (j < a.keep_first || j > newest - a.keep_last)
+              best = __uint_as_float(0x7F800000u);
+            if (!there) best = -__uint_as_float(0x7F800000u);
+            if (t < left && pos >= 0 && j <= newest) *at = best;
+          }
+        };
+        float v[2][32];
+        tensor_load32(from, v[0]);
+        bool next = false;  // the next tile's page, asked for before it is needed
+        if (tile + 1 < item.tiles && j + kLanes < item.seen)
+          next = page_of(c, b, item.seq, j + kLanes) >= 0;
+        for (int part = 0; part < parts; part += 2) {
+          tensor_wait(v[0]);
+          if (part + 1 < parts) tensor_load32(from + (part + 1) * 32, v[1]);
+          write(part, v[0]);
+          if (part + 1 >= parts) break;
+          tensor_wait(v[1]);
+          if (part + 2 < parts) tensor_load32(from + (part + 2) * 32, v[0]);
+          write(part + 1, v[1]);
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        barrier_arrive(&sm.free[buffer]);
+        there = next;
+      }
+    }
+  } else if (tid < kReadOut + kGather) {
     // ---- gather: thread i takes piece i % 8 of the lines of pages i / 8 + 16 k ----
     constexpr int kRows = kLanes / (kGather / 8);
-    const int piece = tid & 7, line0 = (tid - kGather) >> 3;
+    constexpr int kAhead = 3;  // steps on their way beside the newest
+    const int piece = tid & 7, line0 = (tid - kReadOut) >> 3;
     const uint16_t* const bounds = static_cast<const uint16_t*>(c.bounds);
     int step = 0;
     bool ok = true;
@@ -351,117 +450,145 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       barrier_arrive(&sm.full[s % kStages]);
     };
-    for (int tile = 0; tile < tiles && ok; ++tile) {
-      int id[kRows];
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const int j = first_page + tile * kLanes + line0 + k * (kGather / 8);
-        id[k] = j < seen ? page_of(c, b, seq, j) : -1;
-      }
-      for (int chunk = 0; chunk < kChunks; ++chunk, ++step) {
-        const int s = step % kStages;
-        if (step >= kStages && !barrier_wait(&sm.empty[s], (step / kStages - 1) & 1, failed)) {
-          ok = false;
-          break;
-        }
-        const uint32_t to = shared_address(sm.pages[s]);
+    for (int64_t i = blockIdx.x; i < work.items && ok; i += gridDim.x) {
+      if (!prompt_item(c, b, work, kTileTokens, i, &item)) continue;
+      int next[kRows];  // ids of the tile after this one
+      const auto find = [&](int tile) {
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-          const int line = line0 + k * (kGather / 8);
-          const int64_t page = id[k] < 0 ? 0 : id[k];
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                           to + line * (kLine * 2) + ((piece ^ (line & 7)) << 4)),
-                       "l"(bounds + (page * c.heads + h) * (2 * D) + chunk * kLine + piece * 8),
-                       "r"(id[k] < 0 ? 0 : 16)
-                       : "memory");
+          const int j = item.first_page + tile * kLanes + line0 + k * (kGather / 8);
+          next[k] = tile < item.tiles && j < item.seen ? page_of(c, b, item.seq, j) : -1;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (step >= 2) {  // two more on their way
-          asm volatile("cp.async.wait_group 2;" ::: "memory");
-          publish(step - 2);
+      };
+      find(0);
+      for (int tile = 0; tile < item.tiles && ok; ++tile) {
+        int id[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) id[k] = next[k];
+        find(tile + 1);
+        for (int chunk = 0; chunk < kChunks; ++chunk, ++step) {
+          const int s = step % kStages;
+          if (step >= kStages && !barrier_wait(&sm.empty[s], (step / kStages - 1) & 1, failed)) {
+            ok = false;
+            break;
+          }
+          const uint32_t to = shared_address(sm.pages[s]);
+          const int channel = (chunk & 1) * D + (chunk >> 1) * kLine + piece * 8;
+#pragma unroll
+          for (int k = 0; k < kRows; ++k) {
+            const int line = line0 + k * (kGather / 8);
+            const int64_t page = id[k] < 0 ? 0 : id[k];
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             to + line * (kLine * 2) + ((piece ^ (line & 7)) << 4)),
+                         "l"(bounds + (page * c.heads + item.head) * (2 * D) + channel),
+                         "r"(id[k] < 0 ? 0 : 16)
+                         : "memory");
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+          if (step >= kAhead) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
+            publish(step - kAhead);
+          }
         }
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (ok)
-      for (int s = step < 2 ? 0 : step - 2; s < step; ++s) publish(s);
-  } else if (warp == 8) {
+      for (int s = step < kAhead ? 0 : step - kAhead; s < step; ++s) publish(s);
+  } else if (warp < kIssueWarp) {
+    // ---- columns: 8 channels at a time, the positive and the negative part to their lines ----
+    constexpr int kLines = D / kLine;                    // of a column of q
+    constexpr int kPieces = kColumns * kLine / 8 / kFill;  // a thread's pieces of a line
+    const int thread = tid - kReadOut - kGather;
+    const int piece = thread & 7;
+    bool ok = true;
+    int count = 0;  // items so far
+    for (int64_t i = blockIdx.x; i < work.items && ok; i += gridDim.x) {
+      const bool any = prompt_item(c, b, work, kTileTokens, i, &item);
+      // lengths, by the threads of each column tile's first run
+      if (i % work.groups == 0 && thread < item.tokens) {
+        const int pos = item.pos0 + thread;
+        a.ke[(item.row0 + thread) * c.heads + item.head] =
+            pos < 0 ? 0 : (pos >> c.page_shift) + 1;
+      }
+      if (!any) continue;
+      uint4 w[kLines][kPieces];
+#pragma unroll
+      for (int line = 0; line < kLines; ++line)
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+          const int col = (thread >> 3) + n * (kFill / 8);
+          const int token = col / kPadded;
+          const int head = col % kPadded < a.group ? col % kPadded : a.group - 1;
+          w[line][n] = make_uint4(0u, 0u, 0u, 0u);
+          if (token < item.tokens)
+            w[line][n] = __ldg(reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(a.q.data) + (item.row0 + token) * a.q.token_stride +
+                ((int64_t)item.head * a.group + head) * a.q.head_stride + line * kLine +
+                piece * 8));
+        }
+#pragma unroll
+      for (int chunk = 0; chunk < kChunks; ++chunk) {
+        if (ok && count > 0) ok = barrier_wait(&sm.released[chunk], (count - 1) & 1, failed);
+        if (!ok) break;
+        const bool positive = (chunk & 1) == 0;
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+          const int col = (thread >> 3) + n * (kFill / 8);
+          const uint4 u = w[chunk >> 1][n];
+          *reinterpret_cast<uint4*>(
+              &sm.columns[chunk][col * (kLine * 2) + ((piece ^ (col & 7)) << 4)]) =
+              make_uint4(clamp_sign<kFp16>(u.x, positive), clamp_sign<kFp16>(u.y, positive),
+                         clamp_sign<kFp16>(u.z, positive), clamp_sign<kFp16>(u.w, positive));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        barrier_arrive(&sm.filled[chunk]);
+      }
+      ++count;
+    }
+  } else {
     // ---- products, by one thread ----
     if (lane == 0) {
       constexpr uint32_t kType = kFp16 ? 0u : 1u;
       constexpr uint32_t kind = 1u << 4 | kType << 7 | kType << 10 | (kColumns / 8) << 17 |
                                 (kLanes / 16) << 24;
-      int step = 0;
+      int step = 0, count = 0, items = 0;
       bool ok = true;
-      for (int tile = 0; tile < tiles && ok; ++tile) {
-        const int buffer = tile & 1;
-        if (tile >= 2) ok = barrier_wait(&sm.free[buffer], (tile / 2 - 1) & 1, failed);
-        for (int chunk = 0; chunk < kChunks && ok; ++chunk, ++step) {
-          const int s = step % kStages;
-          if (!barrier_wait(&sm.full[s], (step / kStages) & 1, failed)) {
-            ok = false;
-            break;
-          }
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t pages = operand(shared_address(sm.pages[s]));
-          const uint64_t columns = operand(shared_address(sm.columns[chunk]));
+      for (int64_t i = blockIdx.x; i < work.items && ok; i += gridDim.x) {
+        if (!prompt_item(c, b, work, kTileTokens, i, &item)) continue;
+        for (int tile = 0; tile < item.tiles && ok; ++tile, ++count) {
+          const int buffer = count & 1;
+          if (count >= 2) ok = barrier_wait(&sm.free[buffer], ((count >> 1) - 1) & 1, failed);
+          for (int chunk = 0; chunk < kChunks && ok; ++chunk, ++step) {
+            const int s = step % kStages;
+            if (tile == 0) ok = barrier_wait(&sm.filled[chunk], items & 1, failed);
+            if (ok) ok = barrier_wait(&sm.full[s], (step / kStages) & 1, failed);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint64_t pages = operand(shared_address(sm.pages[s]));
+            const uint64_t columns = operand(shared_address(sm.columns[chunk]));
 #pragma unroll
-          for (int k = 0; k < kLine / 16; ++k)  // 32 bytes of a line each
-            tensor_mma(tensor + buffer * kColumns, pages + 2 * k, columns + 2 * k, kind,
-                       chunk > 0 || k > 0);
-          tensor_commit(&sm.empty[s]);
+            for (int k = 0; k < kLine / 16; ++k)  // 32 bytes of a line each
+              tensor_mma(tensor + buffer * kColumns, pages + 2 * k, columns + 2 * k, kind,
+                         chunk > 0 || k > 0);
+            tensor_commit(&sm.empty[s]);
+            if (tile == item.tiles - 1) tensor_commit(&sm.released[chunk]);
+          }
+          if (ok) tensor_commit(&sm.done[buffer]);
         }
-        if (ok) tensor_commit(&sm.done[buffer]);
+        ++items;
       }
       // what was issued ends before the shared memory and the tensor memory go
-      if (!ok) {
-        int none = 0;
-        tensor_commit(&sm.drained);
-        barrier_wait(&sm.drained, 0, &none);
-      }
+      int none = 0;
+      tensor_commit(&sm.drained);
+      barrier_wait(&sm.drained, 0, &none);
     }
     __syncwarp();
-  } else if (warp < 4) {
-    // ---- read out ----
-    constexpr int kEach = 32 / kPadded;  // tokens of 32 columns
-    bool ok = true;
-    for (int tile = 0; tile < tiles; ++tile) {
-      const int buffer = tile & 1;
-      const int j = first_page + tile * kLanes + warp * 32 + lane;
-      const bool there = j < seen && page_of(c, b, seq, j) >= 0;
-      if (ok) ok = barrier_wait(&sm.done[buffer], (tile / 2) & 1, failed);
-      ok = __all_sync(~0u, ok);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      for (int part = 0; part < kColumns / 32 && part * kEach < tokens; ++part) {
-        float v[32];
-        if (ok) {
-          tensor_load32(tensor + ((uint32_t)(warp * 32) << 16) + buffer * kColumns + part * 32, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(0x7FFFFFFFu);
-        }
-#pragma unroll
-        for (int t = 0; t < kEach; ++t) {
-          float best = v[t * kPadded];
-#pragma unroll
-          for (int k = 1; k < kPadded; ++k) best = max_nan(best, v[t * kPadded + k]);
-          const int token = part * kEach + t;
-          const int pos = pos0 + token;
-          const int newest = pos >> c.page_shift;
-          if (token >= tokens || pos < 0 || j > newest) continue;
-          if (j < a.keep_first || j > newest - a.keep_last) best = __uint_as_float(0x7F800000u);
-          if (!there) best = -__uint_as_float(0x7F800000u);
-          a.scores[((row0 + token) * c.heads + h) * a.row_pitch + j] = best;
-        }
-      }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      barrier_arrive(&sm.free[buffer]);
-    }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  if (warp == 8)
+  if (warp == kIssueWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tensor)
                  : "memory");
 }
@@ -476,14 +603,18 @@ int launch_prompt(const CacheArgs& c, const BatchArgs& b, const ScoreArgs& a,
     cudaGetLastError();
     return EXACT_TOPK_ERR_CUDA;
   }
-  const int64_t slots = slot_count(b, kColumns / kPadded, 1);
-  const int64_t tiles = ((int64_t)b.width + kLanes - 1) / kLanes;
-  // A CTA's columns cost as much as about two tiles to bring in; seven waves of CTAs leave
-  // little of the last one idle.
-  int64_t each = slots * c.heads * tiles / (152 * 7);
-  each = each < 1 ? 1 : (each > 16 ? 16 : each);
-  const dim3 grid((unsigned)slots, (unsigned)((tiles + each - 1) / each), (unsigned)c.heads);
-  kernel<<<grid, kPromptThreads, smem, stream>>>(c, b, a, (int)each);
+  PromptWork work;
+  work.slots = slot_count(b, kColumns / kPadded, 1);
+  const int tiles = (b.width + kLanes - 1) / kLanes;
+  // Runs of page tiles: about seven for each CTA, so that the last ones end together, of at
+  // most 16 and at least 2 tiles, which the bringing in of an item's columns hides behind.
+  int64_t each = work.slots * c.heads * tiles / (kSms * 7);
+  each = each < 2 ? 2 : (each > 16 ? 16 : each);
+  work.each = (int)each;
+  work.groups = (int)((tiles + each - 1) / each);
+  work.items = work.slots * c.heads * work.groups;
+  const unsigned grid = (unsigned)(work.items < kSms ? work.items : kSms);
+  kernel<<<grid, kPromptThreads, smem, stream>>>(c, b, a, work);
   return launch_status();
 }
 
