@@ -419,19 +419,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (t < left && pos >= 0 && j <= newest) *at = best;
           }
         };
-        float v[2][32];
-        tensor_load32(from, v[0]);
         bool next = false;  // the next tile's page, asked for before it is needed
         if (tile + 1 < item.tiles && j + kLanes < item.seen)
           next = page_of(c, b, item.seq, j + kLanes) >= 0;
-        for (int part = 0; part < parts; part += 2) {
-          tensor_wait(v[0]);
-          if (part + 1 < parts) tensor_load32(from + (part + 1) * 32, v[1]);
-          write(part, v[0]);
-          if (part + 1 >= parts) break;
-          tensor_wait(v[1]);
-          if (part + 2 < parts) tensor_load32(from + (part + 2) * 32, v[0]);
-          write(part + 1, v[1]);
+        for (int part = 0; part < parts; ++part) {
+          float v[32];
+          tensor_load32(from + part * 32, v);
+          tensor_wait(v);
+          write(part, v);
         }
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         barrier_arrive(&sm.free[buffer]);
@@ -441,15 +436,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   } else if (tid < kReadOut + kGather) {
     // ---- gather: thread i takes piece i % 8 of the lines of pages i / 8 + 16 k ----
     constexpr int kRows = kLanes / (kGather / 8);
-    constexpr int kAhead = 3;  // steps on their way beside the newest
     const int piece = tid & 7, line0 = (tid - kReadOut) >> 3;
     const uint16_t* const bounds = static_cast<const uint16_t*>(c.bounds);
     int step = 0;
     bool ok = true;
-    const auto publish = [&](int s) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      barrier_arrive(&sm.full[s % kStages]);
-    };
     for (int64_t i = blockIdx.x; i < work.items && ok; i += gridDim.x) {
       if (!prompt_item(c, b, work, kTileTokens, i, &item)) continue;
       int next[kRows];  // ids of the tile after this one
@@ -484,17 +474,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                          "r"(id[k] < 0 ? 0 : 16)
                          : "memory");
           }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          if (step >= kAhead) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-            publish(step - kAhead);
-          }
+          // arrives when this thread's copies have; the issuing thread orders them before its reads
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                           shared_address(&sm.full[s]))
+                       : "memory");
         }
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
-    if (ok)
-      for (int s = step < kAhead ? 0 : step - kAhead; s < step; ++s) publish(s);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp < kIssueWarp) {
     // ---- columns: 8 channels at a time, the positive and the negative part to their lines ----
     constexpr int kLines = D / kLine;                    // of a column of q
@@ -564,6 +551,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (tile == 0) ok = barrier_wait(&sm.filled[chunk], items & 1, failed);
             if (ok) ok = barrier_wait(&sm.full[s], (step / kStages) & 1, failed);
             if (!ok) break;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint64_t pages = operand(shared_address(sm.pages[s]));
             const uint64_t columns = operand(shared_address(sm.columns[chunk]));
