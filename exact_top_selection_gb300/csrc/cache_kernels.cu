@@ -47,16 +47,70 @@ __device__ __forceinline__ float scale_for(float amax) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Two numbers as codes.  y + 0 * y is y, and NaN for an infinity, which the
-// saturating conversion would otherwise turn into 448.
+// Two numbers as codes.  The conversion saturates; where kSpecial, y + 0 * y, which is NaN for
+// an infinity, keeps infinities from becoming 448.
+template <bool kSpecial>
 __device__ __forceinline__ uint32_t encode2(float x, float y) {
-  const float2 v = make_float2(fmaf(x, 0.f, x), fmaf(y, 0.f, y));
+  const float2 v = kSpecial ? make_float2(fmaf(x, 0.f, x), fmaf(y, 0.f, y)) : make_float2(x, y);
   return (uint32_t)__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+template <bool kFp16, bool kSpecial>
+__device__ __forceinline__ uint2 encode8(const uint4& x, float by) {
+  const float2 a = unpack2<kFp16>(x.x), b = unpack2<kFp16>(x.y), c = unpack2<kFp16>(x.z),
+               d = unpack2<kFp16>(x.w);
+  return make_uint2(
+      encode2<kSpecial>(a.x * by, a.y * by) | encode2<kSpecial>(b.x * by, b.y * by) << 16,
+      encode2<kSpecial>(c.x * by, c.y * by) | encode2<kSpecial>(d.x * by, d.y * by) << 16);
 }
 
 __device__ __forceinline__ float finite_magnitude(float x) {
   const float a = fabsf(x);
   return a < __uint_as_float(0x7F800000u) ? a : 0.f;
+}
+
+// Pairs of the rows' type.
+template <bool kFp16>
+__device__ __forceinline__ uint32_t larger2(uint32_t x, uint32_t y) {
+  if (kFp16) {
+    const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&x),
+                                   *reinterpret_cast<__nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <bool kFp16>
+__device__ __forceinline__ uint32_t smaller2(uint32_t x, uint32_t y) {
+  if (kFp16) {
+    const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&x),
+                                   *reinterpret_cast<__nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Bit patterns: the type's infinity, in both halves.
+template <bool kFp16>
+constexpr uint32_t infinities() {
+  return kFp16 ? 0x7C007C00u : 0x7F807F80u;
+}
+
+// NaN as 0 and infinities as the type's largest number, in both halves.
+template <bool kFp16>
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  uint32_t r = 0u;
+#pragma unroll
+  for (int s = 0; s < 32; s += 16) {
+    uint32_t x = w >> s & 0xFFFFu;
+    const uint32_t a = x & 0x7FFFu, inf = infinities<kFp16>() & 0xFFFFu;
+    if (a == inf) x -= 1u;  // the pattern before infinity
+    if (a > inf) x = 0u;
+    r |= x << s;
+  }
+  return r;
 }
 
 // One pass over the rows: a page's part is held in registers (8 channels a thread
@@ -66,14 +120,14 @@ __device__ __forceinline__ float finite_magnitude(float x) {
 // move the borders of its exponents, and with powers of two every division here and
 // every product on reading is exact.
 template <bool kFp16, int D, int P>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs c, BatchArgs b,
+__global__ void __launch_bounds__(kThreads, P * D >= 16384 ? 5 : 8) cache_write_kernel(CacheArgs c, BatchArgs b,
                                                                RowArgs krows, RowArgs vrows) {
   constexpr int kLanes = D / 8;               // threads on a row
   constexpr int kRows = kThreads / kLanes;    // rows of a pass
   constexpr int kPasses = P / kRows > 0 ? P / kRows : 1;
   constexpr int kShift = P == 16 ? 4 : (P == 32 ? 5 : (P == 64 ? 6 : 7));
   __shared__ float s_max[kWarps];
-  __shared__ float s_hi[kWarps][D], s_lo[kWarps][D];
+  __shared__ uint32_t s_hi[kWarps][D / 2], s_lo[kWarps][D / 2];
 
   PagePart part;
   if (!page_part(b, kShift, blockIdx.x, &part)) return;
@@ -90,59 +144,79 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs c, Batc
   const uint16_t* const rows = static_cast<const uint16_t*>(src.data);
 
   for (int h = blockIdx.y; h < c.heads; h += gridDim.y) {
+    const uint16_t* const from = rows + row_base * src.token_stride +
+                                 (int64_t)h * src.head_stride + chunk * 8;
     uint4 x[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int o = row0 + i * kRows;
       x[i] = make_uint4(0u, 0u, 0u, 0u);
       if (o >= part.first && o < part.end)
-        x[i] = *reinterpret_cast<const uint4*>(rows + (row_base + o) * src.token_stride +
-                                               h * src.head_stride + chunk * 8);
+        x[i] = __ldg(reinterpret_cast<const uint4*>(from + o * src.token_stride));
     }
-    float amax = 0.f;
-    float hi[8], lo[8];
+    // Magnitudes compare as integers; an infinity or NaN shows as one at or above infinity's
+    // pattern. A page that has one is read again, row by row.
+    uint32_t top = 0u, hi[4], lo[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      hi[j] = -__uint_as_float(0x7F800000u);
-      lo[j] = __uint_as_float(0x7F800000u);
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = infinities<kFp16>() | 0x80008000u;
+      lo[j] = infinities<kFp16>();
     }
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu),
+                                   __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu)));
       const int o = row0 + i * kRows;
-      if (o < part.first || o >= part.end) continue;
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      if (bounds && o >= part.first && o < part.end) {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack2<kFp16>(w[j]);
-        amax = fmaxf(amax, fmaxf(finite_magnitude(f.x), finite_magnitude(f.y)));
-        if (bounds) {
-          const float most = kFp16 ? 65504.f : __uint_as_float(0x7F7F0000u);
-          const float u = f.x == f.x ? fminf(fmaxf(f.x, -most), most) : 0.f;
-          const float v = f.y == f.y ? fminf(fmaxf(f.y, -most), most) : 0.f;
-          hi[2 * j] = fmaxf(hi[2 * j], u);
-          lo[2 * j] = fminf(lo[2 * j], u);
-          hi[2 * j + 1] = fmaxf(hi[2 * j + 1], v);
-          lo[2 * j + 1] = fminf(lo[2 * j + 1], v);
+        for (int j = 0; j < 4; ++j) {
+          hi[j] = larger2<kFp16>(hi[j], w[j]);
+          lo[j] = smaller2<kFp16>(lo[j], w[j]);
         }
       }
     }
+    const bool special =
+        __syncthreads_or((top & 0xFFFFu) >= (infinities<kFp16>() & 0xFFFFu) ||
+                         top >= (infinities<kFp16>() & 0xFFFF0000u)) != 0;
+    const float2 both = unpack2<kFp16>(top);
+    float amax = fmaxf(both.x, both.y);
+    if (special) {
+      amax = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+      for (int j = 0; j < 4; ++j) {
+        hi[j] = infinities<kFp16>() | 0x80008000u;
+        lo[j] = infinities<kFp16>();
+      }
+#pragma unroll 1
+      for (int o = row0; o < part.end; o += kRows) {
+        if (o < part.first) continue;
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(from + o * src.token_stride));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = unpack2<kFp16>(w[j]);
+          amax = fmaxf(amax, fmaxf(finite_magnitude(f.x), finite_magnitude(f.y)));
+          hi[j] = larger2<kFp16>(hi[j], finite2<kFp16>(w[j]));
+          lo[j] = smaller2<kFp16>(lo[j], finite2<kFp16>(w[j]));
+        }
+      }
+    }
     if (bounds) {
 #pragma unroll
       for (int o = 16; o >= kLanes; o >>= 1)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          hi[j] = fmaxf(hi[j], __shfl_xor_sync(~0u, hi[j], o));
-          lo[j] = fminf(lo[j], __shfl_xor_sync(~0u, lo[j], o));
+        for (int j = 0; j < 4; ++j) {
+          hi[j] = larger2<kFp16>(hi[j], __shfl_xor_sync(~0u, hi[j], o));
+          lo[j] = smaller2<kFp16>(lo[j], __shfl_xor_sync(~0u, lo[j], o));
         }
-      if (lane < kLanes)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s_hi[warp][chunk * 8 + j] = hi[j];
-          s_lo[warp][chunk * 8 + j] = lo[j];
-        }
+      if (lane < kLanes) {
+        *reinterpret_cast<uint4*>(&s_hi[warp][chunk * 4]) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(&s_lo[warp][chunk * 4]) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
     if (lane == 0) s_max[warp] = amax;
     const int64_t tile = (int64_t)page * c.heads + h;
     const float held = part.first > 0 ? scales[tile] : 0.f;  // read before it is replaced
@@ -151,19 +225,20 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs c, Batc
     const float scale = fmaxf(scale_for(amax), held);
     uint8_t* const out = codes + tile * (P * D);
     const float inverse = 1.f / scale;  // exact: the scale is a power of two
+    if (!special) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int o = row0 + i * kRows;
-      if (o < part.first || o >= part.end) continue;
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint32_t q[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack2<kFp16>(w[j]);
-        q[j] = encode2(f.x * inverse, f.y * inverse);
+      for (int i = 0; i < kPasses; ++i) {
+        const int o = row0 + i * kRows;
+        if (o >= part.first && o < part.end)
+          *reinterpret_cast<uint2*>(out + o * D + chunk * 8) =
+              encode8<kFp16, false>(x[i], inverse);
       }
-      *reinterpret_cast<uint2*>(out + o * D + chunk * 8) =
-          make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+    } else {
+#pragma unroll 1
+      for (int o = row0; o < part.end; o += kRows)
+        if (o >= part.first)
+          *reinterpret_cast<uint2*>(out + o * D + chunk * 8) = encode8<kFp16, true>(
+              __ldg(reinterpret_cast<const uint4*>(from + o * src.token_stride)), inverse);
     }
     if (part.first > 0 && scale != held) {
       const float ratio = held / scale;
@@ -176,21 +251,24 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(CacheArgs c, Batc
         for (int j = 0; j < 2; ++j) {
           const float2 f0 = codes_to_float2((uint16_t)w[j]);
           const float2 f1 = codes_to_float2((uint16_t)(w[j] >> 16));
-          q[j] = encode2(f0.x * ratio, f0.y * ratio) | encode2(f1.x * ratio, f1.y * ratio) << 16;
+          q[j] = encode2<true>(f0.x * ratio, f0.y * ratio) |
+                 encode2<true>(f1.x * ratio, f1.y * ratio) << 16;
         }
         *at = make_uint2(q[0], q[1]);
       }
     }
-    if (bounds && tid < D) {
-      float u = fmaxf(fmaxf(s_hi[0][tid], s_hi[1][tid]), fmaxf(s_hi[2][tid], s_hi[3][tid]));
-      float v = fminf(fminf(s_lo[0][tid], s_lo[1][tid]), fminf(s_lo[2][tid], s_lo[3][tid]));
-      uint16_t* const at = static_cast<uint16_t*>(c.bounds) + tile * (2 * D) + tid;
+    if (bounds && tid < D / 2) {
+      uint32_t u = larger2<kFp16>(larger2<kFp16>(s_hi[0][tid], s_hi[1][tid]),
+                                  larger2<kFp16>(s_hi[2][tid], s_hi[3][tid]));
+      uint32_t v = smaller2<kFp16>(smaller2<kFp16>(s_lo[0][tid], s_lo[1][tid]),
+                                   smaller2<kFp16>(s_lo[2][tid], s_lo[3][tid]));
+      uint32_t* const at = static_cast<uint32_t*>(c.bounds) + tile * D + tid;
       if (part.first > 0) {
-        u = fmaxf(u, unpack2<kFp16>(at[0]).x);
-        v = fminf(v, unpack2<kFp16>(at[D]).x);
+        u = larger2<kFp16>(u, at[0]);
+        v = smaller2<kFp16>(v, at[D / 2]);
       }
-      at[0] = (uint16_t)pack2<kFp16>(u, 0.f);
-      at[D] = (uint16_t)pack2<kFp16>(v, 0.f);
+      at[0] = u;
+      at[D / 2] = v;
     }
     if (tid == 0) scales[tile] = scale;
     __syncthreads();  // the shared maxima are free for the next head
@@ -228,31 +306,44 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(CacheArgs c, Batch
   const uint8_t* const codes = keys ? c.k : c.v;
   const float* const scales = keys ? c.k_scale : c.v_scale;
   const int steps = heads << (c.page_shift + lane_shift);
-#pragma unroll 4
-  for (int i = threadIdx.x; i < steps; i += kThreads) {
-    const int chunk = i & (lanes - 1), o = (i >> lane_shift) & (P - 1);
-    const int h = (int)blockIdx.y + (i >> (c.page_shift + lane_shift)) * (int)gridDim.y;
-    if (o < part.first || o >= part.end) continue;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    float scale = 0.f;
-    if (page >= 0) {
-      const int64_t tile = (int64_t)page * c.heads + h;
-      x = *reinterpret_cast<const uint4*>(codes + (tile * P + o) * D + chunk * 16);
-      scale = scales[tile];
-    }
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t y[8];
+  constexpr int kBatch = 4;  // loads on their way
+  for (int i0 = threadIdx.x; i0 < steps; i0 += kThreads * kBatch) {
+    uint4 x[kBatch];
+    float scale[kBatch];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f0 = codes_to_float2((uint16_t)w[j]);
-      const float2 f1 = codes_to_float2((uint16_t)(w[j] >> 16));
-      y[2 * j] = pack2<kFp16>(f0.x * scale, f0.y * scale);
-      y[2 * j + 1] = pack2<kFp16>(f1.x * scale, f1.y * scale);
+    for (int n = 0; n < kBatch; ++n) {
+      const int i = i0 + n * kThreads;
+      const int o = (i >> lane_shift) & (P - 1);
+      const int h = (int)blockIdx.y + (i >> (c.page_shift + lane_shift)) * (int)gridDim.y;
+      x[n] = make_uint4(0u, 0u, 0u, 0u);
+      scale[n] = 0.f;
+      if (page >= 0 && i < steps && o >= part.first && o < part.end) {
+        const int64_t tile = (int64_t)page * c.heads + h;
+        x[n] = __ldg(reinterpret_cast<const uint4*>(codes + (tile * P + o) * D +
+                                                    (i & (lanes - 1)) * 16));
+        scale[n] = __ldg(scales + tile);
+      }
     }
-    uint4* const at = reinterpret_cast<uint4*>(rows + (row_base + o) * dst.token_stride +
-                                               h * dst.head_stride + chunk * 16);
-    at[0] = make_uint4(y[0], y[1], y[2], y[3]);
-    at[1] = make_uint4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      const int i = i0 + n * kThreads;
+      const int o = (i >> lane_shift) & (P - 1);
+      const int h = (int)blockIdx.y + (i >> (c.page_shift + lane_shift)) * (int)gridDim.y;
+      if (i >= steps || o < part.first || o >= part.end) continue;
+      const uint32_t w[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+      uint32_t y[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f0 = codes_to_float2((uint16_t)w[j]);
+        const float2 f1 = codes_to_float2((uint16_t)(w[j] >> 16));
+        y[2 * j] = pack2<kFp16>(f0.x * scale[n], f0.y * scale[n]);
+        y[2 * j + 1] = pack2<kFp16>(f1.x * scale[n], f1.y * scale[n]);
+      }
+      uint4* const at = reinterpret_cast<uint4*>(rows + (row_base + o) * dst.token_stride +
+                                                 h * dst.head_stride + (i & (lanes - 1)) * 16);
+      at[0] = make_uint4(y[0], y[1], y[2], y[3]);
+      at[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
   }
 }
 
