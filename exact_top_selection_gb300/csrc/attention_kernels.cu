@@ -115,9 +115,10 @@ __device__ __forceinline__ void tile_shape(const AttentionArgs& a, const CacheAr
 }
 
 // Steps of 16 tokens that a warp holds in shared memory, all but one of them on their
-// way.
+// way: 40 to 48 KB of a CTA where four share an SM, more where fewer do.
 constexpr int ring_steps(int dim, int tiles) {
-  return (tiles == 1 ? 3 : 5) * (dim == 64 ? 2 : 1);
+  const int ctas = attention_ctas_per_sm(tiles * 8, dim);
+  return dim == 128 ? (ctas == 4 ? 3 : (ctas == 3 ? 4 : 5)) : (ctas == 4 ? 5 : 8);
 }
 
 template <int D, int NT>
@@ -140,11 +141,12 @@ struct alignas(128) Shared {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8))
+__global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
     attention_kernel(CacheArgs c, BatchArgs b, AttentionArgs a) {
   constexpr int kTiles = D / 16;    // channel tiles of the output
   constexpr int kHalf = D / 64;     // 64-byte parts of a token's codes
-  constexpr bool kHoldQ = NT <= 2;  // query fragments in registers; else read at each step
+  // query fragments in registers where there is room; else read at each step
+  constexpr bool kHoldQ = D * NT <= 128;
   using Smem = Shared<D, NT>;
   extern __shared__ __align__(16) unsigned char raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8))
       // Codes of step i into its place of the ring. A step is contiguous in memory. In
       // shared memory its 16-byte pieces are exchanged within lines of 128 bytes so
       // that the reads below touch every bank once.
-      const auto fetch = [&](int i) {
+      const auto fetch = [&](int i, int place_in_ring) {
         if (i < steps) {
           int e, row0;
           find(i, &e, &row0);
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8))
           if (page >= 0 && rows > 0) {
             const int64_t at =
                 (((int64_t)page * c.heads + t.head) * c.page + row0) * D + lane * 16;
-            const uint32_t to = ring + (i % Smem::kRing) * (2 * kStep * D);
+            const uint32_t to = ring + place_in_ring * (2 * kStep * D);
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
               const int piece = lane + 32 * j, line = piece >> 3, p = piece & 7;
@@ -421,14 +423,14 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8))
         copy_commit();
       };
 
-      const auto compute = [&](int i) {
+      const auto compute = [&](int i, int place_in_ring) {
         int e, row0;
         find(i, &e, &row0);
         const int pos = position(e, row0);
         if (sm.page[e] < 0 || pos >= most) return;
         const uint32_t members = listed ? sm.entry[e] >> 24 : everyone;
         const float2 scale = sm.scale[e];
-        const uint8_t* const codes = &sm.ring[warp][i % Smem::kRing][0][0];
+        const uint8_t* const codes = &sm.ring[warp][place_in_ring][0][0];
         // Eight columns of which no token takes the page are left out. Where some do and
         // some do not, or the step ends beyond a token, scores are masked.
         bool takes[NT];
@@ -644,14 +646,16 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8))
         }
       };
 
-#pragma unroll
-      for (int i = 0; i < Smem::kRing - 1; ++i) fetch(i);
+      for (int i = 0; i < Smem::kRing - 1; ++i) fetch(i, i);
+      int now = 0, behind = Smem::kRing - 1;
       for (int i = 0; i < steps; ++i) {
         copy_wait<Smem::kRing - 2>();
         __syncwarp();
-        compute(i);
+        compute(i, now);
         __syncwarp();
-        fetch(i + Smem::kRing - 1);
+        fetch(i + Smem::kRing - 1, behind);
+        behind = now;
+        now = now + 1 == Smem::kRing ? 0 : now + 1;
       }
       copy_wait<0>();
     }

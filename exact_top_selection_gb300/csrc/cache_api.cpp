@@ -189,7 +189,7 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
   p.tile_heads = group < p.columns ? group : p.columns;
   p.tile_tokens = p.columns / p.tile_heads < 8 ? p.columns / p.tile_heads : 8;
   if (single_rows) p.tile_tokens = 1;
-  p.workers = info->sm_count * attention_ctas_per_sm(p.columns);
+  p.workers = info->sm_count * attention_ctas_per_sm(p.columns, head_dim);
   // A CTA's four warps take 32 tokens each at a time.
   p.min_units = 128 / page_size;
   p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;

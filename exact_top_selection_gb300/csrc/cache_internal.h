@@ -61,7 +61,9 @@ constexpr int64_t partial_floats(int columns, int dim) {
 }
 
 // Resident CTAs that the attention kernels are built for.
-constexpr int attention_ctas_per_sm(int columns) { return columns == 8 ? 4 : 2; }
+constexpr int attention_ctas_per_sm(int columns, int dim) {
+  return dim == 64 ? (columns == 32 ? 3 : 4) : (columns == 8 ? 4 : (columns == 16 ? 3 : 2));
+}
 
 int launch_cache_write(const CacheArgs&, const BatchArgs&, const RowArgs& k, const RowArgs& v,
                        cudaStream_t);
