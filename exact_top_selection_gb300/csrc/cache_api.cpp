@@ -78,6 +78,11 @@ int check_rows(const exact_topk_rows* rows, int64_t num_tokens, RowArgs* out) {
   return EXACT_TOPK_OK;
 }
 
+// CTAs of an attention launch: the join of a tile that all of them share holds a factor for each.
+int most_workers(int columns, int dim) {
+  return kMaxAttentionWorkers / 4 * attention_ctas_per_sm(columns, dim);
+}
+
 bool heads_ok(int q_heads, int kv_heads) {
   return q_heads >= 1 && q_heads <= 65536 && q_heads % kv_heads == 0;
 }
@@ -168,7 +173,8 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
     return EXACT_TOPK_ERR_BAD_CACHE;
   const int rc = check_batch_shape(num_tokens, num_seqs, single_rows, table_width, page_size);
   if (rc != EXACT_TOPK_OK) return rc;
-  if (!heads_ok(q_heads, kv_heads)) return EXACT_TOPK_ERR_BAD_HEADS;
+  if (!heads_ok(q_heads, kv_heads) || num_tokens * q_heads > 0x7FFFFFFF)
+    return EXACT_TOPK_ERR_BAD_HEADS;
   if (num_blocks < 0 || num_blocks > EXACT_TOPK_MAX_K) return EXACT_TOPK_ERR_BAD_K;
   if (num_blocks > 0 && table_width > EXACT_TOPK_MAX_LISTED_WIDTH) return EXACT_TOPK_ERR_BAD_BATCH;
   exact_topk_attention_plan p{};
@@ -190,6 +196,7 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
   p.tile_tokens = p.columns / p.tile_heads < 8 ? p.columns / p.tile_heads : 8;
   if (single_rows) p.tile_tokens = 1;
   p.workers = info->sm_count * attention_ctas_per_sm(p.columns, head_dim);
+  if (p.workers > most_workers(p.columns, head_dim)) p.workers = most_workers(p.columns, head_dim);
   // A CTA's four warps take 32 tokens each at a time.
   p.min_units = 128 / page_size;
   p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;
@@ -214,7 +221,8 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
   if (rc == EXACT_TOPK_OK) rc = check_rows(out, plan->num_tokens, &a.out);
   if (rc != EXACT_TOPK_OK) return rc;
   if (plan->num_blocks > 0 && blocks == nullptr) return EXACT_TOPK_ERR_NULL_POINTER;
-  if (!heads_ok(plan->q_heads, c.heads)) return EXACT_TOPK_ERR_BAD_HEADS;
+  if (!heads_ok(plan->q_heads, c.heads) || plan->num_tokens * plan->q_heads > 0x7FFFFFFF)
+    return EXACT_TOPK_ERR_BAD_HEADS;
   if (plan->num_blocks < 0 || plan->num_blocks > EXACT_TOPK_MAX_K) return EXACT_TOPK_ERR_BAD_K;
   const int group = plan->q_heads / c.heads;
   if (plan->kv_heads != c.heads || plan->head_dim != c.dim || plan->page_size != c.page ||
@@ -224,7 +232,7 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
       (plan->columns != 8 && plan->columns != 16 && plan->columns != 32) || plan->tile_heads < 1 ||
       plan->tile_heads > group || plan->tile_tokens < 1 || plan->tile_tokens > 8 ||
       plan->tile_tokens * plan->tile_heads > plan->columns || plan->workers < 1 ||
-      plan->workers > 65535 || plan->min_units < 1 || !std::isfinite(scale))
+      plan->workers > most_workers(plan->columns, c.dim) || plan->min_units < 1 || !std::isfinite(scale))
     return EXACT_TOPK_ERR_BAD_PLAN;
   if (counter_bytes < plan->counter_bytes || counter_bytes < (size_t)plan->workers * 4)
     return EXACT_TOPK_ERR_COUNTERS_TOO_SMALL;
@@ -245,6 +253,10 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
   a.tile_heads = plan->tile_heads;
   a.workers = plan->workers;
   a.min_units = plan->min_units;
+  a.group_parts = (group + plan->tile_heads - 1) / plan->tile_heads;
+  // a part of a listed tile: at least 128 tokens, 32 for each warp
+  a.max_cut = plan->num_blocks * c.page / 128;
+  if (a.max_cut < 1) a.max_cut = 1;
   return launch_attention(c, b, a, reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -51,14 +51,17 @@ struct AttentionArgs {
   int32_t* counters;      // [workers] arrivals at the tile a worker starts and does not finish
   float* partial;         // [workers][2] partial tiles (partial_floats each)
   float scale_log2;       // softmax scale * log2(e)
-  int num_blocks, group, columns, tile_tokens, tile_heads, workers, min_units;
+  int num_blocks, group, group_parts, columns, tile_tokens, tile_heads, workers;
+  int min_units, max_cut;  // least pages of a part of the whole cache; most parts of a listed tile
 };
 
-// Floats of one partial tile: running maxima and sums (a pair for each of 4
-// lanes' two columns of every 8, kept for all 32 lanes) and the outputs.
+// Floats of one partial tile: running maxima and sums of the columns, and the outputs.
 constexpr int64_t partial_floats(int columns, int dim) {
-  return (int64_t)columns / 8 * 32 * 4 + (int64_t)columns * dim;
+  return (int64_t)columns * 2 + (int64_t)columns * dim;
 }
+
+// The most CTAs of an attention launch.
+constexpr int kMaxAttentionWorkers = 608;
 
 // Resident CTAs that the attention kernels are built for.
 constexpr int attention_ctas_per_sm(int columns, int dim) {

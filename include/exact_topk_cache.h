@@ -158,6 +158,7 @@ typedef struct exact_topk_attention_plan {
 } exact_topk_attention_plan;
 
 /* Pure host logic. single_rows: nonzero for batches without q_start.
+ * num_tokens * q_heads must stay below 2^31.
  * Errors: NULL_POINTER, BAD_CACHE (page_size, head_dim), BAD_BATCH, BAD_HEADS, BAD_K. */
 int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_rows, int q_heads,
                                    int kv_heads, int head_dim, int page_size, int table_width,
