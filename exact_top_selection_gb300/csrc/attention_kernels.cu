@@ -159,6 +159,125 @@ struct alignas(128) Shared {
                 "a factor for each CTA and column");
 };
 
+// Where a tile's outputs go.
+struct OutPlace {
+  uint16_t* data;  // the tile's first token and head
+  int64_t token_stride, head_stride;
+  int heads, columns, fp16;
+};
+
+// A lane's outputs of column n * 8 + 2 c + j: 2 * kOwn neighbouring channels for each warp.
+template <int D, int NT>
+__device__ __forceinline__ void write_outputs(const OutPlace& out, int col, int token, float l,
+                                              const float (&y)[D / 16 / kWarps][2]) {
+  constexpr int kOwn = D / 16 / kWarps;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint16_t* const at = out.data + token * out.token_stride +
+                       (col - token * out.heads) * out.head_stride + (lane >> 2) * (D / 8) +
+                       warp * kOwn * 2;
+  const float by = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const float y0 = l == 0.f ? 0.f : y[i][0] * by, y1 = l == 0.f ? 0.f : y[i][1] * by;
+    *reinterpret_cast<uint32_t*>(at + i * 2) = out.fp16 ? pack2<true>(y0, y1) : pack2<false>(y0, y1);
+  }
+}
+
+// Joins the partial results of a tile, in the order of its parts, and writes its outputs. Part 0
+// is at `first`, part 1 `second` floats behind it, and each further one `step` behind the one
+// before. `weight` is shared memory for a factor of each part and column, `sums` for a sum of
+// each column. Apart from the kernel's body, whose registers its own would crowd.
+template <int D, int NT>
+__device__ __noinline__ void join_parts(const float* first, int parts, int64_t second,
+                                        int64_t step, float* weight, float* sums, OutPlace out) {
+  constexpr int kColumns = NT * 8, kOwn = D / 16 / kWarps, kOwnRegs = kOwn * NT * 4;
+  constexpr int kCols = kColumns / kWarps;
+  constexpr int kBatch = kOwnRegs < 64 ? 64 / kOwnRegs : 1;  // parts on their way
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q4 = lane & 3;
+  const auto slot = [&](int i) { return first + (i == 0 ? 0 : second + (i - 1) * step); };
+  const int own = 2 * kColumns + warp * kOwnRegs * 32 + lane;
+  float v[kBatch][kOwnRegs];
+  const auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float* const p = slot(i0 + k) + own;
+#pragma unroll
+      for (int i = 0; i < kOwnRegs; ++i) v[k][i] = i0 + k < parts ? __ldcg(p + i * 32) : 0.f;
+    }
+  };
+  load(0);
+  // Every warp takes a quarter of the columns, a part a lane: maxima, then factors and sums.
+  float top[kCols], sum[kCols];
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+    top[k] = -infinity();
+    sum[k] = 0.f;
+  }
+  for (int i = lane; i < parts; i += 32) {
+    const float* const p = slot(i) + warp * kCols;
+    float pm[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) pm[k] = __ldcg(p + k);
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) {
+      top[k] = fmaxf(top[k], pm[k]);
+      weight[i * kColumns + warp * kCols + k] = pm[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(~0u, top[k], d));
+    if (top[k] == -infinity()) top[k] = 0.f;
+  }
+  for (int i = lane; i < parts; i += 32) {
+    const float* const p = slot(i) + kColumns + warp * kCols;
+    float pl[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) pl[k] = __ldcg(p + k);
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) {
+      float* const w = weight + i * kColumns + warp * kCols + k;
+      const float by = exp2_fast(*w - top[k]);
+      *w = by;
+      sum[k] += by * pl[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kCols; ++k) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum[k] += __shfl_xor_sync(~0u, sum[k], d);
+    if (lane == 0) sums[warp * kCols + k] = sum[k];
+  }
+  __syncthreads();
+  float r[kOwnRegs];
+#pragma unroll
+  for (int i = 0; i < kOwnRegs; ++i) r[i] = 0.f;
+  for (int i0 = 0; i0 < parts; i0 += kBatch) {
+    if (i0 > 0) load(i0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float* const by = weight + (i0 + k < parts ? i0 + k : 0) * kColumns + q4 * 2;
+#pragma unroll
+      for (int i = 0; i < kOwnRegs; ++i) r[i] += v[k][i] * by[i / 4 % NT * 8 + (i & 1)];
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int col = n * 8 + q4 * 2 + j;
+      if (col >= out.columns) continue;
+      float y[kOwn][2];
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        y[i][0] = r[(i * NT + n) * 4 + j];
+        y[i][1] = r[(i * NT + n) * 4 + 2 + j];
+      }
+      write_outputs<D, NT>(out, col, col / out.heads, sums[col], y);
+    }
+}
+
 template <int D, int NT, int ST>
 __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
     attention_kernel(CacheArgs c, BatchArgs b, AttentionArgs a) {
@@ -779,7 +898,14 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
         }
 
     // ---- join the CTAs ----
-    bool write = true;
+    OutPlace out;
+    out.data = static_cast<uint16_t*>(a.out.data) + t.row0 * a.out.token_stride +
+               ((int64_t)t.head * a.group + t.head0) * a.out.head_stride;
+    out.token_stride = a.out.token_stride;
+    out.head_stride = a.out.head_stride;
+    out.heads = t.heads;
+    out.columns = columns;
+    out.fp16 = c.fp16;
     const int first_cta = (int)(t.start / part);
     const int last_cta = (int)((t.start + t.units - 1) / part);
     if (first_cta != last_cta) {
@@ -800,90 +926,32 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
 #pragma unroll
       for (int i = 0; i < kOwn * NT * 4; ++i)
         mine_at[i * 32] = r[i / (NT * 4)][i / 4 % NT][i % 4];
-      __threadfence();
       __syncthreads();
       if (tid == 0) {
+        __threadfence();  // the CTA's partial result before its arrival
         const int arrived = atomicAdd(a.counters + first_cta, 1);
         sm.last = arrived == last_cta - first_cta;
         if (sm.last) a.counters[first_cta] = 0;
+        __threadfence();  // the others' arrivals before their partial results
       }
       __syncthreads();
-      write = sm.last != 0;
-      if (write) {
-        __threadfence();
-        const int parts = last_cta - first_cta + 1;
-        // part i: the first one's second slot, then the others' first slots
-        const float* const first =
-            a.partial + ((int64_t)first_cta * 2 + 1) * kFloats;
-        const auto slot = [&](int i) { return first + (i == 0 ? 0 : (2 * i - 1) * kFloats); };
-        // every warp finds the maxima and sums of a quarter of the columns, and each part's factor
-        for (int col = warp; col < kColumns; col += kWarps) {
-          float top = -infinity();
-          for (int i = lane; i < parts; i += 32) top = fmaxf(top, __ldcg(slot(i) + col));
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-          const float base = top == -infinity() ? 0.f : top;
-          float sum = 0.f;
-          for (int i = lane; i < parts; i += 32) {
-            const float by = exp2_fast(__ldcg(slot(i) + col) - base);
-            sm.weight[i * kColumns + col] = by;
-            sum += by * __ldcg(slot(i) + kColumns + col);
-          }
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-          if (lane == 0) sm.sum[col] = sum;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) l[n][j] = sm.sum[n * 8 + q4 * 2 + j];
-#pragma unroll
-        for (int i = 0; i < kOwn * NT * 4; ++i) r[i / (NT * 4)][i / 4 % NT][i % 4] = 0.f;
-        constexpr int kBatch = NT == 1 ? 8 : (NT == 2 ? 4 : 2);  // parts on their way
-        const int64_t own = 2 * kColumns + (warp * kOwn * NT * 4) * 32 + lane;
-        for (int i0 = 0; i0 < parts; i0 += kBatch) {
-          float v[kBatch][kOwn * NT * 4];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-            for (int i = 0; i < kOwn * NT * 4; ++i)
-              v[k][i] = i0 + k < parts ? __ldcg(slot(i0 + k) + own + i * 32) : 0.f;
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            if (i0 + k >= parts) break;
-            const float* const by = &sm.weight[(i0 + k) * kColumns + q4 * 2];
-#pragma unroll
-            for (int i = 0; i < kOwn * NT * 4; ++i)
-              r[i / (NT * 4)][i / 4 % NT][i % 4] += v[k][i] * by[i / 4 % NT * 8 + (i & 1)];
-          }
-        }
-      }
-    }
-
-    // ---- write: a lane has 2 * kOwn neighbouring channels of its columns ----
-    if (write) {
-      constexpr int kLaneChannels = D / 8;  // channels of lane / 4: 2 of each channel tile
+      if (sm.last)
+        join_parts<D, NT>(a.partial + ((int64_t)first_cta * 2 + 1) * kFloats,
+                          last_cta - first_cta + 1, kFloats, 2 * kFloats, sm.weight, sm.sum, out);
+    } else {
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int col = n * 8 + q4 * 2 + j;
-          const int token = (int)(shift[n][j] & 7u);
           if (col >= columns) continue;
-          const float by = l[n][j] == 0.f ? 0.f : 1.f / l[n][j];
-          uint16_t* const at =
-              static_cast<uint16_t*>(a.out.data) + (t.row0 + token) * a.out.token_stride +
-              ((int64_t)t.head * a.group + t.head0 + col - token * t.heads) *
-                  a.out.head_stride +
-              g * kLaneChannels + warp * kOwn * 2;
+          float y[kOwn][2];
 #pragma unroll
           for (int i = 0; i < kOwn; ++i) {
-            const float y0 = l[n][j] == 0.f ? 0.f : r[i][n][j] * by;
-            const float y1 = l[n][j] == 0.f ? 0.f : r[i][n][2 + j] * by;
-            *reinterpret_cast<uint32_t*>(at + i * 2) =
-                c.fp16 ? pack2<true>(y0, y1) : pack2<false>(y0, y1);
+            y[i][0] = r[i][n][j];
+            y[i][1] = r[i][n][2 + j];
           }
+          write_outputs<D, NT>(out, col, (int)(shift[n][j] & 7u), l[n][j], y);
         }
     }
     u = listed ? u + gridDim.x : u_end;

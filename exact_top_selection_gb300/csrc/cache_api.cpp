@@ -197,8 +197,9 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
   if (single_rows) p.tile_tokens = 1;
   p.workers = info->sm_count * attention_ctas_per_sm(p.columns, head_dim);
   if (p.workers > most_workers(p.columns, head_dim)) p.workers = most_workers(p.columns, head_dim);
-  // A CTA's four warps take 32 tokens each at a time.
-  p.min_units = 128 / page_size;
+  // A CTA's four warps take 32 tokens each at a time; with 128 tokens a CTA its part of the join
+  // outweighs its own work (four short sequences: 21.3 us, 17.0 with 256, 18.0 with 512).
+  p.min_units = 256 / page_size;
   p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;
   p.workspace_bytes = (uint64_t)p.workers * 2 * partial_floats(p.columns, head_dim) * 4;
   *plan = p;
