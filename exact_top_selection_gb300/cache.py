@@ -63,7 +63,8 @@ class AttentionPlan(ctypes.Structure):
                 ("table_width", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
                 ("columns", ctypes.c_int32), ("tile_tokens", ctypes.c_int32),
                 ("tile_heads", ctypes.c_int32), ("workers", ctypes.c_int32),
-                ("min_units", ctypes.c_int32), ("counter_bytes", ctypes.c_uint64),
+                ("min_units", ctypes.c_int32), ("prompt_tokens", ctypes.c_int32),
+                ("prompt_heads", ctypes.c_int32), ("counter_bytes", ctypes.c_uint64),
                 ("workspace_bytes", ctypes.c_uint64)]
 
     def as_dict(self):
@@ -85,7 +86,7 @@ def _lib():
         lib.exact_topk_cache_write.argtypes = [cache, batch, i64, rows, rows, p]
         lib.exact_topk_cache_read.argtypes = [cache, batch, i64, rows, rows, p]
         lib.exact_topk_block_scores.argtypes = [cache, batch, i64, i32, rows, i32, i32, p, i64, p, p, p]
-        lib.exact_topk_make_attention_plan.argtypes = [i64] + [i32] * 8 + [
+        lib.exact_topk_make_attention_plan.argtypes = [i64] + [i32] * 9 + [
             ctypes.POINTER(_etk.DeviceInfo), ctypes.POINTER(AttentionPlan)]
         lib.exact_topk_attention_run.argtypes = [ctypes.POINTER(AttentionPlan), cache, batch, rows, rows,
                                                  p, ctypes.c_float, p, sz, p, sz, p]
@@ -327,14 +328,15 @@ def block_scores(cache, batch, q, keep_first=0, keep_last=0, scores=None, ke=Non
 
 
 def make_attention_plan(num_tokens, num_seqs, q_heads, kv_heads, head_dim, page_size, table_width, num_blocks=0,
-                        single_rows=False, device_info=None) -> AttentionPlan:
-    """The attention's launch plan (pure host logic; needs a DeviceInfo, queried when omitted)."""
+                        single_rows=False, device_info=None, prompt=-1) -> AttentionPlan:
+    """The attention's launch plan (pure host logic; needs a DeviceInfo, queried when omitted).
+    prompt: whether the kernel for prompts runs: -1 the planner's choice, 0 no, 1 yes."""
     if device_info is None:
         device_info = _etk.query_device()
     plan = AttentionPlan()
     _etk._check(_lib().exact_topk_make_attention_plan(
         int(num_tokens), int(num_seqs), int(bool(single_rows)), int(q_heads), int(kv_heads), int(head_dim),
-        int(page_size), int(table_width), int(num_blocks), ctypes.byref(device_info), ctypes.byref(plan)),
+        int(page_size), int(table_width), int(num_blocks), int(prompt), ctypes.byref(device_info), ctypes.byref(plan)),
         "exact_topk_make_attention_plan")
     return plan
 
@@ -349,13 +351,13 @@ class CacheAttention:
     once).  A row that sees nothing gives zeros.  Calls of one object must not overlap on the GPU: graphs
     that may run at the same time each need an object of their own."""
 
-    def __init__(self, cache, num_seqs, num_tokens, q_heads, table_width, num_blocks=0):
+    def __init__(self, cache, num_seqs, num_tokens, q_heads, table_width, num_blocks=0, **overrides):
         import torch
         self.cache = cache
         with torch.cuda.device(cache.device):
             self.plan = make_attention_plan(num_tokens, num_seqs, q_heads, cache.kv_heads, cache.head_dim,
                                             cache.page_size, table_width, num_blocks,
-                                            single_rows=num_tokens == num_seqs)
+                                            single_rows=num_tokens == num_seqs, **overrides)
             self.counters = torch.zeros(max(16, self.plan.counter_bytes), dtype=torch.uint8, device=cache.device)
             self.workspace = torch.empty(max(16, self.plan.workspace_bytes), dtype=torch.uint8,
                                          device=cache.device)

@@ -386,6 +386,17 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
       t.head0 = group_part * a.tile_heads;
       t.heads = a.group - t.head0 < a.tile_heads ? a.group - t.head0 : a.tile_heads;
     }
+    if (a.again != nullptr) {  // behind the prompt's kernel: only what it has left
+      const int parts = (a.group + a.prompt_heads - 1) / a.prompt_heads;
+      bool left = false;
+      for (int i = 0; i < t.tokens; ++i)
+        left |= a.again[((t.row0 + i) * c.heads + t.head) * parts + t.head0 / a.prompt_heads] != 0;
+      if (!left) {
+        u = listed ? u + gridDim.x
+                   : (line_end < t.start + t.units ? line_end : t.start + t.units);
+        continue;
+      }
+    }
     const int64_t u_end =
         listed ? u + 1 : (line_end < t.start + t.units ? line_end : t.start + t.units);
     const int columns = t.tokens * t.heads;
@@ -979,6 +990,10 @@ int launch_tile(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a,
 
 int launch_attention(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a,
                      cudaStream_t stream) {
+  if (a.prompt_tokens > 0) {
+    const int rc = launch_prompt_attention(c, b, a, stream);
+    if (rc != EXACT_TOPK_OK) return rc;
+  }
   if (c.dim == 128) {
     if (a.columns == 8) return launch_tile<128, 1, 1>(c, b, a, stream);
     if (a.columns == 16) return launch_tile<128, 2, 1>(c, b, a, stream);

@@ -83,6 +83,15 @@ int most_workers(int columns, int dim) {
   return kMaxAttentionWorkers / 4 * attention_ctas_per_sm(columns, dim);
 }
 
+uint64_t partial_bytes(const exact_topk_attention_plan& p, int dim) {
+  return (uint64_t)p.workers * 2 * partial_floats(p.columns, dim) * 4;
+}
+
+uint64_t again_bytes(const exact_topk_attention_plan& p, int group) {
+  if (p.prompt_tokens == 0) return 0;
+  return (uint64_t)p.num_tokens * p.kv_heads * ((group + p.prompt_heads - 1) / p.prompt_heads);
+}
+
 bool heads_ok(int q_heads, int kv_heads) {
   return q_heads >= 1 && q_heads <= 65536 && q_heads % kv_heads == 0;
 }
@@ -165,7 +174,8 @@ int exact_topk_block_scores(const exact_topk_cache* cache, const exact_topk_batc
 
 int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_rows, int q_heads,
                                    int kv_heads, int head_dim, int page_size, int table_width,
-                                   int num_blocks, const exact_topk_device_info* info,
+                                   int num_blocks, int prompt,
+                                   const exact_topk_device_info* info,
                                    exact_topk_attention_plan* plan) {
   if (info == nullptr || plan == nullptr) return EXACT_TOPK_ERR_NULL_POINTER;
   if (!page_size_ok(page_size) || (head_dim != 64 && head_dim != 128) || kv_heads < 1 ||
@@ -201,7 +211,21 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
   // outweighs its own work (four short sequences: 21.3 us, 17.0 with 256, 18.0 with 512).
   p.min_units = 256 / page_size;
   p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;
-  p.workspace_bytes = (uint64_t)p.workers * 2 * partial_floats(p.columns, head_dim) * 4;
+  // The prompt's kernel takes 128 rows (tokens x heads) at a time and does not split a tile: it
+  // wants filled tiles, and at least as many of them as there are SMs.
+  const int prompt_heads = group < kPromptRows ? group : kPromptRows;
+  const int prompt_tokens =
+      kPromptRows / prompt_heads < kPromptTokens ? kPromptRows / prompt_heads : kPromptTokens;
+  const int64_t prompt_tiles = num_tokens / prompt_tokens * kv_heads *
+                               ((group + prompt_heads - 1) / prompt_heads);
+  const bool prompt_fits = num_blocks == 0 || table_width <= kPromptListedWidth;
+  if (prompt > 0 && !prompt_fits) return EXACT_TOPK_ERR_BAD_PLAN;
+  if (prompt > 0 || (prompt < 0 && prompt_fits && !single_rows && mean >= prompt_tokens &&
+                     prompt_tiles >= info->sm_count)) {
+    p.prompt_tokens = prompt_tokens;
+    p.prompt_heads = prompt_heads;
+  }
+  p.workspace_bytes = partial_bytes(p, head_dim) + again_bytes(p, group);
   *plan = p;
   return EXACT_TOPK_OK;
 }
@@ -233,12 +257,21 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
       (plan->columns != 8 && plan->columns != 16 && plan->columns != 32) || plan->tile_heads < 1 ||
       plan->tile_heads > group || plan->tile_tokens < 1 || plan->tile_tokens > 8 ||
       plan->tile_tokens * plan->tile_heads > plan->columns || plan->workers < 1 ||
-      plan->workers > most_workers(plan->columns, c.dim) || plan->min_units < 1 || !std::isfinite(scale))
+      plan->workers > most_workers(plan->columns, c.dim) || plan->min_units < 1 ||
+      !std::isfinite(scale) || plan->prompt_tokens < 0 || plan->prompt_tokens > kPromptTokens)
+    return EXACT_TOPK_ERR_BAD_PLAN;
+  // A tile of the kernel that runs behind the prompt's lies within one of that one's.
+  if (plan->prompt_tokens > 0 &&
+      (plan->prompt_heads < 1 || plan->prompt_heads > group ||
+       plan->prompt_tokens * plan->prompt_heads > kPromptRows ||
+       (plan->prompt_heads != group && plan->prompt_heads % plan->tile_heads != 0) ||
+       (plan->num_blocks > 0 && b.width > kPromptListedWidth)))
     return EXACT_TOPK_ERR_BAD_PLAN;
   if (counter_bytes < plan->counter_bytes || counter_bytes < (size_t)plan->workers * 4)
     return EXACT_TOPK_ERR_COUNTERS_TOO_SMALL;
-  const size_t partial = (size_t)plan->workers * 2 * partial_floats(plan->columns, c.dim) * 4;
-  if (workspace_bytes < plan->workspace_bytes || workspace_bytes < partial)
+  const uint64_t partial = partial_bytes(*plan, c.dim);
+  if (workspace_bytes < plan->workspace_bytes ||
+      workspace_bytes < partial + again_bytes(*plan, group))
     return EXACT_TOPK_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(counters, 16) || !aligned(workspace, 16) || !aligned(blocks, 4))
     return EXACT_TOPK_ERR_MISALIGNED;
@@ -254,6 +287,9 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
   a.tile_heads = plan->tile_heads;
   a.workers = plan->workers;
   a.min_units = plan->min_units;
+  a.prompt_tokens = plan->prompt_tokens;
+  a.prompt_heads = plan->prompt_heads;
+  a.again = plan->prompt_tokens > 0 ? static_cast<uint8_t*>(workspace) + partial : nullptr;
   a.group_parts = (group + plan->tile_heads - 1) / plan->tile_heads;
   // a part of a listed tile: at least 128 tokens, 32 for each warp
   a.max_cut = plan->num_blocks * c.page / 128;

@@ -52,6 +52,10 @@ struct AttentionArgs {
   float* partial;         // [workers][2] partial tiles (partial_floats each)
   float scale_log2;       // softmax scale * log2(e)
   int num_blocks, group, group_parts, columns, tile_tokens, tile_heads, workers;
+  // The prompt's kernel: tokens and heads of its tiles, 0 where it does not run; and which tokens
+  // it leaves to the other one, [num_tokens][kv_heads][parts of a group] (NULL: all).
+  int prompt_tokens, prompt_heads;
+  uint8_t* again;
   int min_units, max_cut;  // least pages of a part of the whole cache; most parts of a listed tile
 };
 
@@ -59,6 +63,12 @@ struct AttentionArgs {
 constexpr int64_t partial_floats(int columns, int dim) {
   return (int64_t)columns * 2 + (int64_t)columns * dim;
 }
+
+// Rows of a prompt's tile, its tokens at most (a bit of a word each), and the widest page table of
+// a call with lists that it takes (a word for each page in shared memory).
+constexpr int kPromptRows = 128;
+constexpr int kPromptTokens = 32;
+constexpr int kPromptListedWidth = 24576;
 
 // The most CTAs of an attention launch.
 constexpr int kMaxAttentionWorkers = 608;
@@ -73,6 +83,8 @@ int launch_cache_write(const CacheArgs&, const BatchArgs&, const RowArgs& k, con
 int launch_cache_read(const CacheArgs&, const BatchArgs&, const RowArgs& k, const RowArgs& v,
                       cudaStream_t);
 int launch_block_scores(const CacheArgs&, const BatchArgs&, const ScoreArgs&, cudaStream_t);
+int launch_prompt_attention(const CacheArgs&, const BatchArgs&, const AttentionArgs&,
+                            cudaStream_t);
 int launch_attention(const CacheArgs&, const BatchArgs&, const AttentionArgs&, cudaStream_t);
 
 }  // namespace etk

@@ -1,0 +1,635 @@
+// Attention of many neighbouring tokens over the paged 8-bit cache, on the fifth-generation
+// tensor cores (the prompt's form of exact_topk_attention_run).
+//
+// A CTA's tile is up to 128 rows: tokens x heads of one key head. It goes over the pages that
+// any of its tokens takes (all of them, or the union of the tokens' lists) in blocks of 64
+// cached tokens, with each row's running maximum m, sum l and output O:
+//
+//   S = Q K^T          [128 rows][64 tokens], FP32, in tensor memory
+//   P = e^(S - m)      in FP16, in tensor memory
+//   O += P V           [128 rows][D channels], FP32, in tensor memory
+//
+// A lane of tensor memory is a row, so a thread has a whole row of S to itself: its
+// maximum and sum need no exchange, and a token that does not take a page is a row whose
+// probabilities there are zero. Neighbouring tokens of a prompt share most of their
+// pages; where they share none, a block costs as much as if they did, which the tensor cores
+// still do faster than a kernel that leaves the others out.
+//
+// Codes are exact in FP16, so four warps turn them into FP16 operands on their way to
+// shared memory, while four warps do the softmax of the block before and one thread issues the
+// products: two CTAs share an SM, so that one's exponentials fill the other's waits. Values
+// are brought to the tile's largest scale by the power of two between (an exact product), so
+// O stays in one unit.
+//
+// Queries, probabilities and the running maximum are as in attention_kernels.cu. Three
+// things are left to that kernel, which runs behind this one on the tiles that are marked:
+// a NaN among the values (0 * NaN would reach rows that do not see it), scales of values
+// more than 2^12 apart, and a wait that ran out.
+//
+// What bounds it: the exponentials, 64 x 128 a block at 16 a clock of an SM (512 clocks, as the
+// two products take).
+
+#include "cache_device.cuh"
+#include "tensor_device.cuh"
+
+namespace etk {
+namespace {
+
+constexpr int kRows = 128;           // threads of each role
+constexpr int kConvert = 128;
+constexpr int kThreads = kRows + kConvert + 32;
+constexpr int kIssueWarp = (kRows + kConvert) / 32;
+constexpr int kBlock = 64;           // cached tokens of a block
+constexpr int kEntries = 128;        // parts of pages held at a time
+constexpr float kSlack = 8.f;        // see attention_kernels.cu
+constexpr int kFarthest = 12;        // powers of two between scales of values
+
+__device__ __forceinline__ float infinity() { return __uint_as_float(0x7F800000u); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// Operand whose contraction runs over the lines: 64 channels to a line, `chunk` bytes from one
+// 64 channels to the next.
+__device__ __forceinline__ uint64_t operand_across(uint32_t address, uint32_t chunk) {
+  return (uint64_t)((address & 0x3FFFFu) >> 4) | (uint64_t)(chunk >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// As tensor_mma, with the first operand in tensor memory.
+__device__ __forceinline__ void tensor_mma_from(uint32_t d, uint32_t a, uint64_t b,
+                                                uint32_t kind, bool add) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+      "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
+      : "memory");
+}
+
+__device__ __forceinline__ void tensor_store32(uint32_t address, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(address)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// A part of a page: at most 64 tokens.
+struct Entry {
+  int64_t offset;    // of its codes; -1 for an absent page
+  int pos;           // position of its first token
+  uint32_t members;  // tokens of the tile that take it
+  float k_scale;
+  float v_part;      // the values' scale without its power of two
+  uint32_t v_power;  // that power of two over the tile's unit, twice in FP16
+};
+
+template <int D>
+struct Shared {
+  uint8_t q[D / 64][kRows * 128];       // lines of 64 channels, in swizzled blocks of 8
+  uint8_t k[2][D / 64][kBlock * 128];
+  uint8_t v[2][D / 64][kBlock * 128];
+  Entry entry[kEntries];
+  float factor[kRows];
+  uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
+  uint64_t scored, taken, weighed, added, drained;
+  uint32_t tensor;
+  int scan[kIssueWarp];
+  int failed, again, unit;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2)
+    prompt_attention_kernel(CacheArgs c, BatchArgs b, AttentionArgs a) {
+  using Smem = Shared<D>;
+  constexpr int kLines = D / 64;
+  constexpr uint32_t kS = 128, kP = 192, kTensorColumns = 256;  // O, S, P in tensor memory
+  extern __shared__ unsigned char raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(
+      raw + ((1024u - (shared_address(raw) & 1023u)) & 1023u));
+  uint32_t* const marks = reinterpret_cast<uint32_t*>(&sm + 1);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool listed = a.blocks != nullptr;
+  const int head = blockIdx.y, head0 = (int)blockIdx.z * a.prompt_heads;
+  const int heads = a.group - head0 < a.prompt_heads ? a.group - head0 : a.prompt_heads;
+  const int64_t slot = blockIdx.x;
+  const int seq = sequence_of_slot(b, slot, a.prompt_tokens, 1);
+  const SeqRows rows = sequence_rows(b, c.page_shift, seq);
+  const int64_t index = slot - first_slot(b, seq, a.prompt_tokens, 1);
+  const int64_t token0 = index * a.prompt_tokens;
+  if (index < 0 || token0 >= rows.count) return;
+  const int tokens =
+      rows.count - token0 < a.prompt_tokens ? (int)(rows.count - token0) : a.prompt_tokens;
+  const int64_t row0 = rows.begin + token0;
+  const int pos0 = rows.pos0 + (int)token0;
+  const int live = tokens * heads;  // rows of the tile
+  const int most = pos0 + tokens > 0 ? pos0 + tokens : 0;
+  const int pages = (most + c.page - 1) >> c.page_shift;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      barrier_init(&sm.k_full[i], kConvert);
+      barrier_init(&sm.v_full[i], kConvert);
+      barrier_init(&sm.k_free[i], 1);
+      barrier_init(&sm.v_free[i], 1);
+    }
+    barrier_init(&sm.scored, 1);
+    barrier_init(&sm.taken, kRows);
+    barrier_init(&sm.weighed, kRows);
+    barrier_init(&sm.added, 1);
+    barrier_init(&sm.drained, 1);
+    sm.failed = 0;
+    sm.again = 0;
+    sm.unit = -1000;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kIssueWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     shared_address(&sm.tensor)),
+                 "r"(kTensorColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // ---- pages of a list: which tokens of the tile take each ----
+  if (listed)
+    for (int i = tid; i < pages; i += kThreads) marks[i] = 0u;
+  __syncthreads();
+  if (listed)
+    for (int token = warp; token < tokens; token += kThreads / 32) {
+      const int newest = pos0 + token >= 0 ? (pos0 + token) >> c.page_shift : -1;
+      const int32_t* const list = a.blocks + ((row0 + token) * c.heads + head) * a.num_blocks;
+      for (int i = lane; i < a.num_blocks; i += 32) {
+        const int j = __ldg(list + i);
+        if (j >= 0 && j <= newest) atomicOr(&marks[j], 1u << token);
+      }
+    }
+
+  // ---- queries: a row a warp at a time, 8 of them on their way ----
+  if (warp < kIssueWarp) {
+    constexpr int kEach = D / 32;  // channels of a lane
+    for (int r0 = warp; r0 < kRows; r0 += kIssueWarp * 8) {
+      uint32_t w[8][kEach / 2];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int row = r0 + k * kIssueWarp;
+        const int token = row / heads;
+        const uint32_t* const at = reinterpret_cast<const uint32_t*>(
+            static_cast<const uint16_t*>(a.q.data) + (row0 + token) * a.q.token_stride +
+            ((int64_t)head * a.group + head0 + row - token * heads) * a.q.head_stride +
+            lane * kEach);
+#pragma unroll
+        for (int i = 0; i < kEach / 2; ++i) w[k][i] = row < live ? __ldg(at + i) : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int row = r0 + k * kIssueWarp;
+        float2 x[kEach / 2];
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < kEach / 2; ++i) {
+          x[i] = c.fp16 ? unpack2<true>(w[k][i]) : unpack2<false>(w[k][i]);
+          top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+        int e = (int)(__float_as_uint(top) >> 23) - 127;
+        if (e == 128 || top == 0.f) e = 8;
+        int up = 8 - e;
+        up = up < -120 ? -120 : (up > 120 ? 120 : up);
+        const float by = __uint_as_float((uint32_t)(up + 127) << 23);
+        const int channel = lane * kEach, line = channel / 64, piece = channel % 64 / 8;
+        uint32_t* const to = reinterpret_cast<uint32_t*>(
+            &sm.q[line][row * 128 + ((piece ^ (row & 7)) << 4) + channel % 8 * 2]);
+#pragma unroll
+        for (int i = 0; i < kEach / 2; ++i) to[i] = pack2<true>(x[i].x * by, x[i].y * by);
+        if (lane == 0)
+          sm.factor[row] =
+              row < live ? __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2 : 0.f;
+      }
+    }
+  }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tensor = sm.tensor;
+  volatile int* const failed = &sm.failed;
+
+  // ---- how many parts of pages there are, and how many before this thread's ----
+  const int part_shift = c.page_shift > 6 ? c.page_shift - 6 : 0;  // parts of a page
+  const int part_tokens_shift = c.page_shift > 6 ? 6 : c.page_shift;
+  const int per_thread = (pages + kIssueWarp * 32 - 1) / (kIssueWarp * 32);
+  int mine = 0, count = pages;
+  if (listed) {
+    int have = 0;
+    if (warp < kIssueWarp)
+      for (int i = tid * per_thread; i < (tid + 1) * per_thread && i < pages; ++i)
+        have += marks[i] != 0u;
+    int sum = have;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(~0u, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (lane == 31 && warp < kIssueWarp) sm.scan[warp] = sum;
+    __syncthreads();
+    mine = sum - have;
+    count = 0;
+    for (int w = 0; w < kIssueWarp; ++w) {
+      if (w < warp) mine += sm.scan[w];
+      count += sm.scan[w];
+    }
+  }
+
+  // a row's state, kept by its thread
+  const int row = tid;
+  const int row_token = row < live ? row / heads : 0;
+  const int row_pos = row < live ? pos0 + row_token : -1;
+  const float row_factor = tid < kRows ? sm.factor[row] : 0.f;
+  const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+  float m = -infinity(), l = 0.f;
+  int done = 0;  // blocks so far, the same for every role
+  bool ok = true;
+
+  // O times a factor for each row
+  const auto scale_outputs = [&](float by) {
+#pragma unroll 1
+    for (int i = 0; i < D; i += 32) {
+      float v[32];
+      uint32_t w[32];
+      tensor_load32(tensor + lane_base + i, v);
+      tensor_wait(v);
+#pragma unroll
+      for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(v[k] * by);
+      tensor_store32(tensor + lane_base + i, w);
+    }
+  };
+
+  for (int chunk0 = 0; chunk0 < (count << part_shift); chunk0 += kEntries) {
+    const int left = (count << part_shift) - chunk0;
+    const int entries = left < kEntries ? left : kEntries;
+    const int per_block_shift = 6 - part_tokens_shift;
+    const int blocks = (entries + (1 << per_block_shift) - 1) >> per_block_shift;
+    // ---- the chunk's parts of pages ----
+    __syncthreads();
+    if (listed) {
+      if (warp < kIssueWarp) {
+        int at = mine << part_shift;
+        for (int i = tid * per_thread; i < (tid + 1) * per_thread && i < pages; ++i) {
+          const uint32_t who = marks[i];
+          if (who == 0u) continue;
+          for (int k = 0; k < 1 << part_shift; ++k, ++at)
+            if (at >= chunk0 && at < chunk0 + entries) {
+              sm.entry[at - chunk0].pos = (i << c.page_shift) + (k << 6);
+              sm.entry[at - chunk0].members = who;
+            }
+        }
+      }
+      __syncthreads();
+    }
+    int high = -1000;  // the largest power of two among the chunk's scales of values
+    for (int i = tid; i < kEntries; i += kThreads) {
+      Entry& e = sm.entry[i];
+      if (i >= entries) {
+        e.offset = -1;
+        e.members = 0u;
+        e.pos = most;
+        continue;
+      }
+      if (!listed) {
+        e.pos = (chunk0 + i) << part_tokens_shift;
+        e.members = ~0u;
+      }
+      const int page = page_of(c, b, seq, e.pos >> c.page_shift);
+      e.offset = -1;
+      if (page < 0) {
+        e.members = 0u;
+        continue;
+      }
+      const int64_t tile = (int64_t)page * c.heads + head;
+      e.offset = ((tile << c.page_shift) + (e.pos & (c.page - 1))) * D;
+      e.k_scale = __ldg(c.k_scale + tile);
+      const uint32_t v = __float_as_uint(__ldg(c.v_scale + tile));
+      e.v_part = __uint_as_float((v & 0x7FFFFFu) | 127u << 23);
+      const int power = (int)(v >> 23 & 255u) - 127;
+      e.v_power = (uint32_t)power;  // for now
+      high = high > power ? high : power;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const int other = __shfl_xor_sync(~0u, high, o);
+      high = high > other ? high : other;
+    }
+    const int unit_before = sm.unit;
+    __syncthreads();
+    if (lane == 0 && high > unit_before) atomicMax(&sm.unit, high);
+    __syncthreads();
+    const int unit = sm.unit;
+    for (int i = tid; i < entries; i += kThreads) {
+      Entry& e = sm.entry[i];
+      if (e.offset < 0) continue;
+      const int below = unit - (int)e.v_power;
+      if (below > kFarthest) sm.again = 1;
+      const uint32_t half = (uint32_t)(15 - (below > kFarthest ? kFarthest : below)) << 10;
+      e.v_power = half | half << 16;
+    }
+    // O so far is in the unit before
+    if (tid < kRows && done > 0 && unit > unit_before) {
+      ok = ok && barrier_wait(&sm.added, (done - 1) & 1, failed);
+      ok = __all_sync(~0u, ok);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      scale_outputs(exp2f((float)(unit_before - unit)));
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    }
+    __syncthreads();
+
+    if (tid < kRows) {
+      // ---- softmax: a row a thread ----
+      for (int block = 0; block < blocks; ++block) {
+        const int n = done + block;
+        ok = ok && barrier_wait(&sm.scored, n & 1, failed);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        float s[2][32];
+        tensor_load32(tensor + lane_base + kS, s[0]);
+        tensor_load32(tensor + lane_base + kS + 32, s[1]);
+        // what this row sees of each 16 tokens
+        int seen[4];
+        float scale[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int token = k * 16;
+          const Entry& e = sm.entry[(block << per_block_shift) + (token >> part_tokens_shift)];
+          const int pos = e.pos + (token & ((1 << part_tokens_shift) - 1));
+          const bool takes = row_pos >= 0 && (e.members >> row_token & 1u) != 0u;
+          seen[k] = takes ? row_pos + 1 - pos : 0;
+          scale[k] = row_factor * e.k_scale;
+        }
+        tensor_wait(s[0]);
+        tensor_wait(s[1]);
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        barrier_arrive(&sm.taken);
+        float best = -infinity();
+        bool any[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float* const x = &s[k >> 1][(k & 1) * 16];
+          any[k] = __any_sync(~0u, seen[k] > 0);
+          if (!any[k]) continue;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] *= scale[k];
+          if (!__all_sync(~0u, seen[k] >= 16)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = i < seen[k] ? x[i] : -infinity();
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) best = fmaxf(best, x[i]);
+        }
+        float by = 1.f;
+        const bool raise = best > m + kSlack;
+        const bool some = __any_sync(~0u, raise);
+        if (raise) {
+          by = m == -infinity() ? 0.f : exp2_fast(m - best);
+          m = best;
+          l *= by;
+        }
+        const float base = m == -infinity() ? 0.f : m;
+        uint32_t p[32];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float* const x = &s[k >> 1][(k & 1) * 16];
+          if (any[k]) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              x[i] = exp2_fast(x[i] - base);
+              l += x[i];
+            }
+            const Entry& e = sm.entry[(block << per_block_shift) + (k * 16 >> part_tokens_shift)];
+            const float part = e.v_part;
+            if (part != 1.f && e.offset >= 0) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] *= part;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[k * 8 + i] = pack2<true>(x[2 * i], x[2 * i + 1]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[k * 8 + i] = 0u;
+          }
+        }
+        if (n > 0) {  // P and O are free
+          ok = barrier_wait(&sm.added, (n - 1) & 1, failed);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (some) scale_outputs(by);
+        }
+        tensor_store32(tensor + lane_base + kP, p);
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        barrier_arrive(&sm.weighed);
+      }
+    } else if (tid < kRows + kConvert) {
+      // ---- codes to operands: thread i has pieces i, i + 128, ... of 16 codes ----
+      constexpr int kPieces = kBlock * D / 16 / kConvert, kTokenPieces = D / 16;
+      const int thread = tid - kRows;
+      uint4 k[kPieces], v[kPieces];
+      const auto load = [&](int block, const uint8_t* codes, uint4 (&x)[kPieces]) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int piece = thread + i * kConvert, token = piece / kTokenPieces;
+          const int in_part = token & ((1 << part_tokens_shift) - 1);
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (block >= blocks) continue;
+          const Entry& e = sm.entry[(block << per_block_shift) + (token >> part_tokens_shift)];
+          if (e.offset >= 0 && e.pos + in_part < most)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(codes + e.offset + in_part * D +
+                                                        piece % kTokenPieces * 16));
+        }
+      };
+      // 16 codes are two pieces of 8 channels of a line; lanes of the second line write theirs
+      // in the other order, so that a quarter of a warp touches every bank once
+      const auto place = [&](uint8_t (&lines)[kLines][kBlock * 128], int i, const uint4& x,
+                             uint32_t power) {
+        const int piece = thread + i * kConvert, token = piece / kTokenPieces;
+        const int channel = piece % kTokenPieces * 16, line = channel / 64;
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t h[8];
+        const __half2 by = *reinterpret_cast<const __half2*>(&power);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[j] = codes_to_half2((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
+          if (power != 0x3C003C00u) {
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[j]), by);
+            h[j] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+        }
+        const int at = channel % 64 / 8;
+        uint8_t* const to = &lines[line][token * 128];
+        const uint4 first = make_uint4(h[0], h[1], h[2], h[3]);
+        const uint4 second = make_uint4(h[4], h[5], h[6], h[7]);
+        const bool swap = (line & 1) != 0;
+        *reinterpret_cast<uint4*>(to + (((at + swap) ^ (token & 7)) << 4)) =
+            swap ? second : first;
+        *reinterpret_cast<uint4*>(to + (((at + !swap) ^ (token & 7)) << 4)) =
+            swap ? first : second;
+      };
+      load(0, c.k, k);
+      load(0, c.v, v);
+      for (int block = 0; block < blocks; ++block) {
+        const int n = done + block, buffer = n & 1;
+        if (n >= 2) ok = ok && barrier_wait(&sm.k_free[buffer], ((n >> 1) - 1) & 1, failed);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) place(sm.k[buffer], i, k[i], 0x3C003C00u);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        barrier_arrive(&sm.k_full[buffer]);
+        load(block + 1, c.k, k);
+        if (n >= 2) ok = barrier_wait(&sm.v_free[buffer], ((n >> 1) - 1) & 1, failed);
+        if (!ok) break;
+        uint32_t bad = 0u;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          const int token = (thread + i * kConvert) / kTokenPieces;
+          const Entry& e = sm.entry[(block << per_block_shift) + (token >> part_tokens_shift)];
+          place(sm.v[buffer], i, v[i], e.offset >= 0 ? e.v_power : 0x3C003C00u);
+          bad |= nan_codes(v[i].x) | nan_codes(v[i].y) | nan_codes(v[i].z) | nan_codes(v[i].w);
+        }
+        if (bad != 0u) sm.again = 1;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        barrier_arrive(&sm.v_full[buffer]);
+        load(block + 1, c.v, v);
+      }
+    } else if (lane == 0) {
+      // ---- products ----
+      constexpr uint32_t kScores = 1u << 4 | (kBlock / 8) << 17 | (kRows / 16) << 24;
+      constexpr uint32_t kOutputs = 1u << 4 | 1u << 16 | (D / 8) << 17 | (kRows / 16) << 24;
+      const auto outputs = [&](int n) {
+        const int buffer = n & 1;
+        ok = ok && barrier_wait(&sm.v_full[buffer], (n >> 1) & 1, failed);
+        ok = ok && barrier_wait(&sm.weighed, n & 1, failed);
+        if (!ok) return;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint64_t v = operand_across(shared_address(sm.v[buffer][0]), kBlock * 128);
+#pragma unroll
+        for (int k = 0; k < kBlock / 16; ++k)  // 16 tokens: 8 columns of P, 2 KB of V
+          tensor_mma_from(tensor, tensor + kP + 8 * k, v + 128 * k, kOutputs, n > 0 || k > 0);
+        tensor_commit(&sm.v_free[buffer]);
+        tensor_commit(&sm.added);
+      };
+      for (int block = 0; block < blocks && ok; ++block) {
+        const int n = done + block, buffer = n & 1;
+        ok = barrier_wait(&sm.k_full[buffer], (n >> 1) & 1, failed);
+        if (n > 0) ok = ok && barrier_wait(&sm.taken, (n - 1) & 1, failed);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+        for (int line = 0; line < kLines; ++line) {
+          const uint64_t q = operand(shared_address(sm.q[line]));
+          const uint64_t k = operand(shared_address(sm.k[buffer][line]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            tensor_mma(tensor + kS, q + 2 * i, k + 2 * i, kScores, line > 0 || i > 0);
+        }
+        tensor_commit(&sm.k_free[buffer]);
+        tensor_commit(&sm.scored);
+        if (block > 0) outputs(n - 1);
+      }
+      if (ok) outputs(done + blocks - 1);
+    }
+    __syncwarp();
+    done += blocks;
+  }
+
+  // ---- outputs ----
+  if (tid < kRows) {
+    if (done > 0) {
+      ok = ok && barrier_wait(&sm.added, (done - 1) & 1, failed);
+      ok = __all_sync(~0u, ok);
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    const float by = l == 0.f ? 0.f : exp2f((float)(done > 0 ? sm.unit : 0)) / l;
+    uint16_t* const at =
+        static_cast<uint16_t*>(a.out.data) + (row0 + row_token) * a.out.token_stride +
+        ((int64_t)head * a.group + head0 + row - row_token * heads) * a.out.head_stride;
+#pragma unroll 1
+    for (int i = 0; i < D; i += 32) {
+      float v[32];
+      if (done > 0) {
+        tensor_load32(tensor + lane_base + i, v);
+        tensor_wait(v);
+      }
+      if (row < live && ok) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float x = l == 0.f ? 0.f : v[j * 8 + k * 2] * by;
+            const float y = l == 0.f ? 0.f : v[j * 8 + k * 2 + 1] * by;
+            w[k] = c.fp16 ? pack2<true>(x, y) : pack2<false>(x, y);
+          }
+          *reinterpret_cast<uint4*>(at + i + j * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+  if (tid == kIssueWarp * 32) {
+    // what was issued ends before the shared memory and the tensor memory go
+    int none = 0;
+    tensor_commit(&sm.drained);
+    barrier_wait(&sm.drained, 0, &none);
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  // tiles that the kernel behind this one has to do
+  if (tid < tokens)
+    a.again[((row0 + tid) * c.heads + head) * gridDim.z + blockIdx.z] =
+        sm.again != 0 || sm.failed != 0;
+  if (warp == kIssueWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tensor),
+                 "r"(kTensorColumns)
+                 : "memory");
+}
+
+template <int D>
+int launch(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a, cudaStream_t stream) {
+  const size_t smem =
+      sizeof(Shared<D>) + 1024 + (a.blocks != nullptr ? (size_t)b.width * 4 : 0);
+  if (cudaFuncSetAttribute(prompt_attention_kernel<D>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)smem) != cudaSuccess) {
+    cudaGetLastError();
+    return EXACT_TOPK_ERR_CUDA;
+  }
+  const dim3 grid((unsigned)slot_count(b, a.prompt_tokens, 1), (unsigned)c.heads,
+                  (unsigned)((a.group + a.prompt_heads - 1) / a.prompt_heads));
+  prompt_attention_kernel<D><<<grid, kThreads, smem, stream>>>(c, b, a);
+  return launch_status();
+}
+
+}  // namespace
+
+int launch_prompt_attention(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a,
+                            cudaStream_t stream) {
+  return c.dim == 128 ? launch<128>(c, b, a, stream) : launch<64>(c, b, a, stream);
+}
+
+}  // namespace etk

@@ -153,16 +153,21 @@ typedef struct exact_topk_attention_plan {
   int32_t tile_heads;   /* heads of a tile (of one key head) */
   int32_t workers;      /* CTAs that share the work */
   int32_t min_units;    /* least pages a CTA takes at a time */
+  int32_t prompt_tokens; /* tokens and heads of the tiles of the prompt's kernel, which */
+  int32_t prompt_heads;  /* runs first where there are enough rows; 0: it does not run */
   uint64_t counter_bytes;
   uint64_t workspace_bytes;
 } exact_topk_attention_plan;
 
-/* Pure host logic. single_rows: nonzero for batches without q_start.
+/* Pure host logic. single_rows: nonzero for batches without q_start. prompt: whether the
+ * prompt's kernel runs, -1 the planner's choice, 0 no, 1 yes (BAD_PLAN where it cannot: lists
+ * over a table of more than 24576 pages).
  * num_tokens * q_heads must stay below 2^31.
- * Errors: NULL_POINTER, BAD_CACHE (page_size, head_dim), BAD_BATCH, BAD_HEADS, BAD_K. */
+ * Errors: NULL_POINTER, BAD_CACHE (page_size, head_dim), BAD_BATCH, BAD_HEADS, BAD_K, BAD_PLAN. */
 int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_rows, int q_heads,
                                    int kv_heads, int head_dim, int page_size, int table_width,
-                                   int num_blocks, const exact_topk_device_info* info,
+                                   int num_blocks, int prompt,
+                                   const exact_topk_device_info* info,
                                    exact_topk_attention_plan* plan);
 
 /* out[t][head] = sum_p softmax_p(scale * q[t][head] . k[p]) v[p] over the tokens p at

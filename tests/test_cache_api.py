@@ -58,6 +58,23 @@ def test_plan_refusals():
             etk.make_attention_plan(**{**good, **bad})
         assert e.value.code == code, bad
     etk.make_attention_plan(**{**good, "table_width": 131073, "num_blocks": 0})
+    with pytest.raises(etk.ExactTopKError) as e:
+        etk.make_attention_plan(**{**good, "table_width": 24577, "prompt": 1})
+    assert e.value.code == -7
+
+
+@pytest.mark.parametrize("tokens,seqs,q_heads,heads,blocks,width,prompt,expect", [
+    (4096, 1, 16, 2, 32, 2048, -1, (16, 8)), (4096, 1, 16, 2, 0, 2048, -1, (16, 8)), (4096, 1, 16, 2, 32, 2048, 0, (0, 0)),
+    (4096, 1, 16, 2, 32, 30000, -1, (0, 0)), (100, 1, 16, 2, 32, 2048, -1, (0, 0)), (100, 1, 16, 2, 32, 2048, 1, (16, 8)),
+    (6400, 1, 2, 2, 0, 100, -1, (32, 1)), (4096, 4096, 16, 2, 0, 100, -1, (0, 0)), (2000, 1, 260, 1, 0, 100, -1, (1, 128)),
+    (512, 64, 32, 4, 0, 100, -1, (0, 0)),
+])
+def test_plan_of_prompts(tokens, seqs, q_heads, heads, blocks, width, prompt, expect):
+    p = etk.make_attention_plan(tokens, seqs, q_heads, heads, 128, 64, width, blocks, tokens == seqs, GB300, prompt)
+    assert (p.prompt_tokens, p.prompt_heads) == expect
+    group = q_heads // heads
+    flags = tokens * heads * -(-group // p.prompt_heads) if expect[0] else 0
+    assert p.workspace_bytes >= p.workers * 2 * p.columns * 130 * 4 + flags
 
 
 def fake(i):
@@ -151,10 +168,12 @@ def test_attention_refuses_bad_plans_and_buffers():
     assert call(blocks=fake(14)) == -7
     for bad in (dict(scale=math.inf), dict(scale=math.nan), dict(kv_heads=1), dict(head_dim=64), dict(page_size=32), dict(table_width=4),
                 dict(num_seqs=3), dict(columns=24), dict(tile_tokens=0), dict(tile_tokens=9), dict(tile_heads=0), dict(tile_heads=5),
-                dict(tile_tokens=3), dict(workers=0), dict(workers=1 << 20), dict(min_units=0)):
+                dict(tile_tokens=3), dict(prompt_tokens=33, prompt_heads=1), dict(prompt_tokens=-1),
+                dict(prompt_tokens=1, prompt_heads=0), dict(prompt_tokens=1, prompt_heads=3), dict(workers=609), dict(workers=0), dict(workers=1 << 20), dict(min_units=0)):
         assert call(**bad) == -7, bad
     # a plan whose sizes were made smaller by hand does not get past the buffers' checks
     assert call(counter_bytes=16) == -4 and call(workspace_bytes=16) == -5
+    assert call(prompt_tokens=8, prompt_heads=4) == -5  # no room for the marks
     assert call(q_heads=9) == -11
 
 

@@ -199,12 +199,12 @@ def test_scores_of_a_prompt(heads, group, page, dim, dtype):
 
 # ---- attention ----
 
-def check_attention(tensors, batch, q, blocks=None, scale=None, single=False, strided=False, objects=None):
+def check_attention(tensors, batch, q, blocks=None, scale=None, single=False, strided=False, **overrides):
     cache, b = device_cache(tensors), device_batch(batch, single)
     T, QH, D = q.shape
     heads = cache.kv_heads
     K = 0 if blocks is None else blocks.shape[1]
-    a = etk.CacheAttention(cache, b.num_seqs, T, QH, b.table_width, num_blocks=K)
+    a = etk.CacheAttention(cache, b.num_seqs, T, QH, b.table_width, num_blocks=K, **overrides)
     out = rows_to_device(torch.full_like(q, MARK), strided)
     got = a(rows_to_device(q, strided), b, blocks=None if blocks is None else blocks.cuda(), out=out, scale=scale)
     assert got is out
@@ -420,6 +420,94 @@ def test_a_cache_whose_offsets_pass_32_bits():
     want, ke, size = ref.scores(part, (table - low, kv_len, one), q, 0, 0, MARK)
     seen = want != MARK
     assert ((scores.cpu().double() - want).abs()[seen] <= (2 * dim * 2.0 ** -23 * size)[seen]).all()
+
+
+# ---- the prompt's kernel, on tiles that fill it and ones that do not ----
+
+PROMPTS = [([1], [1]), ([90, 0, 2], [40, 2, 2]), ([700, 64], [130, 17]), ([200, 5], [200, 9])]
+
+
+@pytest.mark.parametrize("lens,new", PROMPTS)
+@pytest.mark.parametrize("page,dim,heads,group,dtype", LAYOUTS + [(64, 128, 1, 130, BF16), (32, 64, 2, 7, FP16)])
+def test_prompt_over_the_whole_cache(lens, new, page, dim, heads, group, dtype):
+    tensors, batch = ref.make(130, lens, new, heads, page, dim, dtype)
+    q = ref.rows(131, sum(new), heads * group, dim, dtype, 3.0)
+    check_attention(tensors, batch, q, strided=len(lens) % 2 == 1, prompt=1)
+
+
+@pytest.mark.parametrize("lens,new", PROMPTS)
+@pytest.mark.parametrize("page,dim,heads,group,dtype", LAYOUTS + [(32, 64, 2, 7, FP16)])
+def test_prompt_over_listed_pages(lens, new, page, dim, heads, group, dtype):
+    tensors, batch = ref.make(132, lens, new, heads, page, dim, dtype)
+    T, K = sum(new), 9
+    q = ref.rows(133, T, heads * group, dim, dtype, 3.0)
+    most = max(1, -(-max(lens) // page))
+    blocks = torch.randint(-1, most + 1, (T * heads, K), generator=torch.Generator().manual_seed(134), dtype=torch.int32)
+    blocks[0] = -1
+    blocks[-1, 0], blocks[-1, 1] = 2 ** 31 - 1, -2 ** 31
+    check_attention(tensors, batch, q, blocks, prompt=1)
+
+
+@pytest.mark.parametrize("page,dim,dtype", [(16, 64, BF16), (64, 128, FP16)])
+def test_prompt_passes_the_parts_held_at_a_time(page, dim, dtype):
+    """More parts of pages than the kernel holds at once, with scales that grow along the sequence."""
+    lens, new = [page * 300 + 7], [5]
+    tensors, batch = ref.make(135, lens, new, 1, page, dim, dtype)
+    for j in range(301):
+        tensors[3][batch[0][0, j]] = 2.0 ** (j // 60 - 8)
+    q = ref.rows(136, 5, 3, dim, dtype, 3.0)
+    check_attention(tensors, batch, q, prompt=1)
+    blocks = torch.stack([torch.randperm(301, generator=torch.Generator().manual_seed(k))[:260] for k in range(5)]).to(torch.int32)
+    check_attention(tensors, batch, q, blocks, prompt=1)
+
+
+def test_prompt_leaves_what_it_cannot_do_to_the_other_kernel():
+    """NaN among the values, scales far apart and of no power of two, absent pages: the same results."""
+    lens, new, page, dim = [400, 300], [40, 20], 16, 64
+    for case in range(4):
+        tensors, batch = ref.make(137 + case, lens, new, 2, page, dim, BF16, spread=0 if case == 2 else 4)
+        if case == 0:
+            for position in (399, 390, 370, 10):
+                tensors[1].view(torch.uint8)[batch[0][0, position // page].long(), 1, position % page, 7] = 0x7F
+        elif case == 1:
+            tensors[3][batch[0][1, 3]] = 2.0 ** 20
+            tensors[3][batch[0][0, 2]] = 2.0 ** -30
+        elif case == 2:
+            g = torch.Generator().manual_seed(5)
+            for t in tensors[2:4]:
+                t.mul_(1 + torch.rand(t.shape, generator=g))
+        else:
+            batch[0][0, 4], batch[0][1, :] = -1, 10 ** 6
+        q = ref.rows(141, 60, 16, dim, BF16, 2.0)
+        check_attention(tensors, batch, q, prompt=1)
+        blocks = torch.randint(-1, 25, (120, 6), generator=torch.Generator().manual_seed(142), dtype=torch.int32)
+        check_attention(tensors, batch, q, blocks, prompt=1)
+
+
+@pytest.mark.parametrize("size", [1e-30, 30.0, 3000.0])
+def test_prompt_with_queries_of_any_size(size):
+    lens, new = [300, 64], [20, 9]
+    tensors, batch = ref.make(143, lens, new, 2, 32, 128, BF16)
+    q = ref.rows(144, 29, 8, 128, BF16, 1.0) * size
+    check_attention(tensors, batch, q, scale=min(1.0, 0.05 / size), prompt=1)
+    check_attention(tensors, batch, q, scale=-min(1.0, 0.05 / size), prompt=1)
+
+
+def test_the_planner_takes_the_prompts_kernel_and_both_agree():
+    lens, new, heads, group, page, dim = [4000], [1300], 2, 8, 64, 128
+    tensors, batch = ref.make(145, lens, new, heads, page, dim, BF16)
+    cache, b = device_cache(tensors), device_batch(batch)
+    q = ref.rows(146, 1300, heads * group, dim, BF16, 3.0).cuda()
+    g = torch.Generator().manual_seed(147)
+    score = torch.rand(1, heads, 43, generator=g) + 0.3 * torch.rand(1300, heads, 43, generator=g)
+    blocks = score.topk(12, -1).indices.to(torch.int32).reshape(-1, 12).cuda()
+    for K, lists in ((0, None), (12, blocks)):
+        objects = [etk.CacheAttention(cache, 1, 1300, heads * group, b.table_width, num_blocks=K, prompt=p) for p in (-1, 0)]
+        assert objects[0].plan.prompt_tokens == 16 and objects[1].plan.prompt_tokens == 0
+        x, y = (a(q, b, blocks=lists).double() for a in objects)
+        # two roundings to bf16 (2^-9 of the value each way) and the two kernels' probabilities in FP16
+        bound = float(tensors[1].float().nan_to_num(0.0).abs().max()) * float(tensors[3].max())
+        assert ((x - y).abs() <= 2.0 ** -8 * y.abs() + 2.0 ** -9 * bound).all()
 
 
 # ---- together, streams, graphs ----
