@@ -298,6 +298,23 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
   const int g = lane >> 2, q4 = lane & 3;
   const bool listed = a.blocks != nullptr;
 
+  // Behind the prompt's kernel: nothing to do, most of the time. Marks of up to 64 KB are looked
+  // over at once, and each tile's again below.
+  if (a.again != nullptr) {
+    const int64_t marks_count = (b.q_start == nullptr ? b.num_seqs : clamp_row(b, b.num_seqs)) *
+                                c.heads * ((a.group + a.prompt_heads - 1) / a.prompt_heads);
+    if (marks_count <= 65536) {
+      uint32_t any = 0u;
+      int i = tid * 16;
+      for (; i + 16 <= marks_count; i += kThreads * 16) {
+        const uint4 w = *reinterpret_cast<const uint4*>(a.again + i);
+        any |= w.x | w.y | w.z | w.w;
+      }
+      for (; i < marks_count; ++i) any |= a.again[i];
+      if (!__syncthreads_or(any != 0u)) return;
+    }
+  }
+
   // ---- the line of units: pages over the whole cache, tiles for listed pages ----
   const bool even = listed && b.q_start == nullptr;  // every sequence has one row
   int64_t total = (int64_t)b.num_seqs * c.heads * a.group_parts;

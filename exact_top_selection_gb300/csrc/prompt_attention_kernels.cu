@@ -52,6 +52,30 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 x, float y, float z) {
+  const float2 yy = make_float2(y, y), zz = make_float2(z, z);
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<const uint64_t&>(x)), "l"(reinterpret_cast<const uint64_t&>(yy)),
+        "l"(reinterpret_cast<const uint64_t&>(zz)));
+  return r;
+}
+
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(r))
+      : "l"(reinterpret_cast<const uint64_t&>(x)), "l"(reinterpret_cast<const uint64_t&>(y)));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
@@ -105,7 +129,7 @@ struct Shared {
   Entry entry[kEntries];
   float factor[kRows];
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
-  uint64_t scored, taken, weighed, added, drained;
+  uint64_t scored[2], weighed[2], added[2], drained;
   uint32_t tensor;
   int scan[kIssueWarp];
   int failed, again, unit;
@@ -116,7 +140,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     prompt_attention_kernel(CacheArgs c, BatchArgs b, AttentionArgs a) {
   using Smem = Shared<D>;
   constexpr int kLines = D / 64;
-  constexpr uint32_t kS = 128, kP = 192, kTensorColumns = 256;  // O, S, P in tensor memory
+  // tensor memory: O, then two blocks' S, each of which its P replaces
+  constexpr uint32_t kS = 128, kTensorColumns = 256;
   extern __shared__ unsigned char raw[];
   Smem& sm = *reinterpret_cast<Smem*>(
       raw + ((1024u - (shared_address(raw) & 1023u)) & 1023u));
@@ -146,11 +171,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       barrier_init(&sm.v_full[i], kConvert);
       barrier_init(&sm.k_free[i], 1);
       barrier_init(&sm.v_free[i], 1);
+      barrier_init(&sm.scored[i], 1);
+      barrier_init(&sm.weighed[i], kRows);
+      barrier_init(&sm.added[i], 1);
     }
-    barrier_init(&sm.scored, 1);
-    barrier_init(&sm.taken, kRows);
-    barrier_init(&sm.weighed, kRows);
-    barrier_init(&sm.added, 1);
     barrier_init(&sm.drained, 1);
     sm.failed = 0;
     sm.again = 0;
@@ -211,7 +235,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (e == 128 || top == 0.f) e = 8;
         int up = 8 - e;
         up = up < -120 ? -120 : (up > 120 ? 120 : up);
-        const float by = __uint_as_float((uint32_t)(up + 127) << 23);
+        // the scale's sign goes into the queries, so that a row's largest score is its largest
+        // product
+        const float by = copysignf(__uint_as_float((uint32_t)(up + 127) << 23), a.scale_log2);
         const int channel = lane * kEach, line = channel / 64, piece = channel % 64 / 8;
         uint32_t* const to = reinterpret_cast<uint32_t*>(
             &sm.q[line][row * 128 + ((piece ^ (row & 7)) << 4) + channel % 8 * 2]);
@@ -219,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < kEach / 2; ++i) to[i] = pack2<true>(x[i].x * by, x[i].y * by);
         if (lane == 0)
           sm.factor[row] =
-              row < live ? __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2 : 0.f;
+              row < live ? __uint_as_float((uint32_t)(127 - up) << 23) * fabsf(a.scale_log2) : 0.f;
       }
     }
   }
@@ -265,6 +291,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   float m = -infinity(), l = 0.f;
   int done = 0;  // blocks so far, the same for every role
   bool ok = true;
+
+  // Block n's barriers are those of its parity, so that who waits for one may be a block behind:
+  // all that is known of the others then is that block n - 2 is done.
+  const auto was_added = [&](int n) {
+    return barrier_wait(&sm.added[n & 1], (n >> 1) & 1, failed);
+  };
 
   // O times a factor for each row
   const auto scale_outputs = [&](float by) {
@@ -350,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     // O so far is in the unit before
     if (tid < kRows && done > 0 && unit > unit_before) {
-      ok = ok && barrier_wait(&sm.added, (done - 1) & 1, failed);
+      ok = ok && was_added(done - 1);
       ok = __all_sync(~0u, ok);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       scale_outputs(exp2f((float)(unit_before - unit)));
@@ -362,16 +394,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       // ---- softmax: a row a thread ----
       for (int block = 0; block < blocks; ++block) {
         const int n = done + block;
-        ok = ok && barrier_wait(&sm.scored, n & 1, failed);
+        ok = ok && barrier_wait(&sm.scored[n & 1], (n >> 1) & 1, failed);
         ok = __all_sync(~0u, ok);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        float s[2][32];
-        tensor_load32(tensor + lane_base + kS, s[0]);
-        tensor_load32(tensor + lane_base + kS + 32, s[1]);
+        const uint32_t from = tensor + lane_base + kS + (n & 1) * kBlock;
+        float s[32];
+        tensor_load32(from, s);
         // what this row sees of each 16 tokens
         int seen[4];
-        float scale[4];
+        float scale[4], v_part[4];
+        bool any[4], all[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int token = k * 16;
@@ -380,27 +413,40 @@ __global__ void __launch_bounds__(kThreads, 2)
           const bool takes = row_pos >= 0 && (e.members >> row_token & 1u) != 0u;
           seen[k] = takes ? row_pos + 1 - pos : 0;
           scale[k] = row_factor * e.k_scale;
-        }
-        tensor_wait(s[0]);
-        tensor_wait(s[1]);
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        barrier_arrive(&sm.taken);
-        float best = -infinity();
-        bool any[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float* const x = &s[k >> 1][(k & 1) * 16];
+          v_part[k] = e.offset >= 0 ? e.v_part : 1.f;
           any[k] = __any_sync(~0u, seen[k] > 0);
-          if (!any[k]) continue;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] *= scale[k];
-          if (!__all_sync(~0u, seen[k] >= 16)) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = i < seen[k] ? x[i] : -infinity();
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) best = fmaxf(best, x[i]);
+          all[k] = __all_sync(~0u, seen[k] >= 16);
         }
+        // The largest score, of both halves; then the probabilities, of the second half and of
+        // the first, which is read again: a row's 64 scores at once would not fit the
+        // registers. Sixteen tokens are left out where no row of the warp sees one, and
+        // masked where some row does not see all of them.
+        float best = -infinity();
+        const auto largest = [&](int k, const float* x) {
+          if (!any[k]) return;
+          float high;
+          if (all[k]) {
+            high = max3(x[0], x[1], x[2]);
+            float other = max3(x[3], x[4], x[5]);
+            high = max3(high, x[6], x[7]);
+            other = max3(other, x[8], x[9]);
+            high = max3(high, x[10], x[11]);
+            other = max3(other, x[12], x[13]);
+            high = fmaxf(max3(high, x[14], x[15]), other);
+          } else {
+            high = -infinity();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) high = fmaxf(high, i < seen[k] ? x[i] : -infinity());
+          }
+          best = fmaxf(best, high * scale[k]);  // (-inf * 0, of a row that sees none, is ignored)
+        };
+        tensor_wait(s);
+        largest(0, s);
+        largest(1, s + 16);
+        tensor_load32(from + 32, s);
+        tensor_wait(s);
+        largest(2, s);
+        largest(3, s + 16);
         float by = 1.f;
         const bool raise = best > m + kSlack;
         const bool some = __any_sync(~0u, raise);
@@ -411,83 +457,108 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         const float base = m == -infinity() ? 0.f : m;
         uint32_t p[32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float* const x = &s[k >> 1][(k & 1) * 16];
-          if (any[k]) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              x[i] = exp2_fast(x[i] - base);
-              l += x[i];
-            }
-            const Entry& e = sm.entry[(block << per_block_shift) + (k * 16 >> part_tokens_shift)];
-            const float part = e.v_part;
-            if (part != 1.f && e.offset >= 0) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) x[i] *= part;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[k * 8 + i] = pack2<true>(x[2 * i], x[2 * i + 1]);
-          } else {
+        float2 sum = make_float2(0.f, 0.f);
+        const auto weigh = [&](int k, const float* x) {
+          if (!any[k]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[k * 8 + i] = 0u;
+            return;
           }
-        }
-        if (n > 0) {  // P and O are free
-          ok = barrier_wait(&sm.added, (n - 1) & 1, failed);
+          float2 y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            y[i] = fma2(make_float2(x[2 * i], x[2 * i + 1]), scale[k], -base);
+          if (!all[k]) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              y[i].x = 2 * i < seen[k] ? y[i].x : -infinity();
+              y[i].y = 2 * i + 1 < seen[k] ? y[i].y : -infinity();
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y[i].x = exp2_fast(y[i].x);
+            y[i].y = exp2_fast(y[i].y);
+            sum = add2(sum, y[i]);
+          }
+          if (v_part[k] != 1.f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              y[i].x *= v_part[k];
+              y[i].y *= v_part[k];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[k * 8 + i] = pack2<true>(y[i].x, y[i].y);
+        };
+        weigh(2, s);
+        weigh(3, s + 16);
+        tensor_load32(from, s);
+        tensor_wait(s);
+        weigh(0, s);
+        weigh(1, s + 16);
+        l += sum.x + sum.y;
+        if (some && n > 0) {  // O is in place up to the block before
+          ok = was_added(n - 1);
           ok = __all_sync(~0u, ok);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (some) scale_outputs(by);
+          scale_outputs(by);
         }
-        tensor_store32(tensor + lane_base + kP, p);
+        tensor_store32(from, p);
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        barrier_arrive(&sm.weighed);
+        barrier_arrive(&sm.weighed[n & 1]);  // a warp may be a block ahead of another
       }
     } else if (tid < kRows + kConvert) {
-      // ---- codes to operands: thread i has pieces i, i + 128, ... of 16 codes ----
-      constexpr int kPieces = kBlock * D / 16 / kConvert, kTokenPieces = D / 16;
-      const int thread = tid - kRows;
-      uint4 k[kPieces], v[kPieces];
-      const auto load = [&](int block, const uint8_t* codes, uint4 (&x)[kPieces]) {
+      // ---- codes to operands ----
+      // A warp has 16 tokens of the block, 8 at a time: 4 lanes with 16 codes each for a line of 64
+      // channels. Of a token's line they write every other piece of 16 bytes, of an odd token's
+      // the other ones, so that a quarter of a warp touches every bank once.
+      const int first = (warp - kRows / 32) * 16 + (lane >> 2), chunk = lane & 3;
+      uint4 k[2][kLines], v[2][kLines];  // tokens first, first + 8
+      const auto entry_of = [&](int block, int i) -> const Entry& {
+        return sm.entry[(block << per_block_shift) + ((first + i * 8) >> part_tokens_shift)];
+      };
+      const auto load = [&](int block, const uint8_t* codes, uint4 (&x)[2][kLines]) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int piece = thread + i * kConvert, token = piece / kTokenPieces;
-          const int in_part = token & ((1 << part_tokens_shift) - 1);
-          x[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int line = 0; line < kLines; ++line) x[i][line] = make_uint4(0u, 0u, 0u, 0u);
           if (block >= blocks) continue;
-          const Entry& e = sm.entry[(block << per_block_shift) + (token >> part_tokens_shift)];
-          if (e.offset >= 0 && e.pos + in_part < most)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(codes + e.offset + in_part * D +
-                                                        piece % kTokenPieces * 16));
+          const Entry& e = entry_of(block, i);
+          const int in_part = (first + i * 8) & ((1 << part_tokens_shift) - 1);
+          if (e.offset < 0 || e.pos + in_part >= most) continue;
+          const uint8_t* const at = codes + e.offset + in_part * D + chunk * 16;
+#pragma unroll
+          for (int line = 0; line < kLines; ++line)
+            x[i][line] = __ldg(reinterpret_cast<const uint4*>(at + line * 64));
         }
       };
-      // 16 codes are two pieces of 8 channels of a line; lanes of the second line write theirs
-      // in the other order, so that a quarter of a warp touches every bank once
-      const auto place = [&](uint8_t (&lines)[kLines][kBlock * 128], int i, const uint4& x,
-                             uint32_t power) {
-        const int piece = thread + i * kConvert, token = piece / kTokenPieces;
-        const int channel = piece % kTokenPieces * 16, line = channel / 64;
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t h[8];
-        const __half2 by = *reinterpret_cast<const __half2*>(&power);
+      const int place0 = first * 128 + (((chunk * 2) ^ (first & 7)) << 4);  // + 8 tokens: 1024
+      const auto place = [&](uint8_t (&lines)[kLines][kBlock * 128], int i,
+                             const uint4 (&x)[kLines], uint32_t power) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[j] = codes_to_half2((uint16_t)(w[j >> 1] >> (16 * (j & 1))));
-          if (power != 0x3C003C00u) {
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h[j]), by);
-            h[j] = *reinterpret_cast<const uint32_t*>(&y);
+        for (int line = 0; line < kLines; ++line) {
+          const uint32_t w[4] = {x[line].x, x[line].y, x[line].z, x[line].w};
+          uint32_t y[8];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            y[2 * n] = codes_to_half2((uint16_t)w[n]);
+            y[2 * n + 1] = codes_to_half2((uint16_t)(w[n] >> 16));
           }
+          if (power != 0x3C003C00u) {
+            const __half2 by = *reinterpret_cast<const __half2*>(&power);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[n]), by);
+              y[n] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+          }
+          uint8_t* const to = &lines[line][0];
+          *reinterpret_cast<uint4*>(to + place0 + i * 1024) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(to + (place0 ^ 16) + i * 1024) =
+              make_uint4(y[4], y[5], y[6], y[7]);
         }
-        const int at = channel % 64 / 8;
-        uint8_t* const to = &lines[line][token * 128];
-        const uint4 first = make_uint4(h[0], h[1], h[2], h[3]);
-        const uint4 second = make_uint4(h[4], h[5], h[6], h[7]);
-        const bool swap = (line & 1) != 0;
-        *reinterpret_cast<uint4*>(to + (((at + swap) ^ (token & 7)) << 4)) =
-            swap ? second : first;
-        *reinterpret_cast<uint4*>(to + (((at + !swap) ^ (token & 7)) << 4)) =
-            swap ? first : second;
       };
       load(0, c.k, k);
       load(0, c.v, v);
@@ -496,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (n >= 2) ok = ok && barrier_wait(&sm.k_free[buffer], ((n >> 1) - 1) & 1, failed);
         if (!ok) break;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) place(sm.k[buffer], i, k[i], 0x3C003C00u);
+        for (int i = 0; i < 2; ++i) place(sm.k[buffer], i, k[i], 0x3C003C00u);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         barrier_arrive(&sm.k_full[buffer]);
         load(block + 1, c.k, k);
@@ -504,11 +575,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!ok) break;
         uint32_t bad = 0u;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          const int token = (thread + i * kConvert) / kTokenPieces;
-          const Entry& e = sm.entry[(block << per_block_shift) + (token >> part_tokens_shift)];
+        for (int i = 0; i < 2; ++i) {
+          const Entry& e = entry_of(block, i);
           place(sm.v[buffer], i, v[i], e.offset >= 0 ? e.v_power : 0x3C003C00u);
-          bad |= nan_codes(v[i].x) | nan_codes(v[i].y) | nan_codes(v[i].z) | nan_codes(v[i].w);
+#pragma unroll
+          for (int line = 0; line < kLines; ++line)
+            bad |= nan_codes(v[i][line].x) | nan_codes(v[i][line].y) |
+                   nan_codes(v[i][line].z) | nan_codes(v[i][line].w);
         }
         if (bad != 0u) sm.again = 1;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -519,24 +592,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       // ---- products ----
       constexpr uint32_t kScores = 1u << 4 | (kBlock / 8) << 17 | (kRows / 16) << 24;
       constexpr uint32_t kOutputs = 1u << 4 | 1u << 16 | (D / 8) << 17 | (kRows / 16) << 24;
-      const auto outputs = [&](int n) {
-        const int buffer = n & 1;
-        ok = ok && barrier_wait(&sm.v_full[buffer], (n >> 1) & 1, failed);
-        ok = ok && barrier_wait(&sm.weighed, n & 1, failed);
-        if (!ok) return;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t v = operand_across(shared_address(sm.v[buffer][0]), kBlock * 128);
-#pragma unroll
-        for (int k = 0; k < kBlock / 16; ++k)  // 16 tokens: 8 columns of P, 2 KB of V
-          tensor_mma_from(tensor, tensor + kP + 8 * k, v + 128 * k, kOutputs, n > 0 || k > 0);
-        tensor_commit(&sm.v_free[buffer]);
-        tensor_commit(&sm.added);
-      };
-      for (int block = 0; block < blocks && ok; ++block) {
+      const auto scores = [&](int block) {
         const int n = done + block, buffer = n & 1;
-        ok = barrier_wait(&sm.k_full[buffer], (n >> 1) & 1, failed);
-        if (n > 0) ok = ok && barrier_wait(&sm.taken, (n - 1) & 1, failed);
-        if (!ok) break;
+        ok = ok && barrier_wait(&sm.k_full[buffer], (n >> 1) & 1, failed);
+        // the P that these scores replace has been used; a chunk's first block waits for all
+        const int used = block == 0 ? n - 1 : n - 2;
+        if (used >= 0) ok = ok && was_added(used);
+        if (!ok) return;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
         for (int line = 0; line < kLines; ++line) {
@@ -544,13 +606,29 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint64_t k = operand(shared_address(sm.k[buffer][line]));
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            tensor_mma(tensor + kS, q + 2 * i, k + 2 * i, kScores, line > 0 || i > 0);
+            tensor_mma(tensor + kS + buffer * kBlock, q + 2 * i, k + 2 * i, kScores,
+                       line > 0 || i > 0);
         }
         tensor_commit(&sm.k_free[buffer]);
-        tensor_commit(&sm.scored);
-        if (block > 0) outputs(n - 1);
+        tensor_commit(&sm.scored[buffer]);
+      };
+      scores(0);
+      if (blocks > 1) scores(1);
+      for (int block = 0; block < blocks && ok; ++block) {
+        const int n = done + block, buffer = n & 1;
+        ok = barrier_wait(&sm.v_full[buffer], (n >> 1) & 1, failed);
+        ok = ok && barrier_wait(&sm.weighed[buffer], (n >> 1) & 1, failed);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint64_t v = operand_across(shared_address(sm.v[buffer][0]), kBlock * 128);
+#pragma unroll
+        for (int k = 0; k < kBlock / 16; ++k)  // 16 tokens: 8 columns of P, 2 KB of V
+          tensor_mma_from(tensor, tensor + kS + buffer * kBlock + 8 * k, v + 128 * k, kOutputs,
+                          n > 0 || k > 0);
+        tensor_commit(&sm.v_free[buffer]);
+        tensor_commit(&sm.added[buffer]);
+        if (block + 2 < blocks) scores(block + 2);
       }
-      if (ok) outputs(done + blocks - 1);
     }
     __syncwarp();
     done += blocks;
@@ -559,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ---- outputs ----
   if (tid < kRows) {
     if (done > 0) {
-      ok = ok && barrier_wait(&sm.added, (done - 1) & 1, failed);
+      ok = ok && was_added(done - 1);
       ok = __all_sync(~0u, ok);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     }
