@@ -75,6 +75,15 @@ class AttentionPlan(ctypes.Structure):
 
 
 _bound = None
+torch = None  # imported with the first tensor that arrives here
+
+
+def _need_torch():
+    global torch
+    if torch is None:
+        import torch as module
+        torch = module
+    return torch
 
 
 def _lib():
@@ -96,29 +105,31 @@ def _lib():
     return _bound
 
 
-def _call(device, stream, fn, *args):
-    """fn(*args, stream handle) with ``device`` current; raises on an error status."""
-    import torch
+def _call(cache, stream, fn, *args):
+    """fn(*args, stream handle) with the cache's device current; raises on an error status."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream must be of {device}, got {stream.device}")
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream.cuda_stream)
+        handle = torch._C._cuda_getCurrentRawStream(cache._index)  # current_stream(...).cuda_stream
+    elif stream.device != cache.device:
+        raise ValueError(f"stream must be of {cache.device}, got {stream.device}")
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
+        handle = stream.cuda_stream
+    if torch.cuda.current_device() == cache._index:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(cache._index):
+            rc = fn(*args, handle)
     if rc != 0:
         raise _etk.ExactTopKError(rc, fn.__name__)
 
 
 def _rows(t, name, cache, heads, tokens=None):
     """Checks rows [num_tokens, heads, head_dim] and describes them."""
-    if t.dtype != cache.dtype:
+    dim = cache.head_dim
+    if t.dtype is not cache.dtype:
         raise TypeError(f"{name} must be {cache.dtype}, got {t.dtype}")
     if t.device != cache.device:
         raise ValueError(f"{name} must be on {cache.device}, got {t.device}")
-    shape, dim = t.shape, cache.head_dim
+    shape = t.shape
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim or (tokens is not None and shape[0] != tokens):
         raise ValueError(f"{name} must be [{'num_tokens' if tokens is None else tokens}, {heads}, {dim}], "
                          f"got {list(shape)}")
@@ -142,6 +153,11 @@ def _span(t):
 
 def _written(t, name, other):
     """An output's rows must share no memory with one another, nor with the rows `other`."""
+    if t.is_contiguous() and other.is_contiguous():
+        a, c = t.data_ptr(), other.data_ptr()
+        if a < c + other.nbytes and c < a + t.nbytes:
+            raise ValueError(f"{name} must not share memory with another row argument")
+        return
     if t.numel() == 0:
         return
     if not t.is_contiguous():
@@ -168,7 +184,7 @@ class KVCache:
     """
 
     def __init__(self, k, v, k_scale, v_scale, key_bounds):
-        import torch
+        _need_torch()
         if k.dim() != 4 or k.shape != v.shape:
             raise ValueError("k and v must be [num_pages, kv_heads, page_size, head_dim]")
         pages, heads, page, dim = k.shape
@@ -177,7 +193,7 @@ class KVCache:
                              f"got {list(k.shape)}")
         if key_bounds.dtype not in (torch.bfloat16, torch.float16):
             raise TypeError(f"key_bounds must be bfloat16 or float16, got {key_bounds.dtype}")
-        self.device = k.device
+        self.device, self._index = k.device, k.device.index
         if self.device.type != "cuda":
             raise ValueError(f"the cache must be on a CUDA device, got {self.device}")
         fp8 = torch.float8_e4m3fn
@@ -202,7 +218,7 @@ class KVCache:
     @classmethod
     def allocate(cls, num_pages, kv_heads, page_size, head_dim, dtype=None, device=None):
         """A new cache with every page empty (codes 0, scales 1, bounds 0)."""
-        import torch
+        _need_torch()
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         shape = (num_pages, kv_heads, page_size, head_dim)
         k, v = (torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2))
@@ -219,7 +235,7 @@ class SequenceBatch:
     may change between calls and between the replays of a captured graph."""
 
     def __init__(self, page_table, kv_len, q_start=None):
-        import torch
+        _need_torch()
         dev = page_table.device
         for t, name, ndim in ((page_table, "page_table", 2), (kv_len, "kv_len", 1), (q_start, "q_start", 1)):
             if t is not None:
@@ -256,13 +272,12 @@ def cache_write(cache, batch, k, v, stream=None):
     kr = _rows(k, "k", cache, cache.kv_heads)
     vr = _rows(v, "v", cache, cache.kv_heads, k.shape[0])
     batch._check(cache, k.shape[0])
-    _call(cache.device, stream, _lib().exact_topk_cache_write, cache._ref, batch._ref, k.shape[0], kr, vr)
+    _call(cache, stream, _lib().exact_topk_cache_write, cache._ref, batch._ref, k.shape[0], kr, vr)
 
 
 def cache_read(cache, batch, num_tokens=None, out=None, stream=None):
     """The stored rows of the batch's tokens, (k, v) [num_tokens, kv_heads, head_dim] of the cache's
     type.  ``out``: a pair of tensors to write into; rows of no sequence are left as they are there."""
-    import torch
     if out is None:
         if num_tokens is None:
             num_tokens = batch.num_seqs if batch.q_start is None else None
@@ -275,9 +290,10 @@ def cache_read(cache, batch, num_tokens=None, out=None, stream=None):
     kr = _rows(k, "out[0]", cache, cache.kv_heads, num_tokens)
     vr = _rows(v, "out[1]", cache, cache.kv_heads, k.shape[0])
     _written(k, "out[0]", v)
-    _written(v, "out[1]", k)
+    if not v.is_contiguous():
+        _written(v, "out[1]", k)
     batch._check(cache, k.shape[0])
-    _call(cache.device, stream, _lib().exact_topk_cache_read, cache._ref, batch._ref, k.shape[0], kr, vr)
+    _call(cache, stream, _lib().exact_topk_cache_read, cache._ref, batch._ref, k.shape[0], kr, vr)
     return k, v
 
 
@@ -290,7 +306,6 @@ def block_scores(cache, batch, q, keep_first=0, keep_last=0, scores=None, ke=Non
     keys (from the key bounds); the first keep_first pages and the newest keep_last get +inf.  ke int32
     [num_tokens * kv_heads] is the number of pages seen.  Entries beyond it, and rows of no sequence, are
     left as they were.  num_valid_rows, an int32 tensor of one element, gets the number of live rows."""
-    import torch
     heads = q.shape[1] if q.dim() == 3 else 0
     qr = _rows(q, "q", cache, heads)
     if heads < 1 or heads % cache.kv_heads:
@@ -321,7 +336,7 @@ def block_scores(cache, batch, q, keep_first=0, keep_last=0, scores=None, ke=Non
     if keep_first < 0 or keep_last < 0:
         raise ValueError("keep_first and keep_last must not be negative")
     most = batch.table_width
-    _call(cache.device, stream, _lib().exact_topk_block_scores, cache._ref, batch._ref, T, heads, qr,
+    _call(cache, stream, _lib().exact_topk_block_scores, cache._ref, batch._ref, T, heads, qr,
           min(int(keep_first), most), min(int(keep_last), most), scores.data_ptr(), pitch, ke.data_ptr(),
           None if num_valid_rows is None else num_valid_rows.data_ptr())
     return scores, ke
@@ -352,7 +367,6 @@ class CacheAttention:
     that may run at the same time each need an object of their own."""
 
     def __init__(self, cache, num_seqs, num_tokens, q_heads, table_width, num_blocks=0, **overrides):
-        import torch
         self.cache = cache
         with torch.cuda.device(cache.device):
             self.plan = make_attention_plan(num_tokens, num_seqs, q_heads, cache.kv_heads, cache.head_dim,
@@ -367,7 +381,6 @@ class CacheAttention:
 
     def __call__(self, q, batch, blocks=None, out=None, scale=None, stream=None):
         """out [num_tokens, q_heads, head_dim]; scale defaults to 1 / sqrt(head_dim)."""
-        import torch
         cache, plan = self.cache, self.plan
         qr = _rows(q, "q", cache, plan.q_heads, plan.num_tokens)
         batch._check(cache, plan.num_tokens)
@@ -387,7 +400,7 @@ class CacheAttention:
                 raise ValueError(f"blocks must be contiguous [{plan.num_tokens * plan.kv_heads}, {plan.num_blocks}]")
         if scale is None:
             scale = 1.0 / math.sqrt(cache.head_dim)
-        _call(cache.device, stream, _lib().exact_topk_attention_run, self._plan, cache._ref, batch._ref, qr, outr,
+        _call(cache, stream, _lib().exact_topk_attention_run, self._plan, cache._ref, batch._ref, qr, outr,
               None if blocks is None else blocks.data_ptr(), scale, *self._buffers)
         return out
 
@@ -400,7 +413,6 @@ class SparseAttention:
     selected, which must be at least as many."""
 
     def __init__(self, cache, num_seqs, num_tokens, q_heads, table_width, num_blocks, keep_first=0, keep_last=1):
-        import torch
         if keep_first < 0 or keep_last < 0 or keep_first + keep_last > num_blocks:
             raise ValueError("need 0 <= keep_first + keep_last <= num_blocks")
         if num_tokens < 1 or num_blocks < 1:
@@ -418,7 +430,6 @@ class SparseAttention:
     def __call__(self, q, batch, k=None, v=None, out=None, scale=None, stream=None):
         """Attends with q [num_tokens, q_heads, head_dim]; rows k, v of the same tokens, where given, are
         written to the cache first.  self.blocks holds the pages selected."""
-        import torch
         if (k is None) != (v is None):
             raise ValueError("k and v go together")
         if stream is None:

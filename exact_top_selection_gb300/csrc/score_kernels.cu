@@ -14,6 +14,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int64_t kPromptColumns = 64;
+constexpr int kSms = 152;
+constexpr int kStepCtas = 4;  // resident on an SM
 constexpr int kPages = 16;  // pages of a warp's step: the rows of one matrix instruction
 
 template <bool kFp16>
@@ -43,6 +45,14 @@ __device__ __forceinline__ float max_nan(float x, float y) {
 __device__ __forceinline__ float max_nan(float x, float y, float z) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 r;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+      : "l"(p));
   return r;
 }
 
@@ -96,49 +106,64 @@ __global__ void __launch_bounds__(kThreads) score_step_kernel(CacheArgs c, Batch
   const uint16_t* const bounds = static_cast<const uint16_t*>(c.bounds);
   const uint16_t* const queries = static_cast<const uint16_t*>(a.q.data);
   const int group = a.group;
+  // columns of a pass: tokens x the group's heads when they fit, else 8 heads of one token
+  const int heads = group < 8 ? group : 8;
+  const int columns = tokens * heads;
+  const int own_token = g / heads, own_head = g - own_token * heads;
+  const uint16_t* const own = queries + (rows.begin + token0 + own_token) * a.q.token_stride +
+                              ((int64_t)h * group + own_head) * a.q.head_stride + q4 * 8;
+  uint4 w[kChunks / 2];
+  const auto load_queries = [&](int head0) {
+    const bool live = g < columns && head0 + own_head < group;
+#pragma unroll
+    for (int j = 0; j < kChunks / 2; ++j)
+      w[j] = live ? __ldg(reinterpret_cast<const uint4*>(own + head0 * a.q.head_stride + j * 32))
+                  : make_uint4(0u, 0u, 0u, 0u);
+  };
+  load_queries(0);
 
-  for (int page0 = ((int)blockIdx.y * kWarps + warp) * kPages; page0 < seen;
-       page0 += (int)gridDim.y * kWarps * kPages) {
-    int id[2];
+  const int step = (int)gridDim.y * kWarps * kPages;
+  int page0 = ((int)blockIdx.y * kWarps + warp) * kPages;
+  int next[2];  // ids of the pages after these
+  const auto find = [&](int p) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int j = page0 + g + 8 * r;
-      id[r] = j < seen ? page_of(c, b, seq, j) : -1;
-    }
+    for (int r = 0; r < 2; ++r)
+      next[r] = p + g + 8 * r < seen ? page_of(c, b, seq, p + g + 8 * r) : -1;
+  };
+  find(page0);
+  for (; page0 < seen; page0 += step) {
     uint4 x[2][kChunks];
+    uint32_t absent = 0u;  // of the warp's 16 pages
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const uint16_t* const at = bounds + ((int64_t)id[r] * c.heads + h) * (2 * D) + q4 * 8;
+      const int id = next[r];
+      const uint16_t* const at = bounds + ((int64_t)id * c.heads + h) * (2 * D) + q4 * 8;
 #pragma unroll
       for (int j = 0; j < kChunks; ++j)
-        x[r][j] = id[r] >= 0 ? __ldg(reinterpret_cast<const uint4*>(at + j * 32))
-                             : make_uint4(0u, 0u, 0u, 0u);
+        x[r][j] = id >= 0 ? load_once(at + j * 32) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t lanes = __ballot_sync(~0u, id < 0);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) absent |= (lanes >> (4 * k) & 1u) << (8 * r + k);
     }
-    // columns of a pass: tokens x the group's heads when they fit, else 8 heads of one token
-    const int heads = group < 8 ? group : 8;
-    const int columns = tokens * heads;
+    find(page0 + step);
     float best = -__uint_as_float(0x7F800000u);
     for (int head0 = 0; head0 < group; head0 += heads) {
-      const bool live = g < columns && head0 + g % heads < group;
-      const uint16_t* const q =
-          queries + (rows.begin + token0 + g / heads) * a.q.token_stride +
-          ((int64_t)h * group + head0 + g % heads) * a.q.head_stride + q4 * 8;
-      float s[4] = {0.f, 0.f, 0.f, 0.f};
+      if (group > 8) load_queries(head0);
+      float s[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) {
         const bool positive = j < kChunks / 2;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (live) w = __ldg(reinterpret_cast<const uint4*>(q + (j % (kChunks / 2)) * 32));
+        const uint4& u = w[j % (kChunks / 2)];
         const uint32_t a0[4] = {x[0][j].x, x[1][j].x, x[0][j].y, x[1][j].y};
         const uint32_t a1[4] = {x[0][j].z, x[1][j].z, x[0][j].w, x[1][j].w};
-        mma<kFp16>(s, a0, clamp_sign<kFp16>(w.x, positive), clamp_sign<kFp16>(w.y, positive));
-        mma<kFp16>(s, a1, clamp_sign<kFp16>(w.z, positive), clamp_sign<kFp16>(w.w, positive));
+        mma<kFp16>(s, a0, clamp_sign<kFp16>(u.x, positive), clamp_sign<kFp16>(u.y, positive));
+        mma<kFp16>(s1, a1, clamp_sign<kFp16>(u.z, positive), clamp_sign<kFp16>(u.w, positive));
       }
       __syncwarp();
-      s_out[warp][g][2 * q4] = s[0];
-      s_out[warp][g][2 * q4 + 1] = s[1];
-      s_out[warp][g + 8][2 * q4] = s[2];
-      s_out[warp][g + 8][2 * q4 + 1] = s[3];
+      s_out[warp][g][2 * q4] = s[0] + s1[0];
+      s_out[warp][g][2 * q4 + 1] = s[1] + s1[1];
+      s_out[warp][g + 8][2 * q4] = s[2] + s1[2];
+      s_out[warp][g + 8][2 * q4 + 1] = s[3] + s1[3];
       __syncwarp();
       const int here = group - head0 < heads ? group - head0 : heads;
       if (group > 8) {  // one token a tile: its maximum goes from pass to pass
@@ -158,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) score_step_kernel(CacheArgs c, Batch
             v = max_nan(v, s_out[warp][i % kPages][t * heads + k]);
         }
         if (j < a.keep_first || j > newest - a.keep_last) v = __uint_as_float(0x7F800000u);
-        if (page_of(c, b, seq, j) < 0) v = -__uint_as_float(0x7F800000u);
+        if (absent >> (i % kPages) & 1u) v = -__uint_as_float(0x7F800000u);
         a.scores[((rows.begin + token0 + t) * c.heads + h) * a.row_pitch + j] = v;
       }
     }
@@ -185,7 +210,6 @@ constexpr int kGather = 128;
 constexpr int kFill = 256;
 constexpr int kPromptThreads = kReadOut + kGather + kFill + 32;
 constexpr int kIssueWarp = (kPromptThreads - 32) / 32;
-constexpr int kSms = 152;                // one CTA on each
 constexpr int kColumns = 256;
 constexpr int kLanes = 128;              // pages of a tile
 constexpr int kLine = 64;                // channels of a line
@@ -552,8 +576,12 @@ int launch_block_scores(const CacheArgs& c, const BatchArgs& b, const ScoreArgs&
   }
   const int tile_tokens = a.group >= 8 ? 1 : 8 / a.group;
   const int64_t slots = slot_count(b, tile_tokens, 1);
-  const int steps = (b.width + kWarps * kPages - 1) / (kWarps * kPages);
-  const dim3 grid((unsigned)slots, (unsigned)(steps < 65535 ? steps : 65535), (unsigned)c.heads);
+  // CTAs of a tile: two waves of them over all tiles, each with a few steps of 64 pages whose
+  // next page ids come while the last ones' bounds are used.
+  int64_t steps = ((int64_t)b.width + kWarps * kPages - 1) / (kWarps * kPages);
+  const int64_t wanted = (2 * kSms * kStepCtas + slots * c.heads - 1) / (slots * c.heads);
+  steps = steps < wanted ? steps : wanted;
+  const dim3 grid((unsigned)slots, (unsigned)steps, (unsigned)c.heads);
   if (c.dim == 128) {
     if (c.fp16)
       score_step_kernel<true, 128><<<grid, kThreads, 0, stream>>>(c, b, a, tile_tokens);
