@@ -19,7 +19,7 @@ int check_cache(const exact_topk_cache* cache, CacheArgs* out) {
       cache->k_scale == nullptr || cache->v_scale == nullptr)
     return EXACT_TOPK_ERR_NULL_POINTER;
   if (cache->num_pages < 1 || cache->kv_heads < 1 || cache->kv_heads > 1024 ||
-      !page_size_ok(cache->page_size) || (cache->head_dim != 64 && cache->head_dim != 128) ||
+      (int64_t)cache->num_pages * cache->kv_heads > 0x7FFFFFFF || !page_size_ok(cache->page_size) || (cache->head_dim != 64 && cache->head_dim != 128) ||
       (cache->type != EXACT_TOPK_TYPE_BF16 && cache->type != EXACT_TOPK_TYPE_FP16))
     return EXACT_TOPK_ERR_BAD_CACHE;
   if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(cache->key_bounds, 16) ||

@@ -200,14 +200,20 @@ __global__ void __launch_bounds__(kThreads) score_step_kernel(CacheArgs c, Batch
 // token's heads is a maximum over neighbouring columns of one lane, and a warp's 32 lanes
 // write 32 neighbouring scores.
 //
-// One CTA an SM takes items (256 columns x a run of pages) in turn. Its warps keep to one
-// role each: four gather page rows, which lie anywhere in memory, in lines of 64
-// channels through a ring; eight bring the next item's columns, line by line as the products
-// let go of the old ones; one thread issues the products; four warps read the results
-// out. Every wait is bounded; a CTA whose wait ran out writes NaN for what it has not computed.
+// One CTA an SM takes items (256 columns x a run of pages) in turn; where they lie is worked
+// out for up to 16 of them at once. Its warps keep to one role each: four gather page rows,
+// which lie anywhere in memory, in lines of 64 channels through a ring; eight bring the next
+// item's columns, line by line as the products let go of the old ones; one thread issues
+// the products; four warps read the results out. Every wait is bounded; a CTA whose wait
+// ran out writes NaN for what it has not computed.
+//
+// The products alone, with nothing to wait for, take 87 us of a chunk of 4096 tokens x 32 heads
+// over 2048 pages (an SM's shared memory feeds both operands: 96 of its 128 bytes a clock). A
+// TMA gather of four rows at a time brought lines at a fifth of that rate.
 constexpr int kReadOut = 128;            // threads of each role
 constexpr int kGather = 128;
 constexpr int kFill = 256;
+constexpr int kItems = 16;               // items whose places are held
 constexpr int kPromptThreads = kReadOut + kGather + kFill + 32;
 constexpr int kIssueWarp = (kPromptThreads - 32) / 32;
 constexpr int kColumns = 256;
@@ -215,25 +221,27 @@ constexpr int kLanes = 128;              // pages of a tile
 constexpr int kLine = 64;                // channels of a line
 constexpr int kLineBytes = kLanes * kLine * 2;
 
+// An item: a column tile of a sequence and key head, and a run of page tiles (none where there
+// are no rows, or no pages left for the run).
+struct PromptItem {
+  int64_t row0;
+  int seq, head, pos0, tokens, seen, first_page, tiles, first_run;
+};
+
 // Lines are in the order hi, lo of channels 0-63, then hi, lo of channels 64-127.
 template <int D>
 struct PromptShared {
   static constexpr int kChunks = 2 * D / kLine;
-  static constexpr int kStages = D == 128 ? 5 : 6;
+  static constexpr int kStages = 6;
   uint8_t columns[kChunks][kColumns * kLine * 2];
   uint8_t pages[kStages][kLineBytes];
   uint64_t full[kStages], empty[kStages];       // page lines
   uint64_t filled[kChunks], released[kChunks];  // column lines
   uint64_t done[2], free[2];                    // accumulators
   uint64_t drained;
+  PromptItem item[kItems];
   uint32_t tensor;
   int failed;
-};
-
-// An item: a column tile of a sequence and key head, and a run of page tiles.
-struct PromptItem {
-  int64_t row0;
-  int seq, head, pos0, tokens, seen, first_page, tiles;
 };
 
 struct PromptWork {
@@ -241,31 +249,29 @@ struct PromptWork {
   int groups, each;  // runs of page tiles, and the tiles of one
 };
 
-// False where there is nothing to score: no rows, or no pages left for the run.
-__device__ __forceinline__ bool prompt_item(const CacheArgs& c, const BatchArgs& b,
-                                            const PromptWork& w, int tile_tokens, int64_t i,
-                                            PromptItem* item) {
+__device__ __forceinline__ PromptItem prompt_item(const CacheArgs& c, const BatchArgs& b,
+                                                  const PromptWork& w, int tile_tokens,
+                                                  int64_t i) {
+  PromptItem item = {};
   const int group = (int)(i % w.groups);
   const int64_t rest = i / w.groups;
-  item->head = (int)(rest % c.heads);
+  item.head = (int)(rest % c.heads);
+  item.first_run = group == 0;
   const int64_t slot = rest / c.heads;
-  item->seq = sequence_of_slot(b, slot, tile_tokens, 1);
-  const SeqRows rows = sequence_rows(b, c.page_shift, item->seq);
-  const int64_t index = slot - first_slot(b, item->seq, tile_tokens, 1);
-  const int64_t token0 = index * tile_tokens;
-  item->tokens = 0;
-  item->tiles = 0;
-  if (index < 0 || token0 >= rows.count) return false;
-  item->tokens = rows.count - token0 < tile_tokens ? (int)(rows.count - token0) : tile_tokens;
-  item->row0 = rows.begin + token0;
-  item->pos0 = rows.pos0 + (int)token0;
-  const int last = item->pos0 + item->tokens - 1;
-  item->seen = last < 0 ? 0 : (last >> c.page_shift) + 1;
-  item->first_page = group * w.each * kLanes;
-  if (item->first_page >= item->seen) return false;
-  const int all = (item->seen - item->first_page + kLanes - 1) / kLanes;
-  item->tiles = all < w.each ? all : w.each;
-  return true;
+  item.seq = sequence_of_slot(b, slot, tile_tokens, 1);
+  const SeqRows rows = sequence_rows(b, c.page_shift, item.seq);
+  const int64_t token0 = (slot - first_slot(b, item.seq, tile_tokens, 1)) * tile_tokens;
+  if (token0 < 0 || token0 >= rows.count) return item;
+  item.tokens = rows.count - token0 < tile_tokens ? (int)(rows.count - token0) : tile_tokens;
+  item.row0 = rows.begin + token0;
+  item.pos0 = rows.pos0 + (int)token0;
+  const int last = item.pos0 + item.tokens - 1;
+  item.seen = last < 0 ? 0 : (last >> c.page_shift) + 1;
+  item.first_page = group * w.each * kLanes;
+  if (item.first_page >= item.seen) return item;
+  const int all = (item.seen - item.first_page + kLanes - 1) / kLanes;
+  item.tiles = all < w.each ? all : w.each;
+  return item;
 }
 
 // kPadded: the group's heads rounded up to a power of two, at most 32; a column beyond
@@ -311,211 +317,223 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tensor = sm.tensor;
   volatile int* const failed = &sm.failed;
-  PromptItem item;
 
-  if (tid < kReadOut) {
-    // ---- read out ----
-    constexpr int kEach = 32 / kPadded;  // tokens of 32 columns
-    const int64_t row_step = (int64_t)c.heads * a.row_pitch;
-    bool ok = true;
-    int count = 0;  // tiles so far
-    for (int64_t i = blockIdx.x; i < work.items; i += gridDim.x) {
-      if (!prompt_item(c, b, work, kTileTokens, i, &item)) continue;
-      const int first_newest = item.pos0 >> c.page_shift;  // the first token's newest page
-      const int parts = (item.tokens + kEach - 1) / kEach;
-      int j0 = item.first_page + warp * 32;
-      bool there = j0 + lane < item.seen && page_of(c, b, item.seq, j0 + lane) >= 0;
-      for (int tile = 0; tile < item.tiles; ++tile, ++count, j0 += kLanes) {
-        const int buffer = count & 1, j = j0 + lane;
-        // all of the warp's pages are seen by every token, and scored
-        const bool plain = item.pos0 >= 0 && j0 >= a.keep_first &&
-                           j0 + 31 <= first_newest - a.keep_last && __all_sync(~0u, there);
-        float* at = a.scores + (item.row0 * c.heads + item.head) * a.row_pitch + j;
-        if (ok) ok = barrier_wait(&sm.done[buffer], (count >> 1) & 1, failed);
-        ok = __all_sync(~0u, ok);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t from = tensor + ((uint32_t)(warp * 32) << 16) + buffer * kColumns;
-        const auto largest = [&](const float (&v)[32], int t) {
-          float best = v[t * kPadded];
-          if (kPadded == 2) best = max_nan(best, v[t * kPadded + 1]);
+  // Each role's own counts go on from batch to batch of items, as the barriers' phases do.
+  bool ok = true;
+  int steps = 0, tiles = 0, columns_filled = 0;
+  for (int64_t item0 = blockIdx.x; item0 < work.items; item0 += (int64_t)kItems * gridDim.x) {
+    const int items = (int)((work.items - item0 + gridDim.x - 1) / gridDim.x < kItems
+                                ? (work.items - item0 + gridDim.x - 1) / gridDim.x
+                                : kItems);
+    __syncthreads();
+    if (tid < items)
+      sm.item[tid] = prompt_item(c, b, work, kTileTokens, item0 + (int64_t)tid * gridDim.x);
+    __syncthreads();
+    if (tid < kReadOut) {
+      // ---- read out ----
+      constexpr int kEach = 32 / kPadded;  // tokens of 32 columns
+      const int64_t row_step = (int64_t)c.heads * a.row_pitch;
+      for (int i = 0; i < items; ++i) {
+        const PromptItem& item = sm.item[i];
+        if (item.tiles == 0) continue;
+        const int first_newest = item.pos0 >> c.page_shift;  // the first token's newest page
+        const int parts = (item.tokens + kEach - 1) / kEach;
+        int j0 = item.first_page + warp * 32;
+        bool there = j0 + lane < item.seen && page_of(c, b, item.seq, j0 + lane) >= 0;
+        for (int tile = 0; tile < item.tiles; ++tile, ++tiles, j0 += kLanes) {
+          const int buffer = tiles & 1, j = j0 + lane;
+          // all of the warp's pages are seen by every token, and scored
+          const bool plain = item.pos0 >= 0 && j0 >= a.keep_first &&
+                             j0 + 31 <= first_newest - a.keep_last && __all_sync(~0u, there);
+          float* at = a.scores + (item.row0 * c.heads + item.head) * a.row_pitch + j;
+          if (ok) ok = barrier_wait(&sm.done[buffer], (tiles >> 1) & 1, failed);
+          ok = __all_sync(~0u, ok);
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint32_t from = tensor + ((uint32_t)(warp * 32) << 16) + buffer * kColumns;
+          const auto largest = [&](const float (&v)[32], int t) {
+            float best = v[t * kPadded];
+            if (kPadded == 2) best = max_nan(best, v[t * kPadded + 1]);
 #pragma unroll
-          for (int k = 1; k + 1 < kPadded; k += 2)
-            best = max_nan(best, v[t * kPadded + k], v[t * kPadded + k + 1]);
-          if (kPadded > 2) best = max_nan(best, v[t * kPadded + kPadded - 1]);
-          return best;
-        };
-        const auto write = [&](int part, const float (&v)[32]) {
-          const int left = item.tokens - part * kEach;
-          if (plain && ok && left >= kEach) {
+            for (int k = 1; k + 1 < kPadded; k += 2)
+              best = max_nan(best, v[t * kPadded + k], v[t * kPadded + k + 1]);
+            if (kPadded > 2) best = max_nan(best, v[t * kPadded + kPadded - 1]);
+            return best;
+          };
+          const auto write = [&](int part, const float (&v)[32]) {
+            const int left = item.tokens - part * kEach;
+            if (plain && ok && left >= kEach) {
 #pragma unroll
-            for (int t = 0; t < kEach; ++t, at += row_step) *at = largest(v, t);
-            return;
+              for (int t = 0; t < kEach; ++t, at += row_step) *at = largest(v, t);
+              return;
+            }
+#pragma unroll
+            for (int t = 0; t < kEach; ++t, at += row_step) {
+              float best = ok ? largest(v, t) : __uint_as_float(0x7FFFFFFFu);
+              const int pos = item.pos0 + part * kEach + t;
+              const int newest = pos >> c.page_shift;
+              if (j < a.keep_first || j > newest - a.keep_last)
+                best = __uint_as_float(0x7F800000u);
+              if (!there) best = -__uint_as_float(0x7F800000u);
+              if (t < left && pos >= 0 && j <= newest) *at = best;
+            }
+          };
+          bool next = false;  // the next tile's page, asked for before it is needed
+          if (tile + 1 < item.tiles && j + kLanes < item.seen)
+            next = page_of(c, b, item.seq, j + kLanes) >= 0;
+          for (int part = 0; part < parts; ++part) {
+            float v[32];
+            tensor_load32(from + part * 32, v);
+            tensor_wait(v);
+            write(part, v);
           }
-#pragma unroll
-          for (int t = 0; t < kEach; ++t, at += row_step) {
-            float best = ok ? largest(v, t) : __uint_as_float(0x7FFFFFFFu);
-            const int pos = item.pos0 + part * kEach + t;
-            const int newest = pos >> c.page_shift;
-            if (j < a.keep_first || j > newest - a.keep_last)
-              best = __uint_as_float(0x7F800000u);
-            if (!there) best = -__uint_as_float(0x7F800000u);
-            if (t < left && pos >= 0 && j <= newest) *at = best;
-          }
-        };
-        bool next = false;  // the next tile's page, asked for before it is needed
-        if (tile + 1 < item.tiles && j + kLanes < item.seen)
-          next = page_of(c, b, item.seq, j + kLanes) >= 0;
-        for (int part = 0; part < parts; ++part) {
-          float v[32];
-          tensor_load32(from + part * 32, v);
-          tensor_wait(v);
-          write(part, v);
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          barrier_arrive(&sm.free[buffer]);
+          there = next;
         }
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-        barrier_arrive(&sm.free[buffer]);
-        there = next;
       }
-    }
-  } else if (tid < kReadOut + kGather) {
-    // ---- gather: thread i takes piece i % 8 of the lines of pages i / 8 + 16 k ----
-    constexpr int kRows = kLanes / (kGather / 8);
-    const int piece = tid & 7, line0 = (tid - kReadOut) >> 3;
-    const uint16_t* const bounds = static_cast<const uint16_t*>(c.bounds);
-    int step = 0;
-    bool ok = true;
-    for (int64_t i = blockIdx.x; i < work.items && ok; i += gridDim.x) {
-      if (!prompt_item(c, b, work, kTileTokens, i, &item)) continue;
-      int next[kRows];  // ids of the tile after this one
-      const auto find = [&](int tile) {
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-          const int j = item.first_page + tile * kLanes + line0 + k * (kGather / 8);
-          next[k] = tile < item.tiles && j < item.seen ? page_of(c, b, item.seq, j) : -1;
-        }
-      };
-      find(0);
-      for (int tile = 0; tile < item.tiles && ok; ++tile) {
-        int id[kRows];
-#pragma unroll
-        for (int k = 0; k < kRows; ++k) id[k] = next[k];
-        find(tile + 1);
-        for (int chunk = 0; chunk < kChunks; ++chunk, ++step) {
-          const int s = step % kStages;
-          if (step >= kStages && !barrier_wait(&sm.empty[s], (step / kStages - 1) & 1, failed)) {
-            ok = false;
-            break;
-          }
-          const uint32_t to = shared_address(sm.pages[s]);
-          const int channel = (chunk & 1) * D + (chunk >> 1) * kLine + piece * 8;
+    } else if (tid < kReadOut + kGather) {
+      // ---- gather: thread i takes piece i % 8 of the lines of pages i / 8 + 16 k ----
+      constexpr int kRows = kLanes / (kGather / 8);
+      const int piece = tid & 7, line0 = (tid - kReadOut) >> 3;
+      const uint16_t* const bounds = static_cast<const uint16_t*>(c.bounds);
+      for (int i = 0; i < items && ok; ++i) {
+        const PromptItem& item = sm.item[i];
+        // where the lines of the tile after this one are; those of absent pages and ones that
+        // nobody sees are the first page's, whose results are not written
+        const uint16_t* next[kRows];
+        const auto find = [&](int tile) {
 #pragma unroll
           for (int k = 0; k < kRows; ++k) {
-            const int line = line0 + k * (kGather / 8);
-            const int64_t page = id[k] < 0 ? 0 : id[k];
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             to + line * (kLine * 2) + ((piece ^ (line & 7)) << 4)),
-                         "l"(bounds + (page * c.heads + item.head) * (2 * D) + channel),
-                         "r"(id[k] < 0 ? 0 : 16)
+            const int j = item.first_page + tile * kLanes + line0 + k * (kGather / 8);
+            const int page = tile < item.tiles && j < item.seen ? page_of(c, b, item.seq, j) : 0;
+            next[k] = bounds + ((int64_t)(page < 0 ? 0 : page) * c.heads + item.head) * (2 * D) +
+                      piece * 8;
+          }
+        };
+        find(0);
+        for (int tile = 0; tile < item.tiles && ok; ++tile) {
+          const uint16_t* from[kRows];
+#pragma unroll
+          for (int k = 0; k < kRows; ++k) from[k] = next[k];
+          find(tile + 1);
+          for (int chunk = 0; chunk < kChunks; ++chunk, ++steps) {
+            const int s = steps % kStages;
+            if (steps >= kStages &&
+                !barrier_wait(&sm.empty[s], (steps / kStages - 1) & 1, failed)) {
+              ok = false;
+              break;
+            }
+            const uint32_t to =
+                shared_address(sm.pages[s]) + line0 * (kLine * 2) + ((piece ^ (line0 & 7)) << 4);
+            const int channel = (chunk & 1) * D + (chunk >> 1) * kLine;
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                               to + k * (kGather / 8) * (kLine * 2)),
+                           "l"(from[k] + channel)
+                           : "memory");
+            // arrives when this thread's copies have; the issuing thread orders them before its
+            // reads
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                             shared_address(&sm.full[s]))
                          : "memory");
           }
-          // arrives when this thread's copies have; the issuing thread orders them before its reads
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                           shared_address(&sm.full[s]))
-                       : "memory");
         }
       }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp < kIssueWarp) {
-    // ---- columns: 8 channels at a time, the positive and the negative part to their lines ----
-    constexpr int kLines = D / kLine;                    // of a column of q
-    constexpr int kPieces = kColumns * kLine / 8 / kFill;  // a thread's pieces of a line
-    const int thread = tid - kReadOut - kGather;
-    const int piece = thread & 7;
-    bool ok = true;
-    int count = 0;  // items so far
-    for (int64_t i = blockIdx.x; i < work.items && ok; i += gridDim.x) {
-      const bool any = prompt_item(c, b, work, kTileTokens, i, &item);
-      // lengths, by the threads of each column tile's first run
-      if (i % work.groups == 0 && thread < item.tokens) {
-        const int pos = item.pos0 + thread;
-        a.ke[(item.row0 + thread) * c.heads + item.head] =
-            pos < 0 ? 0 : (pos >> c.page_shift) + 1;
-      }
-      if (!any) continue;
-      uint4 w[kLines][kPieces];
-#pragma unroll
-      for (int line = 0; line < kLines; ++line)
-#pragma unroll
-        for (int n = 0; n < kPieces; ++n) {
-          const int col = (thread >> 3) + n * (kFill / 8);
-          const int token = col / kPadded;
-          const int head = col % kPadded < a.group ? col % kPadded : a.group - 1;
-          w[line][n] = make_uint4(0u, 0u, 0u, 0u);
-          if (token < item.tokens)
-            w[line][n] = __ldg(reinterpret_cast<const uint4*>(
-                static_cast<const uint16_t*>(a.q.data) + (item.row0 + token) * a.q.token_stride +
-                ((int64_t)item.head * a.group + head) * a.q.head_stride + line * kLine +
-                piece * 8));
+    } else if (warp < kIssueWarp) {
+      // ---- columns: 8 channels at a time, the positive and the negative part to their lines ----
+      constexpr int kLines = D / kLine;                    // of a column of q
+      constexpr int kPieces = kColumns * kLine / 8 / kFill;  // a thread's pieces of a line
+      const int thread = tid - kReadOut - kGather;
+      const int piece = thread & 7;
+      for (int i = 0; i < items && ok; ++i) {
+        const PromptItem& item = sm.item[i];
+        // lengths, by the threads of each column tile's first run
+        if (item.first_run && thread < item.tokens) {
+          const int pos = item.pos0 + thread;
+          a.ke[(item.row0 + thread) * c.heads + item.head] =
+              pos < 0 ? 0 : (pos >> c.page_shift) + 1;
         }
+        if (item.tiles == 0) continue;
+        uint4 w[kLines][kPieces];
 #pragma unroll
-      for (int chunk = 0; chunk < kChunks; ++chunk) {
-        if (ok && count > 0) ok = barrier_wait(&sm.released[chunk], (count - 1) & 1, failed);
-        if (!ok) break;
-        const bool positive = (chunk & 1) == 0;
+        for (int line = 0; line < kLines; ++line)
 #pragma unroll
-        for (int n = 0; n < kPieces; ++n) {
-          const int col = (thread >> 3) + n * (kFill / 8);
-          const uint4 u = w[chunk >> 1][n];
-          *reinterpret_cast<uint4*>(
-              &sm.columns[chunk][col * (kLine * 2) + ((piece ^ (col & 7)) << 4)]) =
-              make_uint4(clamp_sign<kFp16>(u.x, positive), clamp_sign<kFp16>(u.y, positive),
-                         clamp_sign<kFp16>(u.z, positive), clamp_sign<kFp16>(u.w, positive));
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        barrier_arrive(&sm.filled[chunk]);
-      }
-      ++count;
-    }
-  } else {
-    // ---- products, by one thread ----
-    if (lane == 0) {
-      constexpr uint32_t kType = kFp16 ? 0u : 1u;
-      constexpr uint32_t kind = 1u << 4 | kType << 7 | kType << 10 | (kColumns / 8) << 17 |
-                                (kLanes / 16) << 24;
-      int step = 0, count = 0, items = 0;
-      bool ok = true;
-      for (int64_t i = blockIdx.x; i < work.items && ok; i += gridDim.x) {
-        if (!prompt_item(c, b, work, kTileTokens, i, &item)) continue;
-        for (int tile = 0; tile < item.tiles && ok; ++tile, ++count) {
-          const int buffer = count & 1;
-          if (count >= 2) ok = barrier_wait(&sm.free[buffer], ((count >> 1) - 1) & 1, failed);
-          for (int chunk = 0; chunk < kChunks && ok; ++chunk, ++step) {
-            const int s = step % kStages;
-            if (tile == 0) ok = barrier_wait(&sm.filled[chunk], items & 1, failed);
-            if (ok) ok = barrier_wait(&sm.full[s], (step / kStages) & 1, failed);
-            if (!ok) break;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint64_t pages = operand(shared_address(sm.pages[s]));
-            const uint64_t columns = operand(shared_address(sm.columns[chunk]));
-#pragma unroll
-            for (int k = 0; k < kLine / 16; ++k)  // 32 bytes of a line each
-              tensor_mma(tensor + buffer * kColumns, pages + 2 * k, columns + 2 * k, kind,
-                         chunk > 0 || k > 0);
-            tensor_commit(&sm.empty[s]);
-            if (tile == item.tiles - 1) tensor_commit(&sm.released[chunk]);
+          for (int n = 0; n < kPieces; ++n) {
+            const int col = (thread >> 3) + n * (kFill / 8);
+            const int token = col / kPadded;
+            const int head = col % kPadded < a.group ? col % kPadded : a.group - 1;
+            w[line][n] = make_uint4(0u, 0u, 0u, 0u);
+            if (token < item.tokens)
+              w[line][n] = __ldg(reinterpret_cast<const uint4*>(
+                  static_cast<const uint16_t*>(a.q.data) + (item.row0 + token) * a.q.token_stride +
+                  ((int64_t)item.head * a.group + head) * a.q.head_stride + line * kLine +
+                  piece * 8));
           }
-          if (ok) tensor_commit(&sm.done[buffer]);
+#pragma unroll
+        for (int chunk = 0; chunk < kChunks; ++chunk) {
+          if (ok && columns_filled > 0)
+            ok = barrier_wait(&sm.released[chunk], (columns_filled - 1) & 1, failed);
+          if (!ok) break;
+          const bool positive = (chunk & 1) == 0;
+#pragma unroll
+          for (int n = 0; n < kPieces; ++n) {
+            const int col = (thread >> 3) + n * (kFill / 8);
+            const uint4 u = w[chunk >> 1][n];
+            *reinterpret_cast<uint4*>(
+                &sm.columns[chunk][col * (kLine * 2) + ((piece ^ (col & 7)) << 4)]) =
+                make_uint4(clamp_sign<kFp16>(u.x, positive), clamp_sign<kFp16>(u.y, positive),
+                           clamp_sign<kFp16>(u.z, positive), clamp_sign<kFp16>(u.w, positive));
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          barrier_arrive(&sm.filled[chunk]);
         }
-        ++items;
+        ++columns_filled;
       }
-      // what was issued ends before the shared memory and the tensor memory go
-      int none = 0;
-      tensor_commit(&sm.drained);
-      barrier_wait(&sm.drained, 0, &none);
+    } else {
+      // ---- products, by one thread ----
+      if (lane == 0) {
+        constexpr uint32_t kType = kFp16 ? 0u : 1u;
+        constexpr uint32_t kind = 1u << 4 | kType << 7 | kType << 10 | (kColumns / 8) << 17 |
+                                  (kLanes / 16) << 24;
+        for (int i = 0; i < items && ok; ++i) {
+          const int item_tiles = sm.item[i].tiles;
+          if (item_tiles == 0) continue;
+          for (int tile = 0; tile < item_tiles && ok; ++tile, ++tiles) {
+            const int buffer = tiles & 1;
+            if (tiles >= 2) ok = barrier_wait(&sm.free[buffer], ((tiles >> 1) - 1) & 1, failed);
+            for (int chunk = 0; chunk < kChunks && ok; ++chunk, ++steps) {
+              const int s = steps % kStages;
+              if (tile == 0) ok = barrier_wait(&sm.filled[chunk], columns_filled & 1, failed);
+              if (ok) ok = barrier_wait(&sm.full[s], (steps / kStages) & 1, failed);
+              if (!ok) break;
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              const uint64_t pages = operand(shared_address(sm.pages[s]));
+              const uint64_t columns = operand(shared_address(sm.columns[chunk]));
+#pragma unroll
+              for (int k = 0; k < kLine / 16; ++k)  // 32 bytes of a line each
+                tensor_mma(tensor + buffer * kColumns, pages + 2 * k, columns + 2 * k, kind,
+                           chunk > 0 || k > 0);
+              tensor_commit(&sm.empty[s]);
+              if (tile == item_tiles - 1) tensor_commit(&sm.released[chunk]);
+            }
+            if (ok) tensor_commit(&sm.done[buffer]);
+          }
+          ++columns_filled;
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
   }
+  if (tid == kIssueWarp * 32) {
+    // what was issued ends before the shared memory and the tensor memory go
+    int none = 0;
+    tensor_commit(&sm.drained);
+    barrier_wait(&sm.drained, 0, &none);
+  }
+  __syncwarp();
+  asm volatile("cp.async.wait_all;" ::: "memory");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -537,12 +555,15 @@ int launch_prompt(const CacheArgs& c, const BatchArgs& b, const ScoreArgs& a,
   PromptWork work;
   work.slots = slot_count(b, kColumns / kPadded, 1);
   const int tiles = (b.width + kLanes - 1) / kLanes;
-  // Runs of page tiles: about seven for each CTA, so that the last ones end together, of at
-  // most 16 and at least 2 tiles, which the bringing in of an item's columns hides behind.
-  int64_t each = work.slots * c.heads * tiles / (kSms * 7);
-  each = each < 2 ? 2 : (each > 16 ? 16 : each);
-  work.each = (int)each;
-  work.groups = (int)((tiles + each - 1) / each);
+  // Runs of page tiles of equal length, as few of them as make six items for each CTA, so that the
+  // last ones end together; of at least 2 tiles, behind which an item's columns come in, and of at
+  // most 16.
+  const int64_t column_tiles = work.slots * c.heads;
+  int64_t groups = (kSms * 6 + column_tiles - 1) / column_tiles;
+  groups = groups < (tiles + 15) / 16 ? (tiles + 15) / 16 : groups;
+  groups = groups > (tiles + 1) / 2 ? (tiles + 1) / 2 : groups;
+  work.each = (int)((tiles + groups - 1) / groups);
+  work.groups = (tiles + work.each - 1) / work.each;
   work.items = work.slots * c.heads * work.groups;
   const unsigned grid = (unsigned)(work.items < kSms ? work.items : kSms);
   kernel<<<grid, kPromptThreads, smem, stream>>>(c, b, a, work);

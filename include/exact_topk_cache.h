@@ -53,7 +53,7 @@ extern "C" {
  *   key_bounds  device `type` [num_pages][kv_heads][2][head_dim]: largest, then
  *               smallest; 16-byte aligned. May be NULL where no bounds are kept:
  *               exact_topk_block_scores then refuses the cache.
- *   page_size   16, 32, 64 or 128;  head_dim 64 or 128
+ *   page_size   16, 32, 64 or 128;  head_dim 64 or 128;  num_pages * kv_heads below 2^31
  *   type        EXACT_TOPK_TYPE_BF16 or _FP16: of the bounds and of every row array */
 typedef struct exact_topk_cache {
   void* k;
