@@ -22,8 +22,8 @@
 // O stays in one unit.
 //
 // Queries, probabilities and the running maximum are as in attention_kernels.cu. Three
-// things are left to that kernel, which runs behind this one on the tiles that are marked:
-// a NaN among the values (0 * NaN would reach rows that do not see it), scales of values
+// things are left to that kernel, which runs behind this one on the tiles that are marked: a
+// NaN among scores or values (which would reach rows that do not see it), scales of values
 // more than 2^12 apart, and a wait that ran out.
 //
 // What bounds it: the exponentials, 64 x 128 a block at 16 a clock of an SM (512 clocks, as the
@@ -112,12 +112,12 @@ __device__ __forceinline__ void tensor_store32(uint32_t address, const uint32_t 
 }
 
 // A part of a page: at most 64 tokens.
-struct Entry {
-  int64_t offset;    // of its codes; -1 for an absent page
+struct alignas(16) Entry {
   int pos;           // position of its first token
-  uint32_t members;  // tokens of the tile that take it
+  uint32_t members;  // tokens of the tile that take it; 0 for an absent page
   float k_scale;
   float v_part;      // the values' scale without its power of two
+  int64_t offset;    // of its codes; -1 for an absent page
   uint32_t v_power;  // that power of two over the tile's unit, twice in FP16
 };
 
@@ -132,10 +132,11 @@ struct Shared {
   uint64_t scored[2], weighed[2], added[2], drained;
   uint32_t tensor;
   int scan[kIssueWarp];
-  int failed, again, unit;
+  int failed, again, unit, odd;
 };
 
-template <int D>
+// kPartShift: log2 of the parts of a block (1 of pages of 64 and 128 tokens, 2 of 32, 4 of 16).
+template <int D, int kPartShift>
 __global__ void __launch_bounds__(kThreads, 2)
     prompt_attention_kernel(CacheArgs c, BatchArgs b, AttentionArgs a) {
   using Smem = Shared<D>;
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     sm.failed = 0;
     sm.again = 0;
     sm.unit = -1000;
+    sm.odd = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kIssueWarp) {
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // ---- how many parts of pages there are, and how many before this thread's ----
   const int part_shift = c.page_shift > 6 ? c.page_shift - 6 : 0;  // parts of a page
-  const int part_tokens_shift = c.page_shift > 6 ? 6 : c.page_shift;
+  constexpr int part_tokens_shift = 6 - kPartShift, per_block_shift = kPartShift;
   const int per_thread = (pages + kIssueWarp * 32 - 1) / (kIssueWarp * 32);
   int mine = 0, count = pages;
   if (listed) {
@@ -315,7 +317,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int chunk0 = 0; chunk0 < (count << part_shift); chunk0 += kEntries) {
     const int left = (count << part_shift) - chunk0;
     const int entries = left < kEntries ? left : kEntries;
-    const int per_block_shift = 6 - part_tokens_shift;
     const int blocks = (entries + (1 << per_block_shift) - 1) >> per_block_shift;
     // ---- the chunk's parts of pages ----
     __syncthreads();
@@ -341,6 +342,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         e.offset = -1;
         e.members = 0u;
         e.pos = most;
+        e.k_scale = 0.f;
+        e.v_part = 1.f;
         continue;
       }
       if (!listed) {
@@ -351,6 +354,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       e.offset = -1;
       if (page < 0) {
         e.members = 0u;
+        e.k_scale = 0.f;
+        e.v_part = 1.f;
         continue;
       }
       const int64_t tile = (int64_t)page * c.heads + head;
@@ -358,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       e.k_scale = __ldg(c.k_scale + tile);
       const uint32_t v = __float_as_uint(__ldg(c.v_scale + tile));
       e.v_part = __uint_as_float((v & 0x7FFFFFu) | 127u << 23);
+      if (e.v_part != 1.f) sm.odd = 1;
       const int power = (int)(v >> 23 & 255u) - 127;
       e.v_power = (uint32_t)power;  // for now
       high = high > power ? high : power;
@@ -390,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncthreads();
 
+    const bool odd = sm.odd != 0;
     if (tid < kRows) {
       // ---- softmax: a row a thread ----
       for (int block = 0; block < blocks; ++block) {
@@ -399,104 +406,88 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t from = tensor + lane_base + kS + (n & 1) * kBlock;
-        float s[32];
-        tensor_load32(from, s);
-        // what this row sees of each 16 tokens
-        int seen[4];
-        float scale[4], v_part[4];
-        bool any[4], all[4];
+        // A part that this row does not take, and tokens behind its own, have probability 0: an
+        // offset of -inf does it for whole parts.
+        constexpr int kParts = 1 << kPartShift;
+        float scale[kParts], v_part[kParts];
+        int seen[kParts];
+        bool cuts = false;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int token = k * 16;
-          const Entry& e = sm.entry[(block << per_block_shift) + (token >> part_tokens_shift)];
-          const int pos = e.pos + (token & ((1 << part_tokens_shift) - 1));
-          const bool takes = row_pos >= 0 && (e.members >> row_token & 1u) != 0u;
-          seen[k] = takes ? row_pos + 1 - pos : 0;
+        for (int k = 0; k < kParts; ++k) {
+          const Entry& e = sm.entry[(block << per_block_shift) + k];
+          const bool takes = row_pos >= e.pos && (e.members >> row_token & 1u) != 0u;
+          seen[k] = takes ? row_pos + 1 - e.pos : 0;
           scale[k] = row_factor * e.k_scale;
-          v_part[k] = e.offset >= 0 ? e.v_part : 1.f;
-          any[k] = __any_sync(~0u, seen[k] > 0);
-          all[k] = __all_sync(~0u, seen[k] >= 16);
+          v_part[k] = e.v_part;
+          cuts |= takes && seen[k] < 1 << part_tokens_shift;
         }
-        // The largest score, of both halves; then the probabilities, of the second half and of
-        // the first, which is read again: a row's 64 scores at once would not fit the
-        // registers. Sixteen tokens are left out where no row of the warp sees one, and
-        // masked where some row does not see all of them.
-        float best = -infinity();
-        const auto largest = [&](int k, const float* x) {
-          if (!any[k]) return;
-          float high;
-          if (all[k]) {
-            high = max3(x[0], x[1], x[2]);
-            float other = max3(x[3], x[4], x[5]);
-            high = max3(high, x[6], x[7]);
-            other = max3(other, x[8], x[9]);
-            high = max3(high, x[10], x[11]);
-            other = max3(other, x[12], x[13]);
-            high = fmaxf(max3(high, x[14], x[15]), other);
-          } else {
-            high = -infinity();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) high = fmaxf(high, i < seen[k] ? x[i] : -infinity());
-          }
-          best = fmaxf(best, high * scale[k]);  // (-inf * 0, of a row that sees none, is ignored)
-        };
-        tensor_wait(s);
-        largest(0, s);
-        largest(1, s + 16);
-        tensor_load32(from + 32, s);
-        tensor_wait(s);
-        largest(2, s);
-        largest(3, s + 16);
-        float by = 1.f;
-        const bool raise = best > m + kSlack;
-        const bool some = __any_sync(~0u, raise);
-        if (raise) {
-          by = m == -infinity() ? 0.f : exp2_fast(m - best);
-          m = best;
-          l *= by;
-        }
-        const float base = m == -infinity() ? 0.f : m;
+        cuts = __any_sync(~0u, cuts);
+        // Probabilities under the running maximum, 16 tokens at a time, the next ones' scores on
+        // their way. Where a score turns out too far above the maximum, that is raised and
+        // the block done again: it is seldom.
         uint32_t p[32];
-        float2 sum = make_float2(0.f, 0.f);
-        const auto weigh = [&](int k, const float* x) {
-          if (!any[k]) {
+        float2 sum;
+        float by = 1.f;
+        bool some = false;
+        for (int attempt = 0; attempt < 2; ++attempt) {
+          const float base = m == -infinity() ? 0.f : m;
+          float high = -infinity();
+          sum = make_float2(0.f, 0.f);
+          float s[2][16];
+          tensor_load16(from, s[0]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) p[k * 8 + i] = 0u;
-            return;
-          }
-          float2 y[8];
+          for (int k = 0; k < 4; ++k) {
+            constexpr int kPartGroups = 4 >> kPartShift;  // 16 tokens of a part
+            const int part = k / kPartGroups;
+            const float(&x)[16] = s[k & 1];
+            tensor_wait(s[k & 1]);
+            if (k < 3) tensor_load16(from + (k + 1) * 16, s[(k + 1) & 1]);
+            const float offset = seen[part] > 0 ? -base : -infinity();
+            float2 y[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            y[i] = fma2(make_float2(x[2 * i], x[2 * i + 1]), scale[k], -base);
-          if (!all[k]) {
+            for (int i = 0; i < 8; ++i)
+              y[i] = fma2(make_float2(x[2 * i], x[2 * i + 1]), scale[part], offset);
+            if (cuts) {
+              const int left = seen[part] - k % kPartGroups * 16;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                y[i].x = 2 * i < left ? y[i].x : -infinity();
+                y[i].y = 2 * i + 1 < left ? y[i].y : -infinity();
+              }
+            }
+            const float high0 =
+                max3(max3(y[0].x, y[0].y, y[1].x), y[1].y, max3(y[2].x, y[2].y, y[3].x));
+            const float high1 =
+                max3(max3(y[3].y, y[4].x, y[4].y), y[5].x, max3(y[5].y, y[6].x, y[6].y));
+            high = max3(high, max3(high0, y[7].x, y[7].y), high1);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              y[i].x = 2 * i < seen[k] ? y[i].x : -infinity();
-              y[i].y = 2 * i + 1 < seen[k] ? y[i].y : -infinity();
+              y[i].x = exp2_fast(y[i].x);
+              y[i].y = exp2_fast(y[i].y);
             }
-          }
+            const float2 sum0 = add2(add2(y[0], y[1]), add2(y[2], y[3]));
+            const float2 sum1 = add2(add2(y[4], y[5]), add2(y[6], y[7]));
+            sum = add2(sum, add2(sum0, sum1));
+            if (odd) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            y[i].x = exp2_fast(y[i].x);
-            y[i].y = exp2_fast(y[i].y);
-            sum = add2(sum, y[i]);
-          }
-          if (v_part[k] != 1.f) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              y[i].x *= v_part[k];
-              y[i].y *= v_part[k];
+              for (int i = 0; i < 8; ++i) {
+                y[i].x *= v_part[part];
+                y[i].y *= v_part[part];
+              }
             }
-          }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) p[k * 8 + i] = pack2<true>(y[i].x, y[i].y);
-        };
-        weigh(2, s);
-        weigh(3, s + 16);
-        tensor_load32(from, s);
-        tensor_wait(s);
-        weigh(0, s);
-        weigh(1, s + 16);
+            for (int i = 0; i < 8; ++i) p[k * 8 + i] = pack2<true>(y[i].x, y[i].y);
+          }
+          const bool raise = high > (m == -infinity() ? m : kSlack);
+          if (!__any_sync(~0u, raise)) break;
+          some = true;
+          if (raise) {
+            const float best = base + high;
+            by = m == -infinity() ? 0.f : exp2_fast(m - best);
+            m = best;
+            l *= by;
+          }
+        }
         l += sum.x + sum.y;
         if (some && n > 0) {  // O is in place up to the block before
           ok = was_added(n - 1);
@@ -560,18 +551,25 @@ __global__ void __launch_bounds__(kThreads, 2)
               make_uint4(y[4], y[5], y[6], y[7]);
         }
       };
-      load(0, c.k, k);
-      load(0, c.v, v);
-      for (int block = 0; block < blocks; ++block) {
+      const auto keys = [&](int block) {
         const int n = done + block, buffer = n & 1;
         if (n >= 2) ok = ok && barrier_wait(&sm.k_free[buffer], ((n >> 1) - 1) & 1, failed);
-        if (!ok) break;
+        if (!ok) return;
 #pragma unroll
         for (int i = 0; i < 2; ++i) place(sm.k[buffer], i, k[i], 0x3C003C00u);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         barrier_arrive(&sm.k_full[buffer]);
         load(block + 1, c.k, k);
-        if (n >= 2) ok = barrier_wait(&sm.v_free[buffer], ((n >> 1) - 1) & 1, failed);
+      };
+      load(0, c.k, k);
+      load(0, c.v, v);
+      keys(0);
+      for (int block = 0; block < blocks; ++block) {
+        // keys are a block ahead: their place is free as soon as the scores are there, the
+        // values' not before the probabilities have been used
+        if (block + 1 < blocks) keys(block + 1);
+        const int n = done + block, buffer = n & 1;
+        if (n >= 2) ok = ok && barrier_wait(&sm.v_free[buffer], ((n >> 1) - 1) & 1, failed);
         if (!ok) break;
         uint32_t bad = 0u;
 #pragma unroll
@@ -636,6 +634,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // ---- outputs ----
   if (tid < kRows) {
+    // NaN among scores: of this row's own, or of a part that it does not take
+    if (l != l) sm.again = 1;
     if (done > 0) {
       ok = ok && was_added(done - 1);
       ok = __all_sync(~0u, ok);
@@ -687,27 +687,35 @@ __global__ void __launch_bounds__(kThreads, 2)
                  : "memory");
 }
 
-template <int D>
+template <int D, int kPartShift>
 int launch(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a, cudaStream_t stream) {
   const size_t smem =
       sizeof(Shared<D>) + 1024 + (a.blocks != nullptr ? (size_t)b.width * 4 : 0);
-  if (cudaFuncSetAttribute(prompt_attention_kernel<D>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess) {
+  const auto kernel = prompt_attention_kernel<D, kPartShift>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess) {
     cudaGetLastError();
     return EXACT_TOPK_ERR_CUDA;
   }
   const dim3 grid((unsigned)slot_count(b, a.prompt_tokens, 1), (unsigned)c.heads,
                   (unsigned)((a.group + a.prompt_heads - 1) / a.prompt_heads));
-  prompt_attention_kernel<D><<<grid, kThreads, smem, stream>>>(c, b, a);
+  kernel<<<grid, kThreads, smem, stream>>>(c, b, a);
   return launch_status();
+}
+
+template <int D>
+int launch_parts(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a,
+                 cudaStream_t stream) {
+  if (c.page == 16) return launch<D, 2>(c, b, a, stream);
+  if (c.page == 32) return launch<D, 1>(c, b, a, stream);
+  return launch<D, 0>(c, b, a, stream);
 }
 
 }  // namespace
 
 int launch_prompt_attention(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a,
                             cudaStream_t stream) {
-  return c.dim == 128 ? launch<128>(c, b, a, stream) : launch<64>(c, b, a, stream);
+  return c.dim == 128 ? launch_parts<128>(c, b, a, stream) : launch_parts<64>(c, b, a, stream);
 }
 
 }  // namespace etk

@@ -322,12 +322,15 @@ def test_nan_reaches_the_rows_that_see_it_and_no_other(page, dim, group):
     put(k8, last - 4, 0)        # by five
     q = ref.rows(48, 7, group, dim, BF16, 2.0)
     check_attention(tensors, batch, q)
+    check_attention(tensors, batch, q, prompt=1)
     put(v8, 2 * page + 1, 5)    # by those that list page 2
     put(k8, 3 * page, 1)        # page 3
     blocks = torch.tensor([[0, 1, -1], [0, 2, 1], [1, 0, 5], [3, 0, 1], [0, 1, 2], [6, 0, 1], [4, 5, 0]], dtype=torch.int32)
     check_attention(tensors, batch, q, blocks)
+    check_attention(tensors, batch, q, blocks, prompt=1)
     q[2], q[4, 0, 0] = math.nan, math.inf
     check_attention(tensors, batch, q, blocks)
+    check_attention(tensors, batch, q, blocks, prompt=1)
 
 
 def test_absent_pages_are_not_seen():
