@@ -586,8 +586,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         barrier_arrive(&sm.v_full[buffer]);
         load(block + 1, c.v, v);
       }
-    } else if (lane == 0) {
+    } else {
       // ---- products ----
+      const bool leader = elected();
       constexpr uint32_t kScores = 1u << 4 | (kBlock / 8) << 17 | (kRows / 16) << 24;
       constexpr uint32_t kOutputs = 1u << 4 | 1u << 16 | (D / 8) << 17 | (kRows / 16) << 24;
       const auto scores = [&](int block) {
@@ -596,19 +597,23 @@ __global__ void __launch_bounds__(kThreads, 2)
         // the P that these scores replace has been used; a chunk's first block waits for all
         const int used = block == 0 ? n - 1 : n - 2;
         if (used >= 0) ok = ok && was_added(used);
+        ok = __all_sync(~0u, ok);
         if (!ok) return;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        if (leader) {
 #pragma unroll
-        for (int line = 0; line < kLines; ++line) {
-          const uint64_t q = operand(shared_address(sm.q[line]));
-          const uint64_t k = operand(shared_address(sm.k[buffer][line]));
+          for (int line = 0; line < kLines; ++line) {
+            const uint64_t q = operand(shared_address(sm.q[line]));
+            const uint64_t k = operand(shared_address(sm.k[buffer][line]));
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            tensor_mma(tensor + kS + buffer * kBlock, q + 2 * i, k + 2 * i, kScores,
-                       line > 0 || i > 0);
+            for (int i = 0; i < 4; ++i)
+              tensor_mma(tensor + kS + buffer * kBlock, q + 2 * i, k + 2 * i, kScores,
+                         line > 0 || i > 0);
+          }
+          tensor_commit(&sm.k_free[buffer]);
+          tensor_commit(&sm.scored[buffer]);
         }
-        tensor_commit(&sm.k_free[buffer]);
-        tensor_commit(&sm.scored[buffer]);
+        __syncwarp();
       };
       scores(0);
       if (blocks > 1) scores(1);
@@ -616,15 +621,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int n = done + block, buffer = n & 1;
         ok = barrier_wait(&sm.v_full[buffer], (n >> 1) & 1, failed);
         ok = ok && barrier_wait(&sm.weighed[buffer], (n >> 1) & 1, failed);
+        ok = __all_sync(~0u, ok);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint64_t v = operand_across(shared_address(sm.v[buffer][0]), kBlock * 128);
+        if (leader) {
+          const uint64_t v = operand_across(shared_address(sm.v[buffer][0]), kBlock * 128);
 #pragma unroll
-        for (int k = 0; k < kBlock / 16; ++k)  // 16 tokens: 8 columns of P, 2 KB of V
-          tensor_mma_from(tensor, tensor + kS + buffer * kBlock + 8 * k, v + 128 * k, kOutputs,
-                          n > 0 || k > 0);
-        tensor_commit(&sm.v_free[buffer]);
-        tensor_commit(&sm.added[buffer]);
+          for (int k = 0; k < kBlock / 16; ++k)  // 16 tokens: 8 columns of P, 2 KB of V
+            tensor_mma_from(tensor, tensor + kS + buffer * kBlock + 8 * k, v + 128 * k, kOutputs,
+                            n > 0 || k > 0);
+          tensor_commit(&sm.v_free[buffer]);
+          tensor_commit(&sm.added[buffer]);
+        }
+        __syncwarp();
         if (block + 2 < blocks) scores(block + 2);
       }
     }
@@ -667,13 +676,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
   }
-  if (tid == kIssueWarp * 32) {
+  if (warp == kIssueWarp) {
     // what was issued ends before the shared memory and the tensor memory go
     int none = 0;
-    tensor_commit(&sm.drained);
+    if (elected()) tensor_commit(&sm.drained);
+    __syncwarp();
     barrier_wait(&sm.drained, 0, &none);
   }
-  __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");

@@ -492,23 +492,25 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     } else {
       // ---- products, by one thread ----
-      if (lane == 0) {
-        constexpr uint32_t kType = kFp16 ? 0u : 1u;
-        constexpr uint32_t kind = 1u << 4 | kType << 7 | kType << 10 | (kColumns / 8) << 17 |
-                                  (kLanes / 16) << 24;
-        for (int i = 0; i < items && ok; ++i) {
-          const int item_tiles = sm.item[i].tiles;
-          if (item_tiles == 0) continue;
-          for (int tile = 0; tile < item_tiles && ok; ++tile, ++tiles) {
-            const int buffer = tiles & 1;
-            if (tiles >= 2) ok = barrier_wait(&sm.free[buffer], ((tiles >> 1) - 1) & 1, failed);
-            for (int chunk = 0; chunk < kChunks && ok; ++chunk, ++steps) {
-              const int s = steps % kStages;
-              if (tile == 0) ok = barrier_wait(&sm.filled[chunk], columns_filled & 1, failed);
-              if (ok) ok = barrier_wait(&sm.full[s], (steps / kStages) & 1, failed);
-              if (!ok) break;
-              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      constexpr uint32_t kType = kFp16 ? 0u : 1u;
+      constexpr uint32_t kind = 1u << 4 | kType << 7 | kType << 10 | (kColumns / 8) << 17 |
+                                (kLanes / 16) << 24;
+      const bool leader = elected();
+      for (int i = 0; i < items && ok; ++i) {
+        const int item_tiles = sm.item[i].tiles;
+        if (item_tiles == 0) continue;
+        for (int tile = 0; tile < item_tiles && ok; ++tile, ++tiles) {
+          const int buffer = tiles & 1;
+          if (tiles >= 2) ok = barrier_wait(&sm.free[buffer], ((tiles >> 1) - 1) & 1, failed);
+          for (int chunk = 0; chunk < kChunks; ++chunk, ++steps) {
+            const int s = steps % kStages;
+            if (tile == 0) ok = ok && barrier_wait(&sm.filled[chunk], columns_filled & 1, failed);
+            ok = ok && barrier_wait(&sm.full[s], (steps / kStages) & 1, failed);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (leader) {
               const uint64_t pages = operand(shared_address(sm.pages[s]));
               const uint64_t columns = operand(shared_address(sm.columns[chunk]));
 #pragma unroll
@@ -517,22 +519,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                            chunk > 0 || k > 0);
               tensor_commit(&sm.empty[s]);
               if (tile == item_tiles - 1) tensor_commit(&sm.released[chunk]);
+              if (chunk == kChunks - 1) tensor_commit(&sm.done[buffer]);
             }
-            if (ok) tensor_commit(&sm.done[buffer]);
+            __syncwarp();
           }
-          ++columns_filled;
         }
+        ++columns_filled;
       }
-      __syncwarp();
     }
   }
-  if (tid == kIssueWarp * 32) {
+  if (warp == kIssueWarp) {
     // what was issued ends before the shared memory and the tensor memory go
     int none = 0;
-    tensor_commit(&sm.drained);
+    if (elected()) tensor_commit(&sm.drained);
+    __syncwarp();
     barrier_wait(&sm.drained, 0, &none);
   }
-  __syncwarp();
   asm volatile("cp.async.wait_all;" ::: "memory");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();

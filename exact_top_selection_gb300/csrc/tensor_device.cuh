@@ -46,6 +46,16 @@ __device__ __forceinline__ bool barrier_wait(uint64_t* b, uint32_t parity, volat
   return false;
 }
 
+// One lane of a converged warp, always the same.  The other lanes go along up to the instructions
+// that only one thread issues, so that what those take is uniform.
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p;\nelect.sync _|p, 0xFFFFFFFF;\nselp.u32 %0, 1, 0, p;\n}"
+      : "=r"(r));
+  return r != 0u;
+}
+
 // Operand in lines of 128 bytes, 8 of them to a swizzled block of 1024 bytes.
 __device__ __forceinline__ uint64_t operand(uint32_t address) {
   return (uint64_t)((address & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
