@@ -196,12 +196,19 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
   p.page_size = page_size;
   p.table_width = table_width;
   p.num_blocks = num_blocks;
-  // Columns: the fewest that hold a sequence's rows for one key head (their mean
-  // number where they differ), at most 32 and 8 tokens.
+  // Columns of a tile: 8 as a rule, more only where a key head has more query heads. Wider tiles
+  // share pages between tokens, but are fewer and their products and joins longer. Over listed
+  // pages 8 columns were the fastest or within 4% of it from 4 to 512 rows of a sequence (8 tokens
+  // of 32 sequences x 16 heads over 32 pages: 50 us, 16 columns 58, 32 columns 56; 32 tokens of one:
+  // 17, 21 and 30). Over the whole cache 16 columns win once passes of 8 would read 256 MB (262 MB:
+  // 43.7 us with 8, 44.4 with 16; 524 MB: 67.2 and 60.3; 2.1 GB: 230 and 161; 65 MB: 20.5 and 23.3).
   const int group = q_heads / kv_heads;
   const int64_t mean = single_rows ? 1 : (num_tokens + num_seqs - 1) / num_seqs;
-  const int64_t tokens = mean < 1 ? 1 : (mean < 8 ? mean : 8);
-  p.columns = group * tokens <= 8 ? 8 : (group * tokens <= 16 ? 16 : 32);
+  const int64_t passes = (mean * group + 7) / 8;
+  const double read = (double)num_seqs * kv_heads * table_width * page_size * 2 * head_dim *
+                      (double)passes;
+  p.columns = group > 16 ? 32 : (group > 8 ? 16 : 8);
+  if (group <= 8 && num_blocks == 0 && passes > 1 && read >= 256e6) p.columns = 16;
   p.tile_heads = group < p.columns ? group : p.columns;
   p.tile_tokens = p.columns / p.tile_heads < 8 ? p.columns / p.tile_heads : 8;
   if (single_rows) p.tile_tokens = 1;
@@ -212,16 +219,19 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
   p.min_units = 256 / page_size;
   p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;
   // The prompt's kernel takes 128 rows (tokens x heads) at a time and does not split a tile: it
-  // wants filled tiles, and at least as many of them as there are SMs.
+  // wants tiles that a sequence fills, and enough of them. Over the whole cache it wins from
+  // about 6000 rows on (16 heads x 256 tokens over 8192: 146 us against 110, 512 tokens: 146 against
+  // 203). Over listed pages it also depends on how many of them neighbours share: 16 heads x 512
+  // tokens over 32 pages of 512 each take 58 us against 84 where most are shared, and 221 against
+  // 84 where none are; 1024 tokens 61 against 138, 2048 tokens without any shared 272 against 288.
   const int prompt_heads = group < kPromptRows ? group : kPromptRows;
   const int prompt_tokens =
       kPromptRows / prompt_heads < kPromptTokens ? kPromptRows / prompt_heads : kPromptTokens;
-  const int64_t prompt_tiles = num_tokens / prompt_tokens * kv_heads *
-                               ((group + prompt_heads - 1) / prompt_heads);
+  const int64_t prompt_rows = num_blocks > 0 ? 16384 : 6144;
   const bool prompt_fits = num_blocks == 0 || table_width <= kPromptListedWidth;
   if (prompt > 0 && !prompt_fits) return EXACT_TOPK_ERR_BAD_PLAN;
   if (prompt > 0 || (prompt < 0 && prompt_fits && !single_rows && mean >= prompt_tokens &&
-                     prompt_tiles >= info->sm_count)) {
+                     num_tokens * q_heads >= prompt_rows)) {
     p.prompt_tokens = prompt_tokens;
     p.prompt_heads = prompt_heads;
   }

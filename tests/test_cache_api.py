@@ -35,8 +35,9 @@ def test_error_strings():
 
 @pytest.mark.parametrize("tokens,seqs,single,q_heads,heads,columns,tile_tokens,tile_heads", [
     (64, 64, True, 32, 4, 8, 1, 8), (64, 64, True, 4, 4, 8, 1, 1), (3, 3, True, 12, 1, 16, 1, 12),
-    (24, 8, False, 8, 2, 16, 4, 4), (4096, 1, False, 16, 2, 32, 4, 8), (100, 1, False, 1, 1, 8, 8, 1),
-    (7, 7, True, 80, 2, 32, 1, 32), (100, 1, False, 6, 2, 32, 8, 3), (0, 1, False, 1, 1, 8, 8, 1),
+    (24, 8, False, 8, 2, 8, 2, 4), (4096, 1, False, 16, 2, 16, 2, 8), (100, 1, False, 1, 1, 8, 8, 1),
+    (7, 7, True, 80, 2, 32, 1, 32), (100, 1, False, 6, 2, 8, 2, 3), (0, 1, False, 1, 1, 8, 8, 1),
+    (64, 16, False, 16, 4, 8, 2, 4), (1024, 256, False, 16, 4, 16, 4, 4), (24, 3, False, 24, 1, 32, 1, 24),
 ])
 def test_plan(tokens, seqs, single, q_heads, heads, columns, tile_tokens, tile_heads):
     p = etk.make_attention_plan(tokens, seqs, q_heads, heads, 128, 64, 100, 0, single, GB300)
