@@ -24,8 +24,7 @@ ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["topk_kernels.cu", "cache_kernels.cu", "score_kernels.cu",
                 "attention_kernels.cu", "prompt_attention_kernels.cu"]
 HOST_SOURCES = ["exact_topk_api.cpp", "cache_api.cpp"]
-HEADERS = ["etk_internal.h", "cache_internal.h", "cache_device.cuh", "tensor_device.cuh",
-           "tensor_map.h"]
+HEADERS = ["etk_internal.h", "cache_internal.h", "cache_device.cuh", "tensor_device.cuh"]
 PUBLIC_HEADERS = ["exact_topk.h", "exact_topk_cache.h"]
 
 

@@ -116,7 +116,7 @@ const char* exact_topk_error_string(int status) {
              "<= 1024, type bf16 or fp16";
     case EXACT_TOPK_ERR_BAD_BATCH:
       return "bad batch: need 1 <= num_seqs <= 4096, table_width * page_size <= 2^30, num_tokens == "
-             "num_seqs without q_start, table_width <= 131072 with a page list";
+             "num_seqs without q_start, table_width <= 65536 with a page list";
     case EXACT_TOPK_ERR_BAD_HEADS:
       return "bad heads: need q_heads a multiple of kv_heads, at most 65536";
     default:

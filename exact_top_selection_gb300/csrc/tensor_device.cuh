@@ -21,13 +21,6 @@ __device__ __forceinline__ void barrier_arrive(uint64_t* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_address(b)) : "memory");
 }
 
-// An arrival, with `bytes` that copies to shared memory will complete in this phase.
-__device__ __forceinline__ void barrier_expect(uint64_t* b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(shared_address(b)),
-               "r"(bytes)
-               : "memory");
-}
-
 // False when the barrier's phase did not complete in time, or another wait has given up.
 __device__ __forceinline__ bool barrier_wait(uint64_t* b, uint32_t parity, volatile int* failed) {
   for (uint32_t i = 0; i < kWaitLimit; ++i) {

@@ -41,7 +41,6 @@
 #include <mutex>
 
 #include "etk_internal.h"
-#include "tensor_map.h"
 
 namespace etk {
 namespace {
@@ -3851,6 +3850,26 @@ int set_attrs(KernelT kernel, int family, size_t smem) {
     return EXACT_TOPK_ERR_CUDA;
   if (cached) g_attr_smem[dev][family] = (int)smem;
   return EXACT_TOPK_OK;
+}
+
+// cuTensorMapEncodeTiled, reached through the runtime's driver entry point
+// (no link-time dependency on the driver library); null when unavailable.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled() {
+  static std::once_flag once;
+  static EncodeTiledFn fn = nullptr;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
 }
 
 // The persistent kernel's view map (Params::view_map): the scores of row z as

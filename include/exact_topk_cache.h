@@ -37,7 +37,7 @@ extern "C" {
 
 /* Limits checked on the host (EXACT_TOPK_ERR_BAD_BATCH beyond them). */
 #define EXACT_TOPK_MAX_SEQS 4096
-#define EXACT_TOPK_MAX_LISTED_WIDTH 131072 /* table_width of a call with a page list */
+#define EXACT_TOPK_MAX_LISTED_WIDTH 65536 /* table_width of a call with a page list */
 
 /* Exponents that a written scale may have: scale = 2^e, e in [MIN, MAX]. */
 #define EXACT_TOPK_SCALE_MIN_EXP (-40)

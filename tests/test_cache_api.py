@@ -53,12 +53,12 @@ def test_plan_refusals():
     etk.make_attention_plan(**good)
     for code, bad in ((-9, dict(head_dim=96)), (-9, dict(page_size=48)), (-9, dict(kv_heads=0)), (-10, dict(num_tokens=9)),
                       (-10, dict(num_seqs=0, num_tokens=0)), (-10, dict(num_seqs=4097, num_tokens=4097)), (-10, dict(table_width=0)),
-                      (-10, dict(table_width=131073)), (-10, dict(num_tokens=-1)), (-10, dict(table_width=1 << 25)),
+                      (-10, dict(table_width=65537)), (-10, dict(num_tokens=-1)), (-10, dict(table_width=1 << 25)),
                       (-11, dict(q_heads=7)), (-11, dict(q_heads=0)), (-3, dict(num_blocks=-1)), (-3, dict(num_blocks=16385))):
         with pytest.raises(etk.ExactTopKError) as e:
             etk.make_attention_plan(**{**good, **bad})
         assert e.value.code == code, bad
-    etk.make_attention_plan(**{**good, "table_width": 131073, "num_blocks": 0})
+    etk.make_attention_plan(**{**good, "table_width": 65537, "num_blocks": 0})
     with pytest.raises(etk.ExactTopKError) as e:
         etk.make_attention_plan(**{**good, "table_width": 24577, "prompt": 1})
     assert e.value.code == -7
