@@ -19,7 +19,8 @@ int check_cache(const exact_topk_cache* cache, CacheArgs* out) {
       cache->k_scale == nullptr || cache->v_scale == nullptr)
     return EXACT_TOPK_ERR_NULL_POINTER;
   if (cache->num_pages < 1 || cache->kv_heads < 1 || cache->kv_heads > 1024 ||
-      (int64_t)cache->num_pages * cache->kv_heads > 0x7FFFFFFF || !page_size_ok(cache->page_size) || (cache->head_dim != 64 && cache->head_dim != 128) ||
+      (int64_t)cache->num_pages * cache->kv_heads > 0x7FFFFFFF ||
+      !page_size_ok(cache->page_size) || (cache->head_dim != 64 && cache->head_dim != 128) ||
       (cache->type != EXACT_TOPK_TYPE_BF16 && cache->type != EXACT_TOPK_TYPE_FP16))
     return EXACT_TOPK_ERR_BAD_CACHE;
   if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(cache->key_bounds, 16) ||
@@ -196,12 +197,13 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
   p.page_size = page_size;
   p.table_width = table_width;
   p.num_blocks = num_blocks;
-  // Columns of a tile: 8 as a rule, more only where a key head has more query heads. Wider tiles
-  // share pages between tokens, but are fewer and their products and joins longer. Over listed
-  // pages 8 columns were the fastest or within 4% of it from 4 to 512 rows of a sequence (8 tokens
-  // of 32 sequences x 16 heads over 32 pages: 50 us, 16 columns 58, 32 columns 56; 32 tokens of one:
-  // 17, 21 and 30). Over the whole cache 16 columns win once passes of 8 would read 256 MB (262 MB:
-  // 43.7 us with 8, 44.4 with 16; 524 MB: 67.2 and 60.3; 2.1 GB: 230 and 161; 65 MB: 20.5 and 23.3).
+  // Columns of a tile: 8 as a rule, more only where a key head has more query heads. Wider
+  // tiles share pages between tokens, but are fewer and their products and joins longer. Over
+  // listed pages 8 columns were the fastest or within 4% of it from 1 to 256 tokens of a sequence
+  // (8 tokens of 32 sequences x 16 heads over 32 pages: 50 us, 16 columns 58, 32 columns 56; 32
+  // tokens of one: 17, 21 and 30; 256: 44, 53 and 49; 512: 84, 88 and 75). Over the whole cache
+  // 16 columns win once passes of 8 would read 256 MB (65 MB: 20.5 us with 8, 23.3 with 16; 262 MB:
+  // 43.7 and 44.4; 524 MB: 67.2 and 60.3; 2.1 GB: 230 and 161), and 32 lose to them (94 and 170).
   const int group = q_heads / kv_heads;
   const int64_t mean = single_rows ? 1 : (num_tokens + num_seqs - 1) / num_seqs;
   const int64_t passes = (mean * group + 7) / 8;
@@ -219,8 +221,8 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
   p.min_units = 256 / page_size;
   p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;
   // The prompt's kernel takes 128 rows (tokens x heads) at a time and does not split a tile: it
-  // wants tiles that a sequence fills, and enough of them. Over the whole cache it wins from
-  // about 6000 rows on (16 heads x 256 tokens over 8192: 146 us against 110, 512 tokens: 146 against
+  // wants tiles that a sequence fills, and enough of them. Over the whole cache it wins from about
+  // 6000 rows on (16 heads x 256 tokens over 8192: 146 us against 110, 512 tokens: 146 against
   // 203). Over listed pages it also depends on how many of them neighbours share: 16 heads x 512
   // tokens over 32 pages of 512 each take 58 us against 84 where most are shared, and 221 against
   // 84 where none are; 1024 tokens 61 against 138, 2048 tokens without any shared 272 against 288.

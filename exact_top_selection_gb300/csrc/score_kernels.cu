@@ -76,6 +76,8 @@ __device__ __forceinline__ uint32_t clamp_sign(uint32_t w, bool positive) {
 // Both operands come from global memory straight into fragments: the order of the
 // contraction is free, so each lane takes 16 contiguous bytes of a page's row and of a
 // column (lane % 4 chunks of 8 channels), which makes 64-byte segments of every load.
+// 64 sequences of up to 1024 pages, 4 x 8 heads of 128 channels (75 MB): 15.5 us; with a CTA for
+// every 64 pages, and their ids not asked for ahead, 19.9.
 // A group of more than 8 heads takes several passes; the maxima are kept between them.
 template <bool kFp16, int D>
 __global__ void __launch_bounds__(kThreads) score_step_kernel(CacheArgs c, BatchArgs b,
