@@ -78,10 +78,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
-  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-}
-
 // Operand whose contraction runs over the lines: 64 channels to a line, `chunk` bytes from one
 // 64 channels to the next.
 __device__ __forceinline__ uint64_t operand_across(uint32_t address, uint32_t chunk) {
@@ -346,6 +342,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         e.pos = most;
         e.k_scale = 0.f;
         e.v_part = 1.f;
+        e.v_power = 0x3C003C00u;
         continue;
       }
       if (!listed) {
@@ -358,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         e.members = 0u;
         e.k_scale = 0.f;
         e.v_part = 1.f;
+        e.v_power = 0x3C003C00u;
         continue;
       }
       const int64_t tile = (int64_t)page * c.heads + head;
@@ -512,20 +510,34 @@ __global__ void __launch_bounds__(kThreads, 2)
       const auto entry_of = [&](int block, int i) -> const Entry& {
         return sm.entry[(block << per_block_shift) + ((first + i * 8) >> part_tokens_shift)];
       };
+      // Loads without branches, so that nothing waits for them: of an absent part they take the
+      // cache's first page, behind the last block its last one, behind the sequence's end what
+      // the page holds. `clear` puts zeros for the first and the last.
       const auto load = [&](int block, const uint8_t* codes, uint4 (&x)[2][kLines]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int line = 0; line < kLines; ++line) x[i][line] = make_uint4(0u, 0u, 0u, 0u);
-          if (block >= blocks) continue;
-          const Entry& e = entry_of(block, i);
+          const Entry& e = entry_of(block < blocks ? block : blocks - 1, i);
           const int in_part = (first + i * 8) & ((1 << part_tokens_shift) - 1);
-          if (e.offset < 0 || e.pos + in_part >= most) continue;
-          const uint8_t* const at = codes + e.offset + in_part * D + chunk * 16;
+          const uint8_t* const at =
+              codes + (e.offset < 0 ? 0 : e.offset) + in_part * D + chunk * 16;
 #pragma unroll
           for (int line = 0; line < kLines; ++line)
             x[i][line] = __ldg(reinterpret_cast<const uint4*>(at + line * 64));
         }
+      };
+      const auto there = [&](int block, int i) {
+        const Entry& e = entry_of(block, i);
+        return e.offset >= 0 && e.pos + ((first + i * 8) & ((1 << part_tokens_shift) - 1)) < most;
+      };
+      // Zeros for what is not there; most blocks have everything.
+      const auto clear = [&](int block, uint4 (&x)[2][kLines]) {
+        const bool in_place[2] = {there(block, 0), there(block, 1)};
+        if (__all_sync(~0u, in_place[0] && in_place[1])) return;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (!in_place[i])
+#pragma unroll
+            for (int line = 0; line < kLines; ++line) x[i][line] = make_uint4(0u, 0u, 0u, 0u);
       };
       const int place0 = first * 128 + (((chunk * 2) ^ (first & 7)) << 4);  // + 8 tokens: 1024
       const auto place = [&](uint8_t (&lines)[kLines][kBlock * 128], int i,
@@ -557,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int n = done + block, buffer = n & 1;
         if (n >= 2) ok = ok && barrier_wait(&sm.k_free[buffer], ((n >> 1) - 1) & 1, failed);
         if (!ok) return;
+        clear(block, k);
 #pragma unroll
         for (int i = 0; i < 2; ++i) place(sm.k[buffer], i, k[i], 0x3C003C00u);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -573,17 +586,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int n = done + block, buffer = n & 1;
         if (n >= 2) ok = ok && barrier_wait(&sm.v_free[buffer], ((n >> 1) - 1) & 1, failed);
         if (!ok) break;
-        uint32_t bad = 0u;
+        clear(block, v);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const Entry& e = entry_of(block, i);
-          place(sm.v[buffer], i, v[i], e.offset >= 0 ? e.v_power : 0x3C003C00u);
-#pragma unroll
-          for (int line = 0; line < kLines; ++line)
-            bad |= nan_codes(v[i][line].x) | nan_codes(v[i][line].y) |
-                   nan_codes(v[i][line].z) | nan_codes(v[i][line].w);
-        }
-        if (bad != 0u) sm.again = 1;
+        for (int i = 0; i < 2; ++i)
+          place(sm.v[buffer], i, v[i], entry_of(block, i).v_power);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         barrier_arrive(&sm.v_full[buffer]);
         load(block + 1, c.v, v);
@@ -645,8 +651,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // ---- outputs ----
   if (tid < kRows) {
-    // NaN among scores: of this row's own, or of a part that it does not take
-    if (l != l) sm.again = 1;
+    float nan = l;  // NaN among scores, of this row's own or of a part that it does not take
     if (done > 0) {
       ok = ok && was_added(done - 1);
       ok = __all_sync(~0u, ok);
@@ -662,6 +667,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (done > 0) {
         tensor_load32(tensor + lane_base + i, v);
         tensor_wait(v);
+        // a NaN among the values has reached every row by now
+#pragma unroll
+        for (int k = 0; k < 32; ++k) nan = fmaf(v[k], 0.f, nan);
       }
       if (row < live && ok) {
 #pragma unroll
@@ -677,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
     }
+    if (nan != nan) sm.again = 1;
   }
   if (warp == kIssueWarp) {
     // what was issued ends before the shared memory and the tensor memory go
