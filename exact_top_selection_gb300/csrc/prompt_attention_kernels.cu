@@ -203,50 +203,55 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
 
-  // ---- queries: a row a warp at a time, 8 of them on their way ----
+  // ---- queries: 8 channels a lane, all of a warp's 16 rows on their way ----
   if (warp < kIssueWarp) {
-    constexpr int kEach = D / 32;  // channels of a lane
-    for (int r0 = warp; r0 < kRows; r0 += kIssueWarp * 8) {
-      uint32_t w[8][kEach / 2];
+    constexpr int kLanes = D / 8, kStepRows = 32 / kLanes;  // lanes of a row, rows of a step
+    constexpr int kSteps = kRows / kIssueWarp / kStepRows;
+    const int piece = lane % kLanes;
+    uint4 w[kSteps];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int row = r0 + k * kIssueWarp;
-        const int token = row / heads;
-        const uint32_t* const at = reinterpret_cast<const uint32_t*>(
+    for (int k = 0; k < kSteps; ++k) {
+      const int row = (warp * kSteps + k) * kStepRows + lane / kLanes;
+      const int token = row / heads;
+      w[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < live)
+        w[k] = __ldg(reinterpret_cast<const uint4*>(
             static_cast<const uint16_t*>(a.q.data) + (row0 + token) * a.q.token_stride +
             ((int64_t)head * a.group + head0 + row - token * heads) * a.q.head_stride +
-            lane * kEach);
+            piece * 8));
+    }
 #pragma unroll
-        for (int i = 0; i < kEach / 2; ++i) w[k][i] = row < live ? __ldg(at + i) : 0u;
+    for (int k = 0; k < kSteps; ++k) {
+      const int row = (warp * kSteps + k) * kStepRows + lane / kLanes;
+      const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      float2 x[4];
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = c.fp16 ? unpack2<true>(u[i]) : unpack2<false>(u[i]);
+        top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int row = r0 + k * kIssueWarp;
-        float2 x[kEach / 2];
-        float top = 0.f;
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+      int e = (int)(__float_as_uint(top) >> 23) - 127;
+      if (e == 128 || top == 0.f) e = 8;
+      int up = 8 - e;
+      up = up < -120 ? -120 : (up > 120 ? 120 : up);
+      // the scale's sign goes into the queries, so that a row's largest score is its largest
+      // product
+      const float by = copysignf(__uint_as_float((uint32_t)(up + 127) << 23), a.scale_log2);
 #pragma unroll
-        for (int i = 0; i < kEach / 2; ++i) {
-          x[i] = c.fp16 ? unpack2<true>(w[k][i]) : unpack2<false>(w[k][i]);
-          top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        int e = (int)(__float_as_uint(top) >> 23) - 127;
-        if (e == 128 || top == 0.f) e = 8;
-        int up = 8 - e;
-        up = up < -120 ? -120 : (up > 120 ? 120 : up);
-        // the scale's sign goes into the queries, so that a row's largest score is its largest
-        // product
-        const float by = copysignf(__uint_as_float((uint32_t)(up + 127) << 23), a.scale_log2);
-        const int channel = lane * kEach, line = channel / 64, piece = channel % 64 / 8;
-        uint32_t* const to = reinterpret_cast<uint32_t*>(
-            &sm.q[line][row * 128 + ((piece ^ (row & 7)) << 4) + channel % 8 * 2]);
-#pragma unroll
-        for (int i = 0; i < kEach / 2; ++i) to[i] = pack2<true>(x[i].x * by, x[i].y * by);
-        if (lane == 0)
-          sm.factor[row] =
-              row < live ? __uint_as_float((uint32_t)(127 - up) << 23) * fabsf(a.scale_log2) : 0.f;
+      for (int i = 0; i < 4; ++i) {
+        x[i].x *= by;
+        x[i].y *= by;
       }
+      *reinterpret_cast<uint4*>(
+          &sm.q[piece / 8][row * 128 + (((piece & 7) ^ (row & 7)) << 4)]) =
+          make_uint4(pack2<true>(x[0].x, x[0].y), pack2<true>(x[1].x, x[1].y),
+                     pack2<true>(x[2].x, x[2].y), pack2<true>(x[3].x, x[3].y));
+      if (piece == 0)
+        sm.factor[row] =
+            row < live ? __uint_as_float((uint32_t)(127 - up) << 23) * fabsf(a.scale_log2) : 0.f;
     }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
