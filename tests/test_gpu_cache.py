@@ -142,7 +142,8 @@ def test_every_page_of_a_long_batch():
                                       ([3, 0, 70], [5, 2, 9]), ([2000, 64, 65], [1, 1, 1])])
 @pytest.mark.parametrize("page,dim,heads,group,dtype", [(16, 64, 2, 8, BF16), (32, 128, 1, 1, FP16),
                                                         (64, 128, 2, 3, BF16), (16, 128, 1, 12, FP16),
-                                                        (128, 64, 3, 4, FP16), (16, 128, 2, 16, BF16)])
+                                                        (128, 64, 3, 4, FP16), (16, 128, 2, 16, BF16),
+                                                        (32, 64, 1, 40, FP16)])
 def test_scores(lens, new, page, dim, heads, group, dtype):
     tensors, batch = ref.make(20, lens, new, heads, page, dim, dtype)
     T = sum(new) + 2
@@ -167,7 +168,8 @@ def test_scores(lens, new, page, dim, heads, group, dtype):
 
 
 @pytest.mark.parametrize("heads,group,page,dim,dtype", [(2, 4, 64, 128, BF16), (1, 8, 16, 64, FP16), (1, 1, 32, 128, FP16),
-                                                        (1, 5, 16, 128, BF16)])
+                                                        (1, 5, 16, 128, BF16), (1, 12, 16, 64, BF16), (1, 20, 64, 128, FP16),
+                                                        (1, 2, 16, 64, FP16), (1, 33, 32, 64, BF16)])
 def test_scores_of_a_prompt(heads, group, page, dim, dtype):
     """Hundreds of rows of a sequence against hundreds of pages, causally ragged."""
     lens, new = [5000, 777], [391, 300]
@@ -593,6 +595,109 @@ def test_a_captured_step_replays_with_new_contents():
         want, tol = ref.attention(plain, batch, hq, None, 1 / math.sqrt(dim), MARK)
         assert ((dense.cpu().double() - want).abs() <= tol).all()
     assert not whole.counters.any() and not step.attention.counters.any()
+
+
+def test_a_captured_prompt_replays_with_new_contents():
+    """Scores and attention of prompts in one graph: lengths, row ranges, rows and caches change."""
+    heads, group, page, dim, B, width, T = 1, 8, 32, 64, 3, 30, 100
+    tensors, batch = ref.make(85, [width * page] * B, [40, 30, 30], heads, page, dim, FP16, poison=False)
+    cache, dev_batch = device_cache(tensors), device_batch(batch)
+    q = torch.zeros(T, heads * group, dim, dtype=FP16, device="cuda")
+    out = torch.zeros_like(q)
+    scores = torch.zeros(T * heads, width, device="cuda")
+    ke = torch.zeros(T * heads, dtype=torch.int32, device="cuda")
+    blocks = torch.zeros(T * heads, 5, dtype=torch.int32, device="cuda")
+    whole = etk.CacheAttention(cache, B, T, heads * group, width, prompt=1)
+    listed = etk.CacheAttention(cache, B, T, heads * group, width, num_blocks=5, prompt=1)
+    listed_out = torch.zeros_like(q)
+
+    def run():
+        etk.block_scores(cache, dev_batch, q, 0, 1, scores, ke)
+        whole(q, dev_batch, out=out)
+        listed(q, dev_batch, blocks=blocks, out=listed_out)
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        run()
+    stream.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        run()
+    for rep, (lens, new) in enumerate((([960, 70, 31], [60, 39, 1]), ([33, 500, 900], [33, 0, 60]), ([0, 1, 960], [0, 1, 99]))):
+        tensors, batch = ref.make(86 + rep, [width * page] * B, [0] * B, heads, page, dim, FP16, poison=False)
+        if rep == 1:  # what the prompt's kernel leaves to the other one
+            tensors[1].view(torch.uint8)[batch[0][2, 3].long(), 0, 5, 9] = 0x7F
+        start = [sum(new[:i]) for i in range(B + 1)]
+        batch = (batch[0], torch.tensor(lens, dtype=torch.int32), torch.tensor(start, dtype=torch.int32))
+        for mine, other in zip((cache.k, cache.v, cache.k_scale, cache.v_scale, cache.key_bounds), tensors):
+            mine.copy_(other)
+        for mine, other in zip((dev_batch.page_table, dev_batch.kv_len, dev_batch.q_start), batch):
+            mine.copy_(other)
+        hq = ref.rows(89 + rep, T, heads * group, dim, FP16, 2.0)
+        lists = torch.randint(-1, width, (T * heads, 5), generator=torch.Generator().manual_seed(rep), dtype=torch.int32)
+        q.copy_(hq), blocks.copy_(lists)
+        for x in (out, listed_out, scores):
+            x.fill_(MARK)
+        ke.fill_(int(MARK))
+        graph.replay()
+        torch.cuda.synchronize()
+        plain = ref.Cache(*tensors)
+        for got, which in ((out, None), (listed_out, lists)):
+            want, tol = ref.attention(plain, batch, hq, which, 1 / math.sqrt(dim), MARK)
+            got = got.cpu().double()
+            assert torch.equal(got.isnan(), want.isnan())
+            fine = ~want.isnan()
+            assert ((got - want).abs()[fine] <= tol[fine]).all()
+        want, want_ke, size = ref.scores(plain, batch, hq, 0, 1, MARK)
+        assert torch.equal(ke.cpu(), want_ke)
+        got, fine = scores.cpu().double(), want.isfinite()
+        assert torch.equal(got[~fine], want[~fine])
+        assert ((got - want).abs()[fine] <= (2 * dim * 2.0 ** -23 * size)[fine]).all()
+
+
+def test_more_slots_than_pages():
+    """A selection of more pages than the table has: every page is taken, the rest is -1."""
+    lens, new, width = [40, 7], [3, 1], 3
+    tensors, batch = ref.make(115, lens, new, 2, 16, 64, BF16, width=width, poison=False)
+    cache, b = device_cache(tensors), device_batch(batch)
+    q = ref.rows(116, 4, 8, 64, BF16, 2.0)
+    step = etk.SparseAttention(cache, 2, 4, 8, width, 20, keep_first=2, keep_last=5)
+    out = step(q.cuda(), b).cpu().double()
+    want, tol = ref.attention(ref.Cache(*tensors), batch, q, None, 0.125, MARK)
+    assert ((out - want).abs() <= tol).all()
+    assert int((step.blocks >= 0).sum()) == 2 * (3 + 3 + 3 + 1)
+
+
+def test_host_threads_with_an_object_each():
+    import threading
+
+    lens, new = [2000, 300], [20, 9]
+    tensors, batch = ref.make(117, lens, new, 2, 16, 64, FP16)
+    cache, b = device_cache(tensors), device_batch(batch)
+    q = ref.rows(118, 29, 16, 64, FP16, 3.0).cuda()
+    objects = [etk.CacheAttention(cache, 2, 29, 16, b.table_width, prompt=i % 2) for i in range(4)]
+    want = [a(q, b).clone() for a in objects]
+    read = etk.cache_read(cache, b, num_tokens=29)
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(a, expect):
+        stream = torch.cuda.Stream()
+        for _ in range(25):
+            got = a(q, b, stream=stream)
+            rows = etk.cache_read(cache, b, num_tokens=29, stream=stream)
+            scores, ke = etk.block_scores(cache, b, q, stream=stream)
+            stream.synchronize()
+            if not torch.equal(got, expect) or not torch.equal(rows[0], read[0]):
+                failed.append(1)
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(objects, want)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not failed
 
 
 def test_two_streams_with_an_object_each():
