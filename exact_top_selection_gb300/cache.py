@@ -122,6 +122,12 @@ def _call(cache, stream, fn, *args):
         raise _etk.ExactTopKError(rc, fn.__name__)
 
 
+def _wait_for_buffers():
+    """Lets the current stream fill an object's buffers: its first call may be on another stream."""
+    if not torch.cuda.is_current_stream_capturing():
+        torch.cuda.current_stream().synchronize()
+
+
 def _rows(t, name, cache, heads, tokens=None):
     """Checks rows [num_tokens, heads, head_dim] and describes them."""
     dim = cache.head_dim
@@ -364,7 +370,7 @@ class CacheAttention:
     listed for each token and key head (``blocks`` int32 [num_tokens * kv_heads, K], as ExactTopK selects
     them: a set in any order, -1 and anything outside the pages that the token sees ignored, repeats counted
     once).  A row that sees nothing gives zeros.  Calls of one object must not overlap on the GPU: graphs
-    that may run at the same time each need an object of their own."""
+    that may run at the same time each need an object of their own.  Keep the object until its last call has run."""
 
     def __init__(self, cache, num_seqs, num_tokens, q_heads, table_width, num_blocks=0, **overrides):
         self.cache = cache
@@ -375,6 +381,7 @@ class CacheAttention:
             self.counters = torch.zeros(max(16, self.plan.counter_bytes), dtype=torch.uint8, device=cache.device)
             self.workspace = torch.empty(max(16, self.plan.workspace_bytes), dtype=torch.uint8,
                                          device=cache.device)
+            _wait_for_buffers()
         self._plan = ctypes.byref(self.plan)
         self._buffers = (self.counters.data_ptr(), self.counters.numel(), self.workspace.data_ptr(),
                          self.workspace.numel())
@@ -426,6 +433,8 @@ class SparseAttention:
         self.ke = torch.zeros(rows, dtype=torch.int32, device=dev)
         self.live = torch.zeros(1, dtype=torch.int32, device=dev)
         self.blocks = torch.full((rows, num_blocks), -1, dtype=torch.int32, device=dev)
+        with torch.cuda.device(dev):
+            _wait_for_buffers()
 
     def __call__(self, q, batch, k=None, v=None, out=None, scale=None, stream=None):
         """Attends with q [num_tokens, q_heads, head_dim]; rows k, v of the same tokens, where given, are

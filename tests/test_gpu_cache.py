@@ -719,6 +719,27 @@ def test_two_streams_with_an_object_each():
             assert torch.equal(x, want)
 
 
+def test_an_object_made_behind_other_work_and_used_on_another_stream():
+    lens, new, width = [4000, 100, 900], [1, 1, 1], 130
+    tensors, batch = ref.make(120, lens, new, 2, 32, 64, BF16, width=width, poison=False)
+    cache, b = device_cache(tensors), device_batch(batch, single=True)
+    q = ref.rows(121, 3, 8, 64, BF16, 3.0).cuda()
+    want = etk.CacheAttention(cache, 3, 3, 8, width)(q, b)
+    sparse = etk.SparseAttention(cache, 3, 3, 8, width, 6)(q, b)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    stale = [torch.full((1 << 18,), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]  # for the buffers to land in
+    del stale
+    torch.cuda._sleep(20_000_000)
+    attention = etk.CacheAttention(cache, 3, 3, 8, width)
+    got = attention(q, b, stream=stream)
+    torch.cuda._sleep(20_000_000)
+    step = etk.SparseAttention(cache, 3, 3, 8, width, 6)
+    got_sparse = step(q, b, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(got_sparse, sparse)
+
+
 def test_empty_calls_do_nothing():
     tensors, batch = ref.make(110, [30, 20], [0, 0], 1, 16, 64, BF16)
     cache, b = device_cache(tensors), device_batch(batch)
