@@ -222,14 +222,14 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
   p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;
   // The prompt's kernel takes 128 rows (tokens x heads) at a time and does not split a tile: it
   // wants tiles that a sequence fills, and enough of them. Over the whole cache it wins from about
-  // 6000 rows on (16 heads x 256 tokens over 8192: 146 us against 110, 512 tokens: 146 against
+  // 5000 rows on (16 heads x 256 tokens over 8192: 132 us against 110, 512 tokens: 133 against
   // 203). Over listed pages it also depends on how many of them neighbours share: 16 heads x 512
-  // tokens over 32 pages of 512 each take 58 us against 84 where most are shared, and 221 against
-  // 84 where none are; 1024 tokens 61 against 138, 2048 tokens without any shared 272 against 288.
+  // tokens over 32 pages of 512 each take 54 us against 84 where most are shared, and 198 against
+  // 84 where none are; 1024 tokens 55 against 138, 2048 tokens without any shared 248 against 288.
   const int prompt_heads = group < kPromptRows ? group : kPromptRows;
   const int prompt_tokens =
       kPromptRows / prompt_heads < kPromptTokens ? kPromptRows / prompt_heads : kPromptTokens;
-  const int64_t prompt_rows = num_blocks > 0 ? 16384 : 6144;
+  const int64_t prompt_rows = num_blocks > 0 ? 16384 : 5120;
   const bool prompt_fits = num_blocks == 0 || table_width <= kPromptListedWidth;
   if (prompt > 0 && !prompt_fits) return EXACT_TOPK_ERR_BAD_PLAN;
   if (prompt > 0 || (prompt < 0 && prompt_fits && !single_rows && mean >= prompt_tokens &&
@@ -262,6 +262,7 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
     return EXACT_TOPK_ERR_BAD_HEADS;
   if (plan->num_blocks < 0 || plan->num_blocks > EXACT_TOPK_MAX_K) return EXACT_TOPK_ERR_BAD_K;
   const int group = plan->q_heads / c.heads;
+  a.scale_log2 = scale * 1.4426950408889634f;
   if (plan->kv_heads != c.heads || plan->head_dim != c.dim || plan->page_size != c.page ||
       plan->table_width != b.width || plan->num_seqs != b.num_seqs ||
       (plan->num_blocks == 0 && blocks != nullptr) ||
@@ -270,7 +271,8 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
       plan->tile_heads > group || plan->tile_tokens < 1 || plan->tile_tokens > 8 ||
       plan->tile_tokens * plan->tile_heads > plan->columns || plan->workers < 1 ||
       plan->workers > most_workers(plan->columns, c.dim) || plan->min_units < 1 ||
-      !std::isfinite(scale) || plan->prompt_tokens < 0 || plan->prompt_tokens > kPromptTokens)
+      !std::isfinite(a.scale_log2) || plan->prompt_tokens < 0 ||
+      plan->prompt_tokens > kPromptTokens)
     return EXACT_TOPK_ERR_BAD_PLAN;
   // A tile of the kernel that runs behind the prompt's lies within one of that one's.
   if (plan->prompt_tokens > 0 &&
@@ -291,7 +293,6 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
   a.blocks = blocks;
   a.counters = static_cast<int32_t*>(counters);
   a.partial = static_cast<float*>(workspace);
-  a.scale_log2 = scale * 1.4426950408889634f;
   a.num_blocks = plan->num_blocks;
   a.group = group;
   a.columns = plan->columns;

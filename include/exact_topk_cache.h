@@ -175,6 +175,7 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
  * A row that sees nothing gets zeros. Scores, sums and outputs are FP32, rounded
  * once to the cache's type; the probabilities enter the second product in FP16.
  *   q, out      [num_tokens][q_heads][head_dim]; they must not overlap
+ *   scale       finite, as is scale * log2(e) (else BAD_PLAN); the scores must be finite in FP32
  *   blocks      NULL when plan->num_blocks is 0, else device int32
  *               [num_tokens * kv_heads][num_blocks]: pages by their place in the
  *               sequence, as exact_topk selects them. A list is a set: order does not

@@ -167,7 +167,7 @@ def test_attention_refuses_bad_plans_and_buffers():
     assert call(counters=fake(12) + 8) == -6 and call(workspace=fake(13) + 8) == -6
     assert call(num_blocks=2, blocks=fake(14) + 2) == -6
     assert call(blocks=fake(14)) == -7
-    for bad in (dict(scale=math.inf), dict(scale=math.nan), dict(kv_heads=1), dict(head_dim=64), dict(page_size=32), dict(table_width=4),
+    for bad in (dict(scale=math.inf), dict(scale=math.nan), dict(scale=3e38), dict(scale=-3e38), dict(kv_heads=1), dict(head_dim=64), dict(page_size=32), dict(table_width=4),
                 dict(num_seqs=3), dict(columns=24), dict(tile_tokens=0), dict(tile_tokens=9), dict(tile_heads=0), dict(tile_heads=5),
                 dict(tile_tokens=3), dict(prompt_tokens=33, prompt_heads=1), dict(prompt_tokens=-1),
                 dict(prompt_tokens=1, prompt_heads=0), dict(prompt_tokens=1, prompt_heads=3), dict(workers=609), dict(workers=0), dict(workers=1 << 20), dict(min_units=0)):
