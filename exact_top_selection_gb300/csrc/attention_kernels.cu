@@ -1,5 +1,5 @@
 // Attention over the paged 8-bit cache (exact_topk_attention_run): a row's
-// running maximum m, sum l and output O, in FP32, over its pages in one pass,
+// running maximum m (up to an offset), sum l and output O, in FP32, over its pages in one pass,
 //
 //   x_p = scale * (q . k_p) * k_scale,  m' = max(m, x_p),
 //   l' = l e^(m - m') + e^(x_p - m'),   O' = O e^(m - m') + e^(x_p - m') v_p.
@@ -22,8 +22,10 @@
 // Types. Codes are exact in FP16, so both products run in FP16 with FP32 sums. A
 // query row is brought to [2^8, 2^9) by a power of two: what is then below FP16's
 // normal range is off by 2^-25, against 2^8, less than FP32's own rounding of
-// the sum. Probabilities are at most 2^8 in FP16 (11 bits, against the 8 or 11 of
-// the output).
+// the sum. Probabilities are held in FP16 with the largest between 2^6 and 2^14: 11 bits
+// (against the 8 or 11 of the output) down to 2^-20 of it, below that off by at most 2^-31 of it.
+// The factor cancels in the quotient. With the largest between 1 and 2^8 instead, a flat tail
+// of 2^-26 each was lost from the outputs, but not from the sum that divides them.
 //
 // Work. Over the whole cache, all pages of all tiles form one line that the CTAs cut into
 // equal parts, whatever the lengths; a CTA's part may cover several tiles. Listed pages
@@ -47,10 +49,12 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 128;   // pages whose ids are held in shared memory at a time
-// The running maximum is raised only when a score is more than this above it (in
-// powers of two): probabilities then reach 2^8, and the sums are rescaled a few
-// times in a row's life instead of at each step.
-constexpr float kSlack = 8.f;
+// m, the exponent that a row's probabilities are relative to, is put kRoom powers of two below the
+// largest score so far, and moved again only when a score is more than kMost above it:
+// probabilities reach 2^14 at most, and the sums are rescaled a few times in a row's life
+// instead of at each step.
+constexpr float kRoom = 6.f;
+constexpr float kMost = 14.f;
 
 __device__ __forceinline__ float infinity() { return __uint_as_float(0x7F800000u); }
 
@@ -730,16 +734,17 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
           }
 #pragma unroll
           for (int r = 0; r < 4 * ST; ++r) high = fmaxf(high, y[r]);
-          if (__any_sync(~0u, high > kSlack)) {
+          if (__any_sync(~0u, high > kMost)) {
             float by[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              float best = m[n][j];
+              float best = -infinity();
 #pragma unroll
               for (int r = j; r < 4 * ST; r += 2) best = fmaxf(best, x[n][r]);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1)
                 best = fmaxf(best, __shfl_xor_sync(~0u, best, d));
+              best = fmaxf(m[n][j], best - kRoom);
               by[j] = m[n][j] == -infinity() ? 0.f : exp2_fast(m[n][j] - best);
               m[n][j] = best;
               l[n][j] *= by[j];

@@ -43,7 +43,8 @@ constexpr int kThreads = kRows + kConvert + 32;
 constexpr int kIssueWarp = (kRows + kConvert) / 32;
 constexpr int kBlock = 64;           // cached tokens of a block
 constexpr int kEntries = 128;        // parts of pages held at a time
-constexpr float kSlack = 8.f;        // see attention_kernels.cu
+constexpr float kRoom = 6.f;         // see attention_kernels.cu; with the part of a value's scale
+constexpr float kMost = 14.f;        // that is no power of two, below 2, all stays under 2^15
 constexpr int kFarthest = 12;        // powers of two between scales of values
 
 __device__ __forceinline__ float infinity() { return __uint_as_float(0x7F800000u); }
@@ -483,11 +484,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int i = 0; i < 8; ++i) p[k * 8 + i] = pack2<true>(y[i].x, y[i].y);
           }
-          const bool raise = high > (m == -infinity() ? m : kSlack);
+          const bool raise = high > (m == -infinity() ? m : kMost);
           if (!__any_sync(~0u, raise)) break;
           some = true;
           if (raise) {
-            const float best = base + high;
+            const float best = base + high - kRoom;
             by = m == -infinity() ? 0.f : exp2_fast(m - best);
             m = best;
             l *= by;

@@ -1,0 +1,124 @@
+"""The cache operators where the sizes of test_gpu_cache.py do not lead."""
+
+import math
+
+import pytest
+import torch
+
+import cache_reference as ref
+import exact_top_selection_gb300 as etk
+from test_gpu_cache import BF16, FP16, device_batch, device_cache
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- small probabilities ----
+
+def tailed(lens, new, page, dim, dtype, dominant):
+    """Sequences of one key head. Tokens at `dominant` (a function of the position) have a key of 1 in channel 0
+    and no value; all others a key of zeros and values of 32 to 64 in steps of 4."""
+    tensors, batch = ref.make(200, lens, new, 1, page, dim, dtype, poison=False)
+    k, v, k_scale, v_scale, _ = tensors
+    g = torch.Generator().manual_seed(201)
+    values = torch.randint(8, 17, (v.shape[0], 1, page, dim), generator=g).float() * 4
+    keys = torch.zeros(k.shape)
+    k_scale.fill_(2.0 ** -4), v_scale.fill_(1.0)
+    for b, n in enumerate(lens):
+        for p in (p for p in range(n) if dominant(p)):
+            at = int(batch[0][b, p // page])
+            keys[at, 0, p % page, 0] = 16.0
+            values[at, 0, p % page] = 0.0
+    k.copy_(keys.to(ref.FP8)), v.copy_(values.to(ref.FP8))
+    return tensors, batch
+
+
+def far(tokens, heads, dim, dtype, powers):
+    """Queries whose product with the key of a dominant token is each of `powers` in turn, in powers of two."""
+    q = torch.zeros(tokens, heads, dim, dtype=dtype)
+    q[:, :, 0] = torch.tensor([powers[i % len(powers)] for i in range(tokens * heads)]).view(tokens, heads).to(dtype)
+    return q
+
+
+def tail_bound(p, v, dim, terms, dtype, want):
+    """How far an output may be from `want` = p @ v, for probabilities p that add up to 1.
+
+    A probability is held in FP16 against a largest one of at least 2^6. It is off by 2^-11 of itself, or, where
+    it is below FP16's normal range, by half of FP16's smallest step, 2^-25: by 2^-31 of the largest. Their sum
+    is that of the unrounded ones. Scores are off as cache_reference.attention says (2^-23 of the terms'
+    magnitudes for each of D + 3 roundings, 2^-21 for the power of two), in the sum too, and the FP32
+    sums by 2^-24 for each of n + 40 steps. The result is rounded to its type once."""
+    n = len(p)
+    rel = 2 * (2.0 ** -11 + 2.0 ** -21 + terms * (dim + 3) * 2.0 ** -23) + (n + 40) * 2.0 ** -24
+    small = n * 2.0 ** -31 * p.max() * v.abs().amax(0)
+    return rel * (p @ v.abs()) + small + want.abs() * torch.finfo(dtype).eps / 2 + torch.finfo(dtype).tiny * torch.finfo(dtype).eps
+
+
+POWERS = [20.0, 25.5, 26.25, 28.0, 12.0, 24.75]
+
+
+@pytest.mark.parametrize("page,dim,group,dtype", [(16, 64, 3, FP16), (64, 128, 8, BF16), (32, 128, 12, BF16), (128, 64, 20, FP16)])
+@pytest.mark.parametrize("prompt", [0, 1])
+@pytest.mark.parametrize("listed", [False, True])
+def test_a_flat_tail_beside_dominant_tokens(page, dim, group, dtype, prompt, listed):
+    """In every 32 tokens one whose probability is 2^12 to 2^28 times that of each other, and whose value is zero:
+    the outputs are what the others add up to."""
+    lens, new = [700, 33, 1300], [5, 2, 9]
+    tensors, batch = tailed(lens, new, page, dim, dtype, lambda p: p % 32 == 0)
+    T, width = sum(new), batch[0].shape[1]
+    q = far(T, group, dim, dtype, POWERS)
+    blocks = None
+    if listed:
+        g = torch.Generator().manual_seed(202)
+        blocks = torch.stack([torch.randperm(width, generator=g)[:max(1, width * 2 // 3)] for _ in range(T)]).to(torch.int32)
+    scale = math.log(2.0)
+    cache = device_cache(tensors)
+    a = etk.CacheAttention(cache, len(lens), T, group, width, num_blocks=0 if blocks is None else blocks.shape[1], prompt=prompt)
+    got = a(q.cuda(), device_batch(batch), blocks=None if blocks is None else blocks.cuda(), scale=scale).cpu().double()
+    plain, row = ref.Cache(*tensors), 0
+    for b, (n, length) in enumerate(zip(new, lens)):
+        for i in range(n):
+            pos = length - n + i
+            at = [p for p in range(pos + 1) if blocks is None or p // page in blocks[row].tolist()]
+            if at:
+                k, v = (plain.rows(name, batch[0][b], 0, at)[0] for name in ("k", "v"))
+            for h in range(group):
+                if not at:
+                    assert not got[row, h].any()
+                    continue
+                x = k @ q[row, h].double() * scale
+                p = torch.softmax(x, 0)
+                want = p @ v
+                bound = tail_bound(p, v, dim, float(x.abs().max()), dtype, want)
+                off = (got[row, h] - want).abs()
+                assert (off <= bound).all(), (row, h, float(off.max()), float(want.max()), float(bound.max()))
+            row += 1
+
+
+@pytest.mark.parametrize("prompt", [0, 1])
+def test_a_long_tail_beside_one_dominant_token(prompt):
+    """Half a million tokens of 2^-26 each, a hundredth of the whole, beside one that was there before them. Many
+    sequences of the same pages, so that a CTA of the kernel of single tokens goes over a whole one alone;
+    its four warps take 32 tokens of a page in turn, so four tokens are dominant."""
+    page, dim, group = 128, 64, 8
+    length = 524288 if prompt else 65536
+    seqs, each = (1, 16) if prompt else (1300, 1)
+    tensors, batch = tailed([length], [each], page, dim, BF16, lambda p: p in (0, 32, 64, 96))
+    table = batch[0].expand(seqs, -1).contiguous()
+    T = seqs * each
+    q = far(T, group, dim, BF16, [26.25, 24.75, 25.5, 26.5])
+    scale = math.log(2.0)
+    cache = device_cache(tensors)
+    kv_len = torch.full((seqs,), length, dtype=torch.int32)
+    dev = device_batch((table, kv_len, torch.tensor([i * each for i in range(seqs + 1)], dtype=torch.int32)), single=each == 1)
+    got = etk.CacheAttention(cache, seqs, T, group, table.shape[1], prompt=prompt)(q.cuda(), dev, scale=scale)
+    order = batch[0][0].long()
+    k, v = (tensors[i].float()[order, 0].flatten(0, 1).cuda().double() * s for i, s in ((0, 2.0 ** -4), (1, 1.0)))
+    for t in range(each):
+        n = length - each + 1 + t
+        for h in range(group):
+            x = k[:n] @ q[t, h].cuda().double() * scale
+            p = torch.softmax(x, 0)
+            want = p @ v[:n]
+            bound = tail_bound(p, v[:n], dim, float(x.abs().max()), BF16, want)
+            off = (got[t::each, h].double() - want).abs()  # every sequence has the same queries
+            assert (off <= bound).all(), (t, h, float(off.max()), float(want.max()), float(bound.max()))
