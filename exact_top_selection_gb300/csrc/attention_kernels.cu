@@ -1001,12 +1001,17 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
 template <int D, int NT, int ST>
 int launch_tile(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a,
                 cudaStream_t stream) {
+  constexpr size_t most = sizeof(Shared<D, NT, ST>) + sizeof(int64_t) * (EXACT_TOPK_MAX_SEQS + 1) +
+                          EXACT_TOPK_MAX_LISTED_WIDTH;
+  static_assert(most <= kMostShared, "every call that the checks let through");
   const size_t smem = sizeof(Shared<D, NT, ST>) + sizeof(int64_t) * ((size_t)b.num_seqs + 1) +
                       (a.blocks != nullptr ? ((size_t)b.width + 3) / 4 * 4 : 0);
-  // Set on every call: a host-side table entry, cheaper than remembering it per device.
+  // Set on every call: a host-side table entry, cheaper than remembering it per device. The limit
+  // belongs to the kernel and not to the call, so it is the largest call's: another thread's
+  // launch may come between this thread's setting and its own launch.
   if (smem > 48 * 1024 && cudaFuncSetAttribute(attention_kernel<D, NT, ST>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)smem) != cudaSuccess) {
+                                               (int)most) != cudaSuccess) {
     cudaGetLastError();
     return EXACT_TOPK_ERR_CUDA;
   }

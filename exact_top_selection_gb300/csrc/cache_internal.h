@@ -70,6 +70,9 @@ constexpr int kPromptRows = 128;
 constexpr int kPromptTokens = 32;
 constexpr int kPromptListedWidth = 24576;
 
+// Shared memory that a CTA may have.
+constexpr size_t kMostShared = 227 * 1024;
+
 // The most CTAs of an attention launch.
 constexpr int kMaxAttentionWorkers = 608;
 

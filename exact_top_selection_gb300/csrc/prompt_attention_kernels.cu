@@ -715,10 +715,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <int D, int kPartShift>
 int launch(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a, cudaStream_t stream) {
+  constexpr size_t most = sizeof(Shared<D>) + 1024 + (size_t)kPromptListedWidth * 4;
+  static_assert(most <= kMostShared, "every call that the checks let through");
   const size_t smem =
       sizeof(Shared<D>) + 1024 + (a.blocks != nullptr ? (size_t)b.width * 4 : 0);
   const auto kernel = prompt_attention_kernel<D, kPartShift>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+  // the largest call's size: the limit is the kernel's, whichever thread launches it
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) !=
       cudaSuccess) {
     cudaGetLastError();
     return EXACT_TOPK_ERR_CUDA;

@@ -1,12 +1,15 @@
 """The cache operators where the sizes of test_gpu_cache.py do not lead."""
 
+import ctypes
 import math
+import threading
 
 import pytest
 import torch
 
 import cache_reference as ref
 import exact_top_selection_gb300 as etk
+from exact_top_selection_gb300 import cache as binding
 from test_gpu_cache import BF16, FP16, device_batch, device_cache
 
 pytestmark = pytest.mark.gpu
@@ -122,3 +125,53 @@ def test_a_long_tail_beside_one_dominant_token(prompt):
             bound = tail_bound(p, v[:n], dim, float(x.abs().max()), BF16, want)
             off = (got[t::each, h].double() - want).abs()  # every sequence has the same queries
             assert (off <= bound).all(), (t, h, float(off.max()), float(want.max()), float(bound.max()))
+
+
+# ---- host threads ----
+
+@pytest.mark.parametrize("prompt", [0, 1])
+def test_host_threads_with_calls_of_different_sizes(prompt):
+    """Objects whose tables and numbers of sequences differ: what a call sets for its launch must not be too
+    small for another thread's. The entry point is called as the binding does, without the binding's
+    checks, which hold the interpreter's lock most of the time."""
+    tensors, batch = ref.make(210, [500, 90], [12, 9], 1, 16, 64, BF16)
+    cache, lib = device_cache(tensors), binding._lib()
+    pages = torch.where(batch[0] < cache.num_pages, batch[0], 0)
+    jobs = []
+    for seqs, width in ((2, 32), (700, 24576 if prompt else 65536), (2, 4000), (4096, 24000)):
+        table = torch.zeros(seqs, width, dtype=torch.int32)
+        table[:2, :pages.shape[1]] = pages
+        lens, start = torch.zeros(seqs, dtype=torch.int32), torch.full((seqs + 1,), 21, dtype=torch.int32)
+        lens[:2], start[:2] = batch[1], batch[2][:2]
+        b = device_batch((table, lens, start))
+        q = ref.rows(211, 21, 8, 64, BF16).cuda()
+        blocks = torch.randint(0, 32, (21, 6), generator=torch.Generator().manual_seed(212), dtype=torch.int32).cuda()
+        a = etk.CacheAttention(cache, seqs, 21, 8, width, num_blocks=6, prompt=prompt)
+        jobs.append((a, b, q, blocks, a(q, b, blocks=blocks).clone()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(j[-1], jobs[0][-1]) for j in jobs)
+    failed = []
+    ready = threading.Barrier(len(jobs))
+
+    def work(a, b, q, blocks, want):
+        stream, out = torch.cuda.Stream(), torch.zeros_like(want)
+        torch.cuda.synchronize()
+        ref_ = ctypes.byref
+        args = (ref_(a.plan), cache._ref, b._ref, ref_(binding._rows(q, "q", cache, 8)), ref_(binding._rows(out, "out", cache, 8)),
+                blocks.data_ptr(), 0.125, *a._buffers, stream.cuda_stream)
+        ready.wait()
+        for _ in range(3000):
+            rc = lib.exact_topk_attention_run(*args)
+            if rc != 0:
+                failed.append(rc)
+                break
+        stream.synchronize()
+        if not torch.equal(out, want):
+            failed.append("differs")
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
