@@ -223,14 +223,17 @@ class KVCache:
 
     @classmethod
     def allocate(cls, num_pages, kv_heads, page_size, head_dim, dtype=None, device=None):
-        """A new cache with every page empty (codes 0, scales 1, bounds 0)."""
+        """A new cache with every page empty (codes 0, scales 1, bounds 0), ready for any stream."""
         _need_torch()
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         shape = (num_pages, kv_heads, page_size, head_dim)
         k, v = (torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2))
         ks, vs = (torch.ones(shape[:2], dtype=torch.float32, device=dev) for _ in range(2))
         bounds = torch.zeros(num_pages, kv_heads, 2, head_dim, dtype=dtype or torch.bfloat16, device=dev)
-        return cls(k, v, ks, vs, bounds)
+        cache = cls(k, v, ks, vs, bounds)
+        with torch.cuda.device(cache.device):
+            _wait_for_buffers()  # tokens written on another stream must not meet the fills
+        return cache
 
 
 class SequenceBatch:

@@ -10,7 +10,7 @@ import torch
 import cache_reference as ref
 import exact_top_selection_gb300 as etk
 from exact_top_selection_gb300 import cache as binding
-from test_gpu_cache import BF16, FP16, device_batch, device_cache
+from test_gpu_cache import BF16, FP16, device_batch, device_cache, same
 
 pytestmark = pytest.mark.gpu
 
@@ -175,3 +175,25 @@ def test_host_threads_with_calls_of_different_sizes(prompt):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+# ---- streams ----
+
+def test_a_cache_made_behind_other_work_and_written_on_another_stream():
+    page, dim, heads, pages = 16, 64, 2, 40
+    stream = torch.cuda.Stream()
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages)
+    n = pages * page
+    b = etk.SequenceBatch(table, torch.tensor([n], dtype=torch.int32, device="cuda"),
+                          torch.tensor([0, n], dtype=torch.int32, device="cuda"))
+    k, v = (ref.rows(s, n, heads, dim, BF16).cuda() for s in (220, 221))
+    want = etk.KVCache.allocate(pages, heads, page, dim, device="cuda")
+    etk.cache_write(want, b, k, v)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    cache = etk.KVCache.allocate(pages, heads, page, dim, device="cuda")
+    etk.cache_write(cache, b, k, v, stream=stream)
+    torch.cuda.synchronize()
+    for name in ("k", "v", "k_scale", "v_scale", "key_bounds"):
+        agree = same(getattr(cache, name).float(), getattr(want, name).float())
+        assert agree, name
