@@ -33,7 +33,7 @@ __all__ = ["KVCache", "SequenceBatch", "AttentionPlan", "CacheAttention", "Spars
 PAGE_SIZES = (16, 32, 64, 128)
 HEAD_DIMS = (64, 128)
 CACHE_SYMBOLS = ("exact_topk_cache_write", "exact_topk_cache_read", "exact_topk_block_scores",
-                 "exact_topk_make_attention_plan", "exact_topk_attention_run")
+                 "exact_topk_make_attention_plan", "exact_topk_attention_run", "exact_topk_set_wait_limit")
 
 
 class _Cache(ctypes.Structure):
@@ -99,6 +99,7 @@ def _lib():
             ctypes.POINTER(_etk.DeviceInfo), ctypes.POINTER(AttentionPlan)]
         lib.exact_topk_attention_run.argtypes = [ctypes.POINTER(AttentionPlan), cache, batch, rows, rows,
                                                  p, ctypes.c_float, p, sz, p, sz, p]
+        lib.exact_topk_set_wait_limit.argtypes = [i64]
         for name in CACHE_SYMBOLS:
             getattr(lib, name).restype = ctypes.c_int
         _bound = lib

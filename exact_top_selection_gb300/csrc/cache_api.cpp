@@ -2,6 +2,7 @@
 // argument checks and the attention's launch plan.  Nothing here synchronizes,
 // allocates or reads device memory.
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -108,7 +109,12 @@ int check_move(const exact_topk_cache* cache, const exact_topk_batch* batch, int
   return rc;
 }
 
+std::atomic<uint32_t> g_wait_limit{kWaitLimit};
+
 }  // namespace
+
+uint32_t wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
 }  // namespace etk
 
 using namespace etk;
@@ -308,6 +314,12 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
   a.max_cut = plan->num_blocks * c.page / 128;
   if (a.max_cut < 1) a.max_cut = 1;
   return launch_attention(c, b, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int exact_topk_set_wait_limit(int64_t polls) {
+  if (polls > (int64_t)kWaitLimit) return EXACT_TOPK_ERR_BAD_SHAPE;
+  g_wait_limit.store(polls < 0 ? kWaitLimit : (uint32_t)polls, std::memory_order_relaxed);
+  return EXACT_TOPK_OK;
 }
 
 }  // extern "C"

@@ -36,6 +36,11 @@ struct RowArgs {
   int64_t token_stride, head_stride;
 };
 
+// Polls of a barrier after which a wait gives up, far beyond any real wait, and the limit that
+// calls take now (exact_topk_set_wait_limit).
+constexpr uint32_t kWaitLimit = 1u << 20;
+uint32_t wait_limit();
+
 struct ScoreArgs {
   RowArgs q;
   float* scores;

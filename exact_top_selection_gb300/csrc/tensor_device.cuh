@@ -4,9 +4,9 @@
 
 #include <cstdint>
 
-namespace etk {
+#include "cache_internal.h"
 
-constexpr uint32_t kWaitLimit = 1u << 20;  // polls of a barrier, far beyond any real wait
+namespace etk {
 
 __device__ __forceinline__ uint32_t shared_address(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
@@ -21,9 +21,11 @@ __device__ __forceinline__ void barrier_arrive(uint64_t* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(shared_address(b)) : "memory");
 }
 
-// False when the barrier's phase did not complete in time, or another wait has given up.
-__device__ __forceinline__ bool barrier_wait(uint64_t* b, uint32_t parity, volatile int* failed) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+// False when the barrier's phase did not complete within `limit` polls, or another wait has given
+// up. Lanes of a warp may be answered differently: they vote before they go on together.
+__device__ __forceinline__ bool barrier_wait(uint64_t* b, uint32_t parity, volatile int* failed,
+                                             uint32_t limit = kWaitLimit) {
+  for (uint32_t i = 0; i < limit; ++i) {
     uint32_t done;
     asm volatile(
         "{\n.reg .pred p;\n"

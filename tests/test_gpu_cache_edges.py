@@ -1,5 +1,6 @@
 """The cache operators where the sizes of test_gpu_cache.py do not lead."""
 
+import contextlib
 import ctypes
 import math
 import threading
@@ -10,7 +11,7 @@ import torch
 import cache_reference as ref
 import exact_top_selection_gb300 as etk
 from exact_top_selection_gb300 import cache as binding
-from test_gpu_cache import BF16, FP16, device_batch, device_cache, same
+from test_gpu_cache import BF16, FP16, LAYOUTS, check_attention, device_batch, device_cache, same
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +198,40 @@ def test_a_cache_made_behind_other_work_and_written_on_another_stream():
     for name in ("k", "v", "k_scale", "v_scale", "key_bounds"):
         agree = same(getattr(cache, name).float(), getattr(want, name).float())
         assert agree, name
+
+
+# ---- waits that run out ----
+
+@contextlib.contextmanager
+def waits(polls):
+    """Waits within a CTA give up after so many polls (0: at once)."""
+    lib = binding._lib()
+    assert lib.exact_topk_set_wait_limit(polls) == 0
+    try:
+        yield
+    finally:
+        assert lib.exact_topk_set_wait_limit(-1) == 0
+
+
+@pytest.mark.parametrize("page,dim,heads,group,dtype", LAYOUTS + [(64, 128, 1, 130, BF16)])
+def test_a_prompt_whose_waits_run_out(page, dim, heads, group, dtype):
+    """The kernel behind the prompt's computes all that was left: its own results, bit for bit. The tensor memory
+    is given back each time."""
+    lens, new = [page * 9 + 3, 64], [23, 9]
+    tensors, batch = ref.make(230, lens, new, heads, page, dim, dtype)
+    T, K = sum(new), 5
+    q = ref.rows(231, T, heads * group, dim, dtype, 3.0)
+    blocks = torch.randint(-1, 10, (T * heads, K), generator=torch.Generator().manual_seed(232), dtype=torch.int32)
+    cache, b = device_cache(tensors), device_batch(batch)
+    for lists in (None, blocks):
+        with waits(0):
+            check_attention(tensors, batch, q, lists, prompt=1)
+        dev = None if lists is None else lists.cuda()
+        plain, prompt = (etk.CacheAttention(cache, 2, T, heads * group, b.table_width, num_blocks=0 if dev is None else K, prompt=p)
+                         for p in (0, 1))
+        want = plain(q.cuda(), b, blocks=dev)
+        with waits(0):
+            for _ in range(10):
+                got = prompt(q.cuda(), b, blocks=dev)
+        assert torch.equal(got, want)
+        check_attention(tensors, batch, q, lists, prompt=1)
