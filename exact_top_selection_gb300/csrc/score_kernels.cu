@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) score_step_kernel(CacheArgs c, Batch
 // which lie anywhere in memory, in lines of 64 channels through a ring; eight bring the next
 // item's columns, line by line as the products let go of the old ones; one thread issues
 // the products; four warps read the results out. Every wait is bounded; a CTA whose wait
-// ran out writes NaN for what it has not computed.
+// ran out computes its items again, one score a thread (score_again).
 //
 // The products alone, with nothing to wait for, take 87 us of a chunk of 4096 tokens x 32 heads
 // over 2048 pages (an SM's shared memory feeds both operands: 96 of its 128 bytes a clock). A
@@ -276,11 +276,64 @@ __device__ __forceinline__ PromptItem prompt_item(const CacheArgs& c, const Batc
   return item;
 }
 
+// All scores of a CTA's items from their definition, without waits. Apart from the kernel's body,
+// whose registers its own would crowd.
+template <bool kFp16, int D>
+__device__ __noinline__ void score_again(const CacheArgs& c, const BatchArgs& b,
+                                         const ScoreArgs& a, const PromptWork& work,
+                                         int tile_tokens) {
+  const uint16_t* const bounds = static_cast<const uint16_t*>(c.bounds);
+  const uint16_t* const queries = static_cast<const uint16_t*>(a.q.data);
+  for (int64_t i = blockIdx.x; i < work.items; i += gridDim.x) {
+    const PromptItem item = prompt_item(c, b, work, tile_tokens, i);
+    if (item.tiles == 0) continue;
+    const int left = item.seen - item.first_page;
+    const int pages = left < item.tiles * kLanes ? left : item.tiles * kLanes;
+    for (int n = threadIdx.x; n < item.tokens * pages; n += kPromptThreads) {
+      const int token = n / pages, j = item.first_page + n % pages;
+      const int pos = item.pos0 + token, newest = pos >> c.page_shift;
+      if (pos < 0 || j > newest) continue;
+      const int page = page_of(c, b, item.seq, j);
+      float best = -__uint_as_float(0x7F800000u);
+      if (page >= 0 && (j < a.keep_first || j > newest - a.keep_last)) {
+        best = __uint_as_float(0x7F800000u);
+      } else if (page >= 0) {
+        const uint4* const at = reinterpret_cast<const uint4*>(
+            bounds + ((int64_t)page * c.heads + item.head) * (2 * D));
+        for (int g = 0; g < a.group; ++g) {
+          const uint4* const q = reinterpret_cast<const uint4*>(
+              queries + (item.row0 + token) * a.q.token_stride +
+              ((int64_t)item.head * a.group + g) * a.q.head_stride);
+          float sum = 0.f;
+#pragma unroll 1
+          for (int k = 0; k < D / 8; ++k) {
+            const uint4 x = __ldg(q + k), y = __ldg(at + k), z = __ldg(at + D / 8 + k);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w}, hi[4] = {y.x, y.y, y.z, y.w},
+                           lo[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float2 up = unpack2<kFp16>(clamp_sign<kFp16>(u[m], true));
+              const float2 down = unpack2<kFp16>(clamp_sign<kFp16>(u[m], false));
+              const float2 most = unpack2<kFp16>(hi[m]), least = unpack2<kFp16>(lo[m]);
+              sum = fmaf(up.x, most.x, fmaf(down.x, least.x, sum));
+              sum = fmaf(up.y, most.y, fmaf(down.y, least.y, sum));
+            }
+          }
+          best = g == 0 ? sum : max_nan(best, sum);
+        }
+      }
+      a.scores[((item.row0 + token) * c.heads + item.head) * a.row_pitch + j] = best;
+    }
+  }
+}
+
 // kPadded: the group's heads rounded up to a power of two, at most 32; a column beyond
 // the group repeats its last head, which leaves the maximum as it is.
 template <bool kFp16, int D, int kPadded>
 __global__ void __launch_bounds__(kPromptThreads, 1)
-    score_prompt_kernel(CacheArgs c, BatchArgs b, ScoreArgs a, PromptWork work) {
+    score_prompt_kernel(const __grid_constant__ CacheArgs c, const __grid_constant__ BatchArgs b,
+                        const __grid_constant__ ScoreArgs a,
+                        const __grid_constant__ PromptWork work, uint32_t wait_limit) {
   using Smem = PromptShared<D>;
   constexpr int kChunks = Smem::kChunks, kStages = Smem::kStages;
   constexpr int kTileTokens = kColumns / kPadded;
@@ -335,7 +388,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       // ---- read out ----
       constexpr int kEach = 32 / kPadded;  // tokens of 32 columns
       const int64_t row_step = (int64_t)c.heads * a.row_pitch;
-      for (int i = 0; i < items; ++i) {
+      for (int i = 0; i < items && ok; ++i) {
         const PromptItem& item = sm.item[i];
         if (item.tiles == 0) continue;
         const int first_newest = item.pos0 >> c.page_shift;  // the first token's newest page
@@ -348,8 +401,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           const bool plain = item.pos0 >= 0 && j0 >= a.keep_first &&
                              j0 + 31 <= first_newest - a.keep_last && __all_sync(~0u, there);
           float* at = a.scores + (item.row0 * c.heads + item.head) * a.row_pitch + j;
-          if (ok) ok = barrier_wait(&sm.done[buffer], (tiles >> 1) & 1, failed);
+          ok = barrier_wait(&sm.done[buffer], (tiles >> 1) & 1, failed);
           ok = __all_sync(~0u, ok);
+          if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t from = tensor + ((uint32_t)(warp * 32) << 16) + buffer * kColumns;
           const auto largest = [&](const float (&v)[32], int t) {
@@ -363,14 +417,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           };
           const auto write = [&](int part, const float (&v)[32]) {
             const int left = item.tokens - part * kEach;
-            if (plain && ok && left >= kEach) {
+            if (plain && left >= kEach) {
 #pragma unroll
               for (int t = 0; t < kEach; ++t, at += row_step) *at = largest(v, t);
               return;
             }
 #pragma unroll
             for (int t = 0; t < kEach; ++t, at += row_step) {
-              float best = ok ? largest(v, t) : __uint_as_float(0x7FFFFFFFu);
+              float best = largest(v, t);
               const int pos = item.pos0 + part * kEach + t;
               const int newest = pos >> c.page_shift;
               if (j < a.keep_first || j > newest - a.keep_last)
@@ -448,15 +502,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       constexpr int kPieces = kColumns * kLine / 8 / kFill;  // a thread's pieces of a line
       const int thread = tid - kReadOut - kGather;
       const int piece = thread & 7;
-      for (int i = 0; i < items && ok; ++i) {
+      for (int i = 0; i < items; ++i) {
         const PromptItem& item = sm.item[i];
-        // lengths, by the threads of each column tile's first run
+        // lengths, by the threads of each column tile's first run, whether or not a wait ran out
         if (item.first_run && thread < item.tokens) {
           const int pos = item.pos0 + thread;
           a.ke[(item.row0 + thread) * c.heads + item.head] =
               pos < 0 ? 0 : (pos >> c.page_shift) + 1;
         }
-        if (item.tiles == 0) continue;
+        if (item.tiles == 0 || !ok) continue;
         uint4 w[kLines][kPieces];
 #pragma unroll
         for (int line = 0; line < kLines; ++line)
@@ -474,7 +528,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           }
 #pragma unroll
         for (int chunk = 0; chunk < kChunks; ++chunk) {
-          if (ok && columns_filled > 0)
+          if (columns_filled > 0)
             ok = barrier_wait(&sm.released[chunk], (columns_filled - 1) & 1, failed);
           if (!ok) break;
           const bool positive = (chunk & 1) == 0;
@@ -494,6 +548,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
       }
     } else {
       // ---- products, by one thread ----
+      // The waits for operands are the ones whose limit the host sets: once one has run out, the
+      // others give up as well.
       constexpr uint32_t kType = kFp16 ? 0u : 1u;
       constexpr uint32_t kind = 1u << 4 | kType << 7 | kType << 10 | (kColumns / 8) << 17 |
                                 (kLanes / 16) << 24;
@@ -506,8 +562,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (tiles >= 2) ok = barrier_wait(&sm.free[buffer], ((tiles >> 1) - 1) & 1, failed);
           for (int chunk = 0; chunk < kChunks; ++chunk, ++steps) {
             const int s = steps % kStages;
-            if (tile == 0) ok = ok && barrier_wait(&sm.filled[chunk], columns_filled & 1, failed);
-            ok = ok && barrier_wait(&sm.full[s], (steps / kStages) & 1, failed);
+            if (tile == 0) ok = ok && barrier_wait(&sm.filled[chunk], columns_filled & 1, failed, wait_limit);
+            ok = ok && barrier_wait(&sm.full[s], (steps / kStages) & 1, failed, wait_limit);
             ok = __all_sync(~0u, ok);
             if (!ok) break;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -544,6 +600,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   if (warp == kIssueWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tensor)
                  : "memory");
+  if (*failed) score_again<kFp16, D>(c, b, a, work, kTileTokens);
 }
 
 template <bool kFp16, int D, int kPadded>
@@ -570,7 +627,7 @@ int launch_prompt(const CacheArgs& c, const BatchArgs& b, const ScoreArgs& a,
   work.groups = (tiles + work.each - 1) / work.each;
   work.items = work.slots * c.heads * work.groups;
   const unsigned grid = (unsigned)(work.items < kSms ? work.items : kSms);
-  kernel<<<grid, kPromptThreads, smem, stream>>>(c, b, a, work);
+  kernel<<<grid, kPromptThreads, smem, stream>>>(c, b, a, work, wait_limit());
   return launch_status();
 }
 

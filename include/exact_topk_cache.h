@@ -193,10 +193,10 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
                              void* counters, size_t counter_bytes, void* workspace,
                              size_t workspace_bytes, struct CUstream_st* stream);
 
-/* How many times the issuing thread of the attention's prompt kernel polls for its operands before
- * it gives up, for the calls that this process makes from now on: at most 2^20, which a negative
- * number brings back. What a CTA has not computed then is computed again by the kernel behind
- * it. With 0 it always gives up, which is how that is tested.
+/* How many times the issuing threads of the prompts' kernels (page scores and attention) poll for
+ * their operands before they give up, for the calls that this process makes from now on: at most
+ * 2^20, which a negative number brings back. What a CTA has not computed then is computed again
+ * without waits. With 0 they always give up, which is how that is tested.
  * Errors: BAD_SHAPE (more than 2^20). */
 int exact_topk_set_wait_limit(int64_t polls);
 

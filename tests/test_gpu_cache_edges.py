@@ -235,3 +235,77 @@ def test_a_prompt_whose_waits_run_out(page, dim, heads, group, dtype):
                 got = prompt(q.cuda(), b, blocks=dev)
         assert torch.equal(got, want)
         check_attention(tensors, batch, q, lists, prompt=1)
+
+
+# ---- page scores ----
+
+def check_scores(lens, new, page, dim, heads, group, dtype, first, last, absent=0.0, before=lambda: contextlib.nullcontext()):
+    """All rows against the definition in 64 bits, computed on the GPU by one product for each sequence and
+    head. `absent`: share of the table's entries, the first and the newest among them, that name no page."""
+    g = torch.Generator().manual_seed(240)
+    held = [-(-n // page) for n in lens]
+    total = sum(held) + 1
+    mid, half = torch.randn(total, heads, dim, generator=g), torch.rand(total, heads, dim, generator=g)
+    bounds = torch.stack([mid + half, mid - half], 2).to(dtype).cuda()
+    codes = torch.zeros(total, heads, page, dim, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    one = torch.ones(total, heads, device="cuda")
+    cache = etk.KVCache(codes, codes, one, one, bounds)
+    table = torch.full((len(lens), max(held)), total + 3, dtype=torch.int32)
+    order, at = torch.randperm(total, generator=g).int(), 0
+    for b, n in enumerate(held):
+        table[b, :n] = order[at:at + n]
+        gone = torch.rand(n, generator=g) < absent
+        if absent and n > 2:
+            gone[0] = gone[n - 1] = True
+        table[b, :n][gone] = torch.tensor([-1, total, 2 ** 31 - 1], dtype=torch.int32)[torch.arange(int(gone.sum())) % 3]
+        at += n
+    T = sum(new)
+    start = torch.tensor([sum(new[:i]) for i in range(len(new) + 1)], dtype=torch.int32)
+    dev = device_batch((table, torch.tensor(lens, dtype=torch.int32), start))
+    q = ref.rows(241, T + 5, heads * group, dim, dtype, 2.0).cuda()
+    q[T:] = math.nan
+    got = torch.full(((T + 5) * heads, max(held)), -7.0, device="cuda")
+    ke = torch.full(((T + 5) * heads,), -7, dtype=torch.int32, device="cuda")
+    live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with before():
+        etk.block_scores(cache, dev, q, first, last, got, ke, live)
+        torch.cuda.synchronize()
+    assert int(live) == T * heads
+    assert bool((got[T * heads:] == -7).all()) and bool((ke[T * heads:] == -7).all())
+    got, ke = got.view(T + 5, heads, -1), ke.view(T + 5, heads)
+    page_ids = dev.page_table.long()
+    for b, (n, length) in enumerate(zip(new, lens)):
+        if n == 0:
+            continue
+        lo = int(start[b])
+        pos = length - n + torch.arange(n, device="cuda")
+        newest = torch.where(pos >= 0, torch.div(pos, page, rounding_mode="floor"), -1)[:, None]
+        assert bool((ke[lo:lo + n] == newest + 1).all())
+        j = torch.arange(held[b], device="cuda")[None]
+        there = (page_ids[b, :held[b]] >= 0) & (page_ids[b, :held[b]] < total)
+        ends = bounds[torch.where(there, page_ids[b, :held[b]], 0)].double()
+        for h in range(heads):
+            u = q[lo:lo + n, h * group:(h + 1) * group].double().flatten(0, 1)
+            hi, low = ends[:, h, 0].T, ends[:, h, 1].T
+            want = (u.clamp(min=0) @ hi + u.clamp(max=0) @ low).view(n, group, -1).amax(1)
+            size = (u.abs() @ torch.maximum(hi.abs(), low.abs())).view(n, group, -1).amax(1)
+            want = torch.where((j < first) | (j > newest - last), math.inf, want)
+            want = torch.where(there[None], want, -math.inf)
+            want = torch.where(j > newest, -7.0, want)
+            mine = got[lo:lo + n, h].double()
+            assert bool((mine[:, held[b]:] == -7).all())
+            mine = mine[:, :held[b]]
+            fine = want.isfinite() & (j <= newest)
+            # 2 D exact products summed in FP32, each sum within 2^-23 of the terms' magnitudes
+            good = torch.where(fine, (mine - want).abs() <= 2 * dim * 2.0 ** -23 * size, mine == want)
+            assert bool(good.all()), (b, h, (~good).nonzero()[:4].tolist(), mine[~good][:4].tolist(), want[~good][:4].tolist())
+
+
+@pytest.mark.parametrize("lens,new,page,dim,heads,group,dtype", [
+    ([777], [300], 16, 64, 2, 4, BF16), ([3, 9000, 64], [70, 700, 33], 64, 128, 3, 5, FP16), ([10300], [4096], 16, 64, 10, 16, BF16),
+    ([6000], [1000], 32, 128, 1, 1, BF16), ([2500, 2100], [300, 256], 16, 128, 2, 32, FP16)])
+def test_scores_of_a_prompt_whose_waits_run_out(lens, new, page, dim, heads, group, dtype):
+    """Everything is computed again, the lengths are written all the same, and the tensor memory is given back."""
+    for first, last, absent in ((1, 2, 0.1), (0, 0, 0.0)):
+        check_scores(lens, new, page, dim, heads, group, dtype, first, last, absent, before=lambda: waits(0))
+    check_scores(lens, new, page, dim, heads, group, dtype, 1, 2, 0.1)
