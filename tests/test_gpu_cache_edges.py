@@ -309,3 +309,23 @@ def test_scores_of_a_prompt_whose_waits_run_out(lens, new, page, dim, heads, gro
     for first, last, absent in ((1, 2, 0.1), (0, 0, 0.0)):
         check_scores(lens, new, page, dim, heads, group, dtype, first, last, absent, before=lambda: waits(0))
     check_scores(lens, new, page, dim, heads, group, dtype, 1, 2, 0.1)
+
+
+# Items (256 columns x a run of page tiles) of each: 2570 of 6 tiles, more than 16 for each CTA; 1020 of 16 tiles; 420 of
+# 2 tiles; 864 of 2 tiles; 1004 of 2 tiles; 1060 of 4 and fewer.
+@pytest.mark.parametrize("lens,new,page,dim,heads,group,dtype", [
+    ([10300], [4096], 16, 64, 10, 16, BF16), ([32768, 500], [1500, 100], 16, 128, 10, 16, FP16),
+    ([70000, 3000, 200], [700, 0, 130], 64, 128, 3, 5, BF16), ([20000], [9000], 32, 64, 8, 1, FP16),
+    ([6000], [2000], 16, 64, 2, 32, BF16), ([16000, 1, 900, 15000], [800, 1, 333, 500], 16, 64, 5, 12, FP16)])
+@pytest.mark.parametrize("absent", [0.0, 0.15])
+def test_scores_of_more_items_than_ctas(lens, new, page, dim, heads, group, dtype, absent):
+    """A CTA goes from item to item: accumulators, column lines and barriers are used again and again."""
+    check_scores(lens, new, page, dim, heads, group, dtype, 1, 2, absent)
+
+
+@pytest.mark.parametrize("page,dim,heads,group,dtype", [(16, 64, 2, 8, BF16), (64, 128, 1, 3, FP16), (32, 128, 2, 12, BF16), (16, 64, 1, 40, FP16)])
+def test_scores_of_absent_pages(page, dim, heads, group, dtype):
+    """Pages that no id names score -inf, also where they are to be kept: single tokens, tokens to verify, prompts."""
+    for lens, new in (([page * 90, 5, page * 7 + 3], [1, 1, 1]), ([page * 40 + 1, page * 9], [5, 2]), ([page * 50, 300], [270, 190])):
+        for first, last in ((0, 0), (2, 3), (1000, 0)):
+            check_scores(lens, new, page, dim, heads, group, dtype, first, last, 0.25)
