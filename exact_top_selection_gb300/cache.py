@@ -313,7 +313,7 @@ def block_scores(cache, batch, q, keep_first=0, keep_last=0, scores=None, ke=Non
 
     scores float32 [num_tokens * kv_heads, table_width]: row token * kv_heads + head holds, for each page
     the token sees, the largest over the key head's query heads of an upper bound of q . k over the page's
-    keys (from the key bounds); the first keep_first pages and the newest keep_last get +inf.  ke int32
+    keys as they were written (from the key bounds); the first keep_first pages and the newest keep_last get +inf.  ke int32
     [num_tokens * kv_heads] is the number of pages seen.  Entries beyond it, and rows of no sequence, are
     left as they were.  num_valid_rows, an int32 tensor of one element, gets the number of live rows."""
     heads = q.shape[1] if q.dim() == 3 else 0
@@ -421,7 +421,8 @@ class SparseAttention:
     attention over the pages selected for each token and key head.  Owns every buffer between.
 
     keep_first and keep_last pages (the sequence's first and newest) are always among the num_blocks
-    selected, which must be at least as many."""
+    selected, which must be at least as many.  As of CacheAttention, calls of one object must not overlap
+    on the GPU, and the object is kept until its last call has run."""
 
     def __init__(self, cache, num_seqs, num_tokens, q_heads, table_width, num_blocks, keep_first=0, keep_last=1):
         if keep_first < 0 or keep_last < 0 or keep_first + keep_last > num_blocks:

@@ -81,7 +81,11 @@ constexpr size_t kMostShared = 227 * 1024;
 // The most CTAs of an attention launch.
 constexpr int kMaxAttentionWorkers = 608;
 
-// Resident CTAs that the attention kernels are built for.
+// Resident CTAs that the attention kernels are built for. They have to fit the SM's shared memory
+// with 8 bytes for each sequence and, over lists, a byte for each page of the table: with 8
+// columns of 128 channels one fewer fits from 384 sequences on, and over lists of 64 sequences
+// from 2553 pages on. The prompt's kernel takes 4 bytes for each page over lists, and a second CTA
+// fits up to about 2900. Beyond that all still runs, in more waves than the plan counts on.
 constexpr int attention_ctas_per_sm(int columns, int dim) {
   return dim == 64 ? (columns == 32 ? 3 : 4) : (columns == 8 ? 4 : (columns == 16 ? 3 : 2));
 }

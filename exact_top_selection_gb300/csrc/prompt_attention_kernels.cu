@@ -29,7 +29,7 @@
 // A block's exponentials are 512 clocks of an SM and its products about as many; what bounds
 // it is the latency from scores over softmax to outputs, with two CTAs to fill it. 4096
 // tokens x 16 query heads (2 key heads of 128 channels), 32 pages of 64 tokens each, 40 in a
-// tile's union: 133 us (520 TFLOP/s of the products that count).
+// tile's union: 133 us in a graph (520 TFLOP/s of the products that count), 137 by calls.
 
 #include "cache_device.cuh"
 #include "tensor_device.cuh"

@@ -14,7 +14,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int64_t kPromptColumns = 64;
-constexpr int kSms = 152;
+constexpr int kSms = 152;  // of a GB300; with fewer or more the items are shared out all the same
 constexpr int kStepCtas = 4;  // resident on an SM
 constexpr int kPages = 16;  // pages of a warp's step: the rows of one matrix instruction
 
@@ -562,7 +562,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
           if (tiles >= 2) ok = barrier_wait(&sm.free[buffer], ((tiles >> 1) - 1) & 1, failed);
           for (int chunk = 0; chunk < kChunks; ++chunk, ++steps) {
             const int s = steps % kStages;
-            if (tile == 0) ok = ok && barrier_wait(&sm.filled[chunk], columns_filled & 1, failed, wait_limit);
+            if (tile == 0)
+              ok = ok && barrier_wait(&sm.filled[chunk], columns_filled & 1, failed, wait_limit);
             ok = ok && barrier_wait(&sm.full[s], (steps / kStages) & 1, failed, wait_limit);
             ok = __all_sync(~0u, ok);
             if (!ok) break;

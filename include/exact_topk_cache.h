@@ -103,7 +103,8 @@ typedef struct exact_topk_rows {
  * (first written at offset o > 0) keeps the larger of its scale and the one the
  * new rows need; where that is larger, its codes [0, o) are brought to it. Codes
  * at offsets behind the last written one are left as they were. Codes are
- * rounded to nearest even; infinities and NaN become NaN. The bounds
+ * rounded to nearest even (where a kept scale is no power of two, of the row times
+ * the scale's rounded reciprocal); infinities and NaN become NaN. The bounds
  * are exact: the extremes of the rows as given, NaN taken as 0 and infinities
  * as the type's largest number. No page may be written by two sequences of a
  * call (its contents are undefined then; nothing else is touched).
@@ -123,7 +124,8 @@ int exact_topk_cache_read(const exact_topk_cache* cache, const exact_topk_batch*
  * that the token sees (j * page_size <= position),
  *   max over the q_heads / kv_heads query heads g of the key head of
  *   sum_d max(q[g][d] * hi[j][d], q[g][d] * lo[j][d]),
- * the upper bound of q . k over the page's keys, in FP32 (products exact). Its
+ * the upper bound of q . k over the page's keys as they were written, in FP32 (products
+ * exact); a stored key is off by e4m3's rounding, 2^-4 of itself, and may lie beyond them. Its
  * first keep_first pages and its newest keep_last ones get +inf instead, so that a
  * selection of at least as many always takes them.
  *   scores      device float32 [num_tokens * kv_heads][row_pitch], row_pitch >= table_width;
@@ -173,7 +175,8 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
 /* out[t][head] = sum_p softmax_p(scale * q[t][head] . k[p]) v[p] over the tokens p at
  * positions up to t's own: all of them, or those of the pages listed for the row.
  * A row that sees nothing gets zeros. Scores, sums and outputs are FP32, rounded
- * once to the cache's type; the probabilities enter the second product in FP16.
+ * once to the cache's type; the probabilities enter the second product in FP16, off by
+ * 2^-11 of themselves and, below 2^-20 of the row's largest, by at most 2^-31 of that.
  *   q, out      [num_tokens][q_heads][head_dim]; they must not overlap
  *   scale       finite, as is scale * log2(e) (else BAD_PLAN); the scores must be finite in FP32
  *   blocks      NULL when plan->num_blocks is 0, else device int32
