@@ -13,9 +13,10 @@ Attention" (sections 4-5); API shape from the HPC-Ops pull request
     workspace = torch.empty(workspace_bytes, dtype=torch.uint8, device="cuda")
     topk(logits, ke, output, num_valid_rows, top_k, counters, workspace)
 
-The operators around the selection in a sparse-attention step (an 8-bit paged
-cache, page scores, attention over the cache or its selected pages) are bound
-in ``cache.py`` and offered here too.
+The operators around the selection in a sparse-attention step (a paged cache in 8 or 4
+bits, page scores, attention over the cache or its selected pages) are bound in
+``cache.py``, those before them (page tables kept on the GPU, rotary positions) in
+``batch.py``; all are offered here too.
 """
 
 from __future__ import annotations
@@ -31,7 +32,7 @@ __all__ = [
     "error_string", "version", "stream_floor", "FAMILY_AUTO", "FAMILY_PERSISTENT_SAMPLED", "FAMILY_KV_SPLIT",
     "FAMILY_ROW_LOCAL_EXACT", "FAMILY_CLUSTER_SPLIT", "TRACE_FIELDS", "ROUTES", "EXPORTED_SYMBOLS",
     "KVCache", "SequenceBatch", "AttentionPlan", "CacheAttention", "SparseAttention", "cache_write",
-    "cache_read", "block_scores", "make_attention_plan", "CACHE_SYMBOLS",
+    "cache_read", "block_scores", "make_attention_plan", "CACHE_SYMBOLS", "KVCache4", "Rotary", "PageTables",
 ]
 
 FAMILY_AUTO = 0
@@ -304,5 +305,6 @@ class ExactTopK:
                    prev_topk=prev_topk, trace=trace, stream=stream)
 
 
-from .cache import (CACHE_SYMBOLS, AttentionPlan, CacheAttention, KVCache, SequenceBatch,  # noqa: E402
-                    SparseAttention, block_scores, cache_read, cache_write, make_attention_plan)
+from .cache import (CACHE_SYMBOLS, AttentionPlan, CacheAttention, KVCache, KVCache4,  # noqa: E402
+                    SequenceBatch, SparseAttention, block_scores, cache_read, cache_write, make_attention_plan)
+from .batch import PageTables, Rotary  # noqa: E402

@@ -1,8 +1,8 @@
 """Python binding of the cache operators (include/exact_topk_cache.h).
 
 The steps of sparse attention around the exact Top-K: a paged key/value cache in
-8 bits, the page scores that the selection reads, and the attention over the pages it
-selected (or over the whole cache)::
+8 bits (KVCache) or 4 (KVCache4), the page scores that the selection reads, and the attention over the
+pages it selected (or over the whole cache)::
 
     cache = KVCache.allocate(num_pages, kv_heads, page_size, head_dim, device="cuda")
     batch = SequenceBatch(page_table, kv_len, q_start)     # q_start=None: one row per sequence
@@ -27,13 +27,17 @@ import math
 
 import exact_top_selection_gb300 as _etk
 
-__all__ = ["KVCache", "SequenceBatch", "AttentionPlan", "CacheAttention", "SparseAttention", "cache_write",
+__all__ = ["KVCache", "KVCache4", "SequenceBatch", "AttentionPlan", "CacheAttention", "SparseAttention", "cache_write",
            "cache_read", "block_scores", "make_attention_plan", "CACHE_SYMBOLS", "PAGE_SIZES", "HEAD_DIMS"]
 
 PAGE_SIZES = (16, 32, 64, 128)
 HEAD_DIMS = (64, 128)
 CACHE_SYMBOLS = ("exact_topk_cache_write", "exact_topk_cache_read", "exact_topk_block_scores",
-                 "exact_topk_make_attention_plan", "exact_topk_attention_run", "exact_topk_set_wait_limit")
+                 "exact_topk_make_attention_plan", "exact_topk_attention_run", "exact_topk_set_wait_limit",
+                 "exact_topk_cache4_write", "exact_topk_cache4_read", "exact_topk_cache4_block_scores",
+                 "exact_topk_cache4_attention_run", "exact_topk_rotary", "exact_topk_tables_workspace",
+                 "exact_topk_update_tables")
+GROUP = 16  # channels that share a scale in 4 bits
 
 
 class _Cache(ctypes.Structure):
@@ -42,6 +46,14 @@ class _Cache(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _Cache4(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("key_bounds", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("type", ctypes.c_int32), ("k_unit", ctypes.c_float), ("v_unit", ctypes.c_float)]
 
 
 class _Batch(ctypes.Structure):
@@ -91,14 +103,17 @@ def _lib():
     if _bound is None:
         lib = _etk.library()
         p, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
-        cache, batch, rows = (ctypes.POINTER(t) for t in (_Cache, _Batch, _Rows))
-        lib.exact_topk_cache_write.argtypes = [cache, batch, i64, rows, rows, p]
-        lib.exact_topk_cache_read.argtypes = [cache, batch, i64, rows, rows, p]
-        lib.exact_topk_block_scores.argtypes = [cache, batch, i64, i32, rows, i32, i32, p, i64, p, p, p]
+        batch, rows = ctypes.POINTER(_Batch), ctypes.POINTER(_Rows)
+        plan = ctypes.POINTER(AttentionPlan)
+        for prefix, cache in (("exact_topk_cache", ctypes.POINTER(_Cache)), ("exact_topk_cache4", ctypes.POINTER(_Cache4))):
+            getattr(lib, prefix + "_write").argtypes = [cache, batch, i64, rows, rows, p]
+            getattr(lib, prefix + "_read").argtypes = [cache, batch, i64, rows, rows, p]
+            prefix = "exact_topk" if prefix == "exact_topk_cache" else prefix
+            getattr(lib, prefix + "_block_scores").argtypes = [cache, batch, i64, i32, rows, i32, i32, p, i64, p, p, p]
+            getattr(lib, prefix + "_attention_run").argtypes = [plan, cache, batch, rows, rows, p, ctypes.c_float,
+                                                                p, sz, p, sz, p]
         lib.exact_topk_make_attention_plan.argtypes = [i64] + [i32] * 9 + [
-            ctypes.POINTER(_etk.DeviceInfo), ctypes.POINTER(AttentionPlan)]
-        lib.exact_topk_attention_run.argtypes = [ctypes.POINTER(AttentionPlan), cache, batch, rows, rows,
-                                                 p, ctypes.c_float, p, sz, p, sz, p]
+            ctypes.POINTER(_etk.DeviceInfo), plan]
         lib.exact_topk_set_wait_limit.argtypes = [i64]
         for name in CACHE_SYMBOLS:
             getattr(lib, name).restype = ctypes.c_int
@@ -190,6 +205,9 @@ class KVCache:
     are used in place and kept alive by this object.
     """
 
+    _functions = ("exact_topk_cache_write", "exact_topk_cache_read", "exact_topk_block_scores",
+                  "exact_topk_attention_run")
+
     def __init__(self, k, v, k_scale, v_scale, key_bounds):
         _need_torch()
         if k.dim() != 4 or k.shape != v.shape:
@@ -237,6 +255,69 @@ class KVCache:
         return cache
 
 
+class KVCache4:
+    """A paged cache of e2m1 codes, with an e4m3 scale for every 16 channels of a token and key head.
+
+    k, v: uint8 [num_pages, kv_heads, page_size, head_dim / 2], two codes a byte, the even channel in the
+    lower four bits; k_scale, v_scale: float8_e4m3fn [num_pages, kv_heads, page_size, head_dim / 16];
+    key_bounds as of KVCache.  A stored number is code * scale * unit; k_unit and v_unit are powers of
+    two: groups whose largest magnitude lies between 0.1 and 2688 units keep the codes' precision.
+    Takes KVCache's place in every call."""
+
+    _functions = ("exact_topk_cache4_write", "exact_topk_cache4_read", "exact_topk_cache4_block_scores",
+                  "exact_topk_cache4_attention_run")
+
+    def __init__(self, k, v, k_scale, v_scale, key_bounds, k_unit=1.0, v_unit=1.0):
+        _need_torch()
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be [num_pages, kv_heads, page_size, head_dim / 2]")
+        pages, heads, page, dim = *k.shape[:3], 2 * k.shape[3]
+        if pages < 1 or heads < 1 or page not in PAGE_SIZES or dim not in HEAD_DIMS:
+            raise ValueError(f"need pages, kv_heads >= 1, page_size in {PAGE_SIZES}, head_dim / 2 of head_dim in "
+                             f"{HEAD_DIMS}; got {list(k.shape)}")
+        if key_bounds.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"key_bounds must be bfloat16 or float16, got {key_bounds.dtype}")
+        for unit, name in ((k_unit, "k_unit"), (v_unit, "v_unit")):
+            if math.frexp(unit)[0] != 0.5 or not 2.0 ** -40 <= unit <= 2.0 ** 40:
+                raise ValueError(f"{name} must be a power of two between 2^-40 and 2^40, got {unit}")
+        self.device, self._index = k.device, k.device.index
+        if self.device.type != "cuda":
+            raise ValueError(f"the cache must be on a CUDA device, got {self.device}")
+        scales = (pages, heads, page, dim // GROUP)
+        for t, name, dtype, shape in ((k, "k", torch.uint8, k.shape), (v, "v", torch.uint8, k.shape),
+                                      (k_scale, "k_scale", torch.float8_e4m3fn, scales),
+                                      (v_scale, "v_scale", torch.float8_e4m3fn, scales),
+                                      (key_bounds, "key_bounds", key_bounds.dtype, (pages, heads, 2, dim))):
+            if t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.device != self.device:
+                raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+            if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {list(shape)}, got {list(t.shape)}")
+        self.k, self.v, self.k_scale, self.v_scale, self.key_bounds = k, v, k_scale, v_scale, key_bounds
+        self.num_pages, self.kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
+        self.k_unit, self.v_unit, self.dtype = float(k_unit), float(v_unit), key_bounds.dtype
+        self._c = _Cache4(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                          key_bounds.data_ptr(), pages, heads, page, dim,
+                          0 if self.dtype == torch.bfloat16 else 1, self.k_unit, self.v_unit)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def allocate(cls, num_pages, kv_heads, page_size, head_dim, dtype=None, device=None, k_unit=1.0, v_unit=1.0):
+        """A new cache with every page empty (codes, scales and bounds 0), ready for any stream."""
+        _need_torch()
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        shape = (num_pages, kv_heads, page_size)
+        k, v = (torch.zeros(*shape, head_dim // 2, dtype=torch.uint8, device=dev) for _ in range(2))
+        ks, vs = (torch.zeros(*shape, head_dim // GROUP, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+                  for _ in range(2))
+        bounds = torch.zeros(num_pages, kv_heads, 2, head_dim, dtype=dtype or torch.bfloat16, device=dev)
+        cache = cls(k, v, ks, vs, bounds, k_unit, v_unit)
+        with torch.cuda.device(cache.device):
+            _wait_for_buffers()  # tokens written on another stream must not meet the fills
+        return cache
+
+
 class SequenceBatch:
     """The sequences of a call: page_table int32 [num_seqs, table_width] (rows may be strided),
     kv_len int32 [num_seqs] with the call's own tokens counted in, and q_start int32 [num_seqs + 1],
@@ -278,11 +359,15 @@ def cache_write(cache, batch, k, v, stream=None):
 
     A page's scale is the power of two that brings its largest magnitude within e4m3's 448; a page
     continued by larger rows has its earlier codes rescaled, one written from its first offset starts
-    anew.  The key bounds follow.  Infinities and NaN are stored as NaN."""
+    anew.  The key bounds follow.  Infinities and NaN are stored as NaN.
+
+    In 4 bits (KVCache4) each 16 channels of a token have a scale of their own, the e4m3 number nearest to
+    their largest magnitude over 6 units; nothing of earlier tokens changes but their page's bounds.  An infinity
+    or NaN makes NaN of its 16 channels."""
     kr = _rows(k, "k", cache, cache.kv_heads)
     vr = _rows(v, "v", cache, cache.kv_heads, k.shape[0])
     batch._check(cache, k.shape[0])
-    _call(cache, stream, _lib().exact_topk_cache_write, cache._ref, batch._ref, k.shape[0], kr, vr)
+    _call(cache, stream, getattr(_lib(), cache._functions[0]), cache._ref, batch._ref, k.shape[0], kr, vr)
 
 
 def cache_read(cache, batch, num_tokens=None, out=None, stream=None):
@@ -303,7 +388,7 @@ def cache_read(cache, batch, num_tokens=None, out=None, stream=None):
     if not v.is_contiguous():
         _written(v, "out[1]", k)
     batch._check(cache, k.shape[0])
-    _call(cache, stream, _lib().exact_topk_cache_read, cache._ref, batch._ref, k.shape[0], kr, vr)
+    _call(cache, stream, getattr(_lib(), cache._functions[1]), cache._ref, batch._ref, k.shape[0], kr, vr)
     return k, v
 
 
@@ -346,7 +431,7 @@ def block_scores(cache, batch, q, keep_first=0, keep_last=0, scores=None, ke=Non
     if keep_first < 0 or keep_last < 0:
         raise ValueError("keep_first and keep_last must not be negative")
     most = batch.table_width
-    _call(cache, stream, _lib().exact_topk_block_scores, cache._ref, batch._ref, T, heads, qr,
+    _call(cache, stream, getattr(_lib(), cache._functions[2]), cache._ref, batch._ref, T, heads, qr,
           min(int(keep_first), most), min(int(keep_last), most), scores.data_ptr(), pitch, ke.data_ptr(),
           None if num_valid_rows is None else num_valid_rows.data_ptr())
     return scores, ke
@@ -367,8 +452,8 @@ def make_attention_plan(num_tokens, num_seqs, q_heads, kv_heads, head_dim, page_
 
 
 class CacheAttention:
-    """Attention of a batch's rows over their cached tokens, for one captured shape; owns its
-    plan, counters and workspace.
+    """Attention of a batch's rows over their cached tokens (of a KVCache or a KVCache4), for one captured
+    shape; owns its plan, counters and workspace.
 
     num_blocks=0 attends to every cached token up to the row's own; num_blocks=K to those of the pages
     listed for each token and key head (``blocks`` int32 [num_tokens * kv_heads, K], as ExactTopK selects
@@ -411,7 +496,7 @@ class CacheAttention:
                 raise ValueError(f"blocks must be contiguous [{plan.num_tokens * plan.kv_heads}, {plan.num_blocks}]")
         if scale is None:
             scale = 1.0 / math.sqrt(cache.head_dim)
-        _call(cache, stream, _lib().exact_topk_attention_run, self._plan, cache._ref, batch._ref, qr, outr,
+        _call(cache, stream, getattr(_lib(), cache._functions[3]), self._plan, cache._ref, batch._ref, qr, outr,
               None if blocks is None else blocks.data_ptr(), scale, *self._buffers)
         return out
 
@@ -421,15 +506,19 @@ class SparseAttention:
     attention over the pages selected for each token and key head.  Owns every buffer between.
 
     keep_first and keep_last pages (the sequence's first and newest) are always among the num_blocks
-    selected, which must be at least as many.  As of CacheAttention, calls of one object must not overlap
-    on the GPU, and the object is kept until its last call has run."""
+    selected, which must be at least as many.  rotary: a Rotary that turns q and k by their positions before
+    anything else.  As of CacheAttention, calls of one object must not overlap on the GPU, and the object is
+    kept until its last call has run."""
 
-    def __init__(self, cache, num_seqs, num_tokens, q_heads, table_width, num_blocks, keep_first=0, keep_last=1):
+    def __init__(self, cache, num_seqs, num_tokens, q_heads, table_width, num_blocks, keep_first=0, keep_last=1,
+                 rotary=None):
         if keep_first < 0 or keep_last < 0 or keep_first + keep_last > num_blocks:
             raise ValueError("need 0 <= keep_first + keep_last <= num_blocks")
         if num_tokens < 1 or num_blocks < 1:
             raise ValueError("need num_tokens, num_blocks >= 1")
-        self.cache, self.keep = cache, (keep_first, keep_last)
+        if rotary is not None and (rotary.device != cache.device or rotary.head_dim != cache.head_dim):
+            raise ValueError(f"the rotary must be on {cache.device} and of {cache.head_dim} channels")
+        self.cache, self.keep, self.rotary = cache, (keep_first, keep_last), rotary
         rows = num_tokens * cache.kv_heads
         self.attention = CacheAttention(cache, num_seqs, num_tokens, q_heads, table_width, num_blocks)
         self.select = _etk.ExactTopK(rows, table_width, num_blocks, device=cache.device)
@@ -438,6 +527,9 @@ class SparseAttention:
         self.ke = torch.zeros(rows, dtype=torch.int32, device=dev)
         self.live = torch.zeros(1, dtype=torch.int32, device=dev)
         self.blocks = torch.full((rows, num_blocks), -1, dtype=torch.int32, device=dev)
+        if rotary is not None:  # zeros: rows of no sequence are left as they are
+            self.turned = tuple(torch.zeros(num_tokens, h, cache.head_dim, dtype=cache.dtype, device=dev)
+                                for h in (q_heads, cache.kv_heads))
         with torch.cuda.device(dev):
             _wait_for_buffers()
 
@@ -451,6 +543,12 @@ class SparseAttention:
         if k is not None:
             if k.shape[0] != q.shape[0]:
                 raise ValueError("k, v and q must have the same tokens")
+        if self.rotary is not None:
+            if k is None:
+                q = self.rotary(q, batch=batch, out=self.turned[0], stream=stream)
+            else:
+                q, k = self.rotary(q, k, batch=batch, out=self.turned, stream=stream)
+        if k is not None:
             cache_write(self.cache, batch, k, v, stream=stream)
         block_scores(self.cache, batch, q, *self.keep, scores=self.scores, ke=self.ke,
                      num_valid_rows=self.live, stream=stream)

@@ -87,6 +87,12 @@ __device__ __forceinline__ void copy16(uint32_t to, const void* from, bool there
                : "memory");
 }
 
+// The first `bytes` of 16, and zeros behind them.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ void copy_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -128,23 +134,28 @@ __device__ __forceinline__ int page_units(const CacheArgs& c, const SeqRows& s) 
 
 // Steps that a warp holds in shared memory, all but one of them on their way: 48 KB of a
 // CTA where four share an SM, more where fewer do.
-constexpr int ring_steps(int dim, int tiles, int blocks) {
+constexpr int ring_steps(int dim, int tiles, int blocks, int bits) {
   const int ctas = attention_ctas_per_sm(tiles * 8, dim);
-  const int tokens = ctas == 4 ? 48 : (ctas == 3 ? 64 : 80);  // of 128 channels
+  // of 128 channels
+  const int tokens = bits == 8 ? (ctas == 4 ? 48 : (ctas == 3 ? 64 : 80))
+                               : (ctas == 4 ? 80 : (ctas == 3 ? 112 : 144));
   const int steps = tokens * 128 / dim / (16 * blocks);
   return steps;
 }
 
-// ST: blocks of 16 tokens in a step.
-template <int D, int NT, int ST>
+// ST: blocks of 16 tokens in a step. kBits: of a code.
+template <int D, int NT, int ST, int kBits>
 struct alignas(128) Shared {
   static constexpr int kRegs = D / 16 * NT * 4;  // output registers of a lane
   static constexpr int kRow = D + 8;             // halves of a query row, padded by 16 bytes
-  static constexpr int kRing = ring_steps(D, NT, ST);
-  static constexpr int kRingBytes = kWarps * kRing * 2 * 16 * ST * D;
+  static constexpr int kRing = ring_steps(D, NT, ST, kBits);
+  static constexpr int kCodes = 16 * ST * D * kBits / 8;             // bytes of a step's keys
+  static constexpr int kScales = kBits == 4 ? 16 * ST * D / 16 : 0;  // and of their scales
+  static constexpr int kStep = 2 * (kCodes + kScales);  // keys, values, and the scales of both
+  static constexpr int kRingBytes = kWarps * kRing * kStep;
   static constexpr int kOutBytes = kWarps * kRegs * 32 * 4;
   union {
-    uint8_t ring[kWarps][kRing][2][16 * ST * D];  // codes of keys and values
+    uint8_t ring[kWarps][kRing][kStep];
     float out[kWarps][kRegs][32];                 // after the last step
     // after the outputs: each partial result's factor for each column
     float weight[(kRingBytes > kOutBytes ? kRingBytes : kOutBytes) / 4];
@@ -289,16 +300,16 @@ __device__ __noinline__ void join_parts(const float* first, int parts, int64_t s
     }
 }
 
-template <int D, int NT, int ST>
+template <int D, int NT, int ST, int kBits>
 __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
-    attention_kernel(CacheArgs c, BatchArgs b, AttentionArgs a) {
+    attention_kernel(typename CacheOf<kBits>::Args c, BatchArgs b, AttentionArgs a) {
   constexpr int kTiles = D / 16;    // channel tiles of the output
   constexpr int kHalf = D / 64;     // 64-byte parts of a token's codes
   constexpr int kTokens = 16 * ST;  // of a step
   constexpr int kColumns = NT * 8;
   // query fragments in registers where there is room; else read at each step
   constexpr bool kHoldQ = D * NT <= 128;
-  using Smem = Shared<D, NT, ST>;
+  using Smem = Shared<D, NT, ST, kBits>;
   extern __shared__ __align__(128) unsigned char raw[];
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   // behind it: prefix sums of the sequences' units, then the members of each page (listed pages)
@@ -481,9 +492,14 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
       up = up < -120 ? -120 : (up > 120 ? 120 : up);
       const float by = __uint_as_float((uint32_t)(up + 127) << 23);
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i)
-        *reinterpret_cast<__half2*>(&sm.q[col][i * 64 + lane * 2]) =
+      for (int i = 0; i < D / 64; ++i) {
+        // a lane's 4-bit keys are 32 neighbouring channels of 128: its 16 of the first half of
+        // a row here, then its 16 of the second
+        int at = i * 64 + lane * 2;
+        if constexpr (kBits == 4 && D == 128) at = (at & 15) | (at >> 5) << 4 | (at >> 4 & 1) << 6;
+        *reinterpret_cast<__half2*>(&sm.q[col][at]) =
             __floats2half2_rn(x[i].x * by, x[i].y * by);
+      }
       if (lane == 0)
         sm.factor[col] =
             col < columns ? __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2 : 0.f;
@@ -558,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
     }
     const uint32_t everyone = (1u << t.tokens) - 1u;
     float unit = 1.f;  // the values' scale that o is held in
+    if constexpr (kBits == 4) unit = c.v_unit;
 
     // A warp keeps to 32 tokens of a page (a page of 16: all of it), in `per_page` steps:
     // those from `row0` on, of entries first_entry, first_entry + entry_step, ...
@@ -565,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
     const int row0 = (warp & ((1 << sub_shift) - 1)) * 32;
     const int first_entry = warp >> sub_shift, entry_step = kWarps >> sub_shift;
     const int per_page = (c.page < 32 ? c.page : 32) / kTokens;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0][0]);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0][0]);
 
     for (int chunk0 = from; chunk0 < to; chunk0 += kChunk) {
       const int entries = to - chunk0 < kChunk ? to - chunk0 : kChunk;
@@ -593,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
         if (!listed) sm.entry[i] = (uint32_t)place;
         const int64_t tile = (int64_t)page * c.heads + t.head;
         sm.offset[i] = page >= 0 ? tile * c.page * D : -1;
-        if (page >= 0)
+        if (kBits == 8 && page >= 0)
           sm.scale[i] = make_float2(__ldg(c.k_scale + tile), __ldg(c.v_scale + tile));
       }
       __syncthreads();
@@ -610,16 +627,41 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
           const int row = row0 + fetch_step * kTokens;
           const int rows = most - (place << c.page_shift) - row;  // tokens that anyone sees
           if (offset >= 0 && rows > 0) {
-            const int64_t at = offset + row * D + lane * 16;
-            const uint32_t to = ring + place_in_ring * (2 * kTokens * D);
+            const uint32_t to = ring + place_in_ring * Smem::kStep;
+            if constexpr (kBits == 8) {
+              const int64_t at = offset + row * D + lane * 16;
 #pragma unroll
-            for (int j = 0; j < kTokens * D / 512; ++j) {
-              const int piece = lane + 32 * j, line = piece >> 3, p = piece & 7;
-              const bool there = (D == 128 ? line : piece >> 2) < rows;
-              const int pk = D == 128 ? p ^ ((line & 1) << 2) : p;
-              const int pv = D == 128 ? p ^ ((line >> 1 & 3) << 1) : p ^ ((line & 3) << 1);
-              copy16(to + line * 128 + pk * 16, c.k + at + j * 512, there);
-              copy16(to + kTokens * D + line * 128 + pv * 16, c.v + at + j * 512, there);
+              for (int j = 0; j < kTokens * D / 512; ++j) {
+                const int piece = lane + 32 * j, line = piece >> 3, p = piece & 7;
+                const bool there = (D == 128 ? line : piece >> 2) < rows;
+                const int pk = D == 128 ? p ^ ((line & 1) << 2) : p;
+                const int pv = D == 128 ? p ^ ((line >> 1 & 3) << 1) : p ^ ((line & 3) << 1);
+                copy16(to + line * 128 + pk * 16, c.k + at + j * 512, there);
+                copy16(to + kTokens * D + line * 128 + pv * 16, c.v + at + j * 512, there);
+              }
+            } else {
+              // A line of 128 bytes is 2 tokens of 128 channels or 4 of 64.
+              const int64_t at = (offset + row * D) / 2 + lane * 16;
+#pragma unroll
+              for (int j = 0; j < kTokens * D / 1024; ++j) {
+                const int piece = lane + 32 * j, line = piece >> 3, p = piece & 7;
+                const bool there = (D == 128 ? piece >> 2 : piece >> 1) < rows;
+                const int pv = p ^ ((line & (D == 128 ? 3 : 1)) << 1);
+                copy16(to + line * 128 + p * 16, c.k + at + j * 512, there);
+                copy16(to + Smem::kCodes + line * 128 + pv * 16, c.v + at + j * 512, there);
+              }
+              // A piece of scales is 2 (4) tokens, zeros behind the last that anyone sees.
+              constexpr int kPieces = Smem::kScales / 16, kBytes = D / 16;
+              static_assert(kPieces * 2 <= 32, "a piece a lane");
+              if (lane < 2 * kPieces) {
+                const int piece = lane % kPieces;
+                const int bytes = (rows - piece * (16 / kBytes)) * kBytes;
+                const uint8_t* const scales =
+                    reinterpret_cast<const uint8_t*>(lane < kPieces ? c.k_scale : c.v_scale);
+                copy16(to + 2 * Smem::kCodes + lane * 16,
+                       scales + (offset + row * D) / 16 + piece * 16,
+                       bytes < 0 ? 0 : (bytes < 16 ? bytes : 16));
+              }
             }
           }
           if (++fetch_step == per_page) {
@@ -636,8 +678,8 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
         const int pos = (place << c.page_shift) + row0 + step * kTokens;
         if (sm.offset[e] < 0 || pos >= most) return;
         const uint32_t members = listed ? entry >> 24 : everyone;
-        const float2 scale = sm.scale[e];
-        const uint8_t* const codes = &sm.ring[warp][place_in_ring][0][0];
+        const float2 scale = kBits == 8 ? sm.scale[e] : make_float2(1.f, unit);
+        const uint8_t* const codes = &sm.ring[warp][place_in_ring][0];
         // Eight columns of which no token takes the page are left out. Where some do and
         // some do not, or the step ends beyond a token, scores are masked.
         bool takes[NT];
@@ -653,6 +695,41 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
 #pragma unroll
         for (int st = 0; st < ST; ++st) {
           uint32_t f[D / 16][4];
+          if constexpr (kBits == 4) {
+            // two rows, each 16 codes with a scale of their own for each p
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int row = st * 16 + g + 8 * r;
+              const uint8_t* const at = codes + (row * 4 + q4) * (D / 8);
+              const uint8_t* const scale_at = codes + 2 * Smem::kCodes + row * (D / 16) + q4 * kHalf;
+              uint32_t w[kHalf][2], s[kHalf];
+              if constexpr (D == 128) {
+                const uint4 u = *reinterpret_cast<const uint4*>(at);
+                w[0][0] = u.x;
+                w[0][1] = u.y;
+                w[kHalf - 1][0] = u.z;
+                w[kHalf - 1][1] = u.w;
+                const uint32_t both = codes_to_half2(*reinterpret_cast<const uint16_t*>(scale_at));
+                s[0] = __byte_perm(both, 0u, 0x1010);
+                s[kHalf - 1] = __byte_perm(both, 0u, 0x3232);
+              } else {
+                const uint2 u = *reinterpret_cast<const uint2*>(at);
+                w[0][0] = u.x;
+                w[0][1] = u.y;
+                s[0] = scale_to_half2(*scale_at);
+              }
+#pragma unroll
+              for (int p = 0; p < kHalf; ++p)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  uint32_t y[4];
+                  codes4_to_half2(w[p][k], y);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    f[p * 4 + k * 2 + (i >> 1)][(i & 1) * 2 + r] = times2(y[i], s[p]);
+                }
+            }
+          } else {
 #pragma unroll
           for (int p = 0; p < kHalf; ++p) {
             uint4 w[2];
@@ -670,6 +747,7 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
               f[p * 4 + k][1] = codes_to_half2((uint16_t)w1);
               f[p * 4 + k][3] = codes_to_half2((uint16_t)(w1 >> 16));
             }
+          }
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
@@ -697,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
         }
 
         // ---- probabilities ----
-        if (scale.y != unit) {
+        if (kBits == 8 && scale.y != unit) {
           const float by = unit / scale.y;
           unit = scale.y;
 #pragma unroll
@@ -774,6 +852,61 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
         for (int st = 0; st < ST; ++st) {
           // ---- values: tokens 2c, 2c+1, 2c+8, 2c+9 of 16 (8) channels ----
           uint4 v[4];
+          uint32_t vs[2] = {0u, 0u};  // 4 bits: scales of tokens 2c and 2c+1, 2c+8 and 2c+9
+          if constexpr (kBits == 4) {
+            uint32_t byte[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int row = st * 16 + q4 * 2 + (r & 1) + (r >> 1) * 8;
+              const uint8_t* const at = codes + Smem::kCodes;
+              if (D == 128) {
+                const int line = row >> 1, p = (row & 1) * 4 + (g >> 1);
+                const uint2 both = *reinterpret_cast<const uint2*>(
+                    at + line * 128 + (p ^ ((line & 3) << 1)) * 16 + (g & 1) * 8);
+                v[r] = make_uint4(both.x, both.y, 0u, 0u);
+              } else {
+                const int line = row >> 2, p = (row & 3) * 2 + (g >> 2);
+                v[r] = make_uint4(*reinterpret_cast<const uint32_t*>(
+                                      at + line * 128 + (p ^ ((line & 1) << 1)) * 16 + (g & 3) * 4),
+                                  0u, 0u, 0u);
+              }
+              byte[r] = codes[2 * Smem::kCodes + Smem::kScales + row * (D / 16) +
+                              (D == 128 ? g : g >> 1)];
+            }
+            vs[0] = byte[0] | byte[1] << 8;
+            vs[1] = byte[2] | byte[3] << 8;
+            // A NaN among the scales, as of the codes below: of all of the lane's channels at once.
+            if (masked) {
+              uint32_t one[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                one[i] = ((vs[i] & 0x7Fu) == 0x7Fu ? 0x3C00u : 0u) |
+                         ((vs[i] & 0x7F00u) == 0x7F00u ? 0x3C000000u : 0u);
+              if (__any_sync(~0u, (one[0] | one[1]) != 0u)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  if (!takes[n]) continue;
+                  const uint32_t bits = seen[st] >> (n * 4);
+                  const uint32_t s0 = transpose8((bits & 1u ? 0x3C00u : 0u) |
+                                                 (bits & 2u ? 0x3C000000u : 0u));
+                  const uint32_t s1 = transpose8((bits & 4u ? 0x3C00u : 0u) |
+                                                 (bits & 8u ? 0x3C000000u : 0u));
+                  float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma(hit, one[0], one[0], one[1], one[1], s0, s1);
+#pragma unroll
+                  for (int k = 0; k < kTiles; ++k)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                      if (hit[r] > 0.f) o[k][n][r] = __uint_as_float(0x7FFFFFFFu);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  vs[i] &= (one[i] & 0xFFFFu ? 0u : 0xFFu) | (one[i] >> 16 ? 0u : 0xFF00u);
+              }
+            }
+            vs[0] = codes_to_half2((uint16_t)vs[0]);
+            vs[1] = codes_to_half2((uint16_t)vs[1]);
+          } else {
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const int row = st * 16 + q4 * 2 + (r & 1) + (r >> 1) * 8;
@@ -788,10 +921,11 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
               v[r] = make_uint4(half.x, half.y, 0u, 0u);
             }
           }
+          }
           // A value that is NaN makes NaN of the columns that see its token, and of no
           // other: where not every column sees every token, such values are taken out
           // of the product, and a product of ones marks the outputs that they reach.
-          if (masked) {
+          if (kBits == 8 && masked) {
             uint32_t bad = 0u;
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -837,11 +971,27 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
             }
           }
 
-          // ---- O^T, half of the channels at a time ----
-          constexpr int kPart = kTiles / 2;
+          // ---- O^T, half of the channels at a time (64 in 4 bits: all of them) ----
+          constexpr int kPart = kBits == 4 ? 4 : kTiles / 2;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < kTiles / kPart; ++half) {
             uint32_t f[kPart][4];
+            if constexpr (kBits == 4) {
+              // Codes of two tokens side by side in a byte, even channels and odd ones apart: four
+              // tiles are a word of each token.
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t v0 = word(v[2 * i], half), v1 = word(v[2 * i + 1], half);
+                uint32_t even[4], odd[4];
+                codes4_to_half2((v0 & 0x0F0F0F0Fu) | (v1 << 4 & 0xF0F0F0F0u), even);
+                codes4_to_half2((v0 >> 4 & 0x0F0F0F0Fu) | (v1 & 0xF0F0F0F0u), odd);
+#pragma unroll
+                for (int k = 0; k < kPart; ++k) {
+                  f[k][2 * i] = times2(even[k], vs[i]);
+                  f[k][2 * i + 1] = times2(odd[k], vs[i]);
+                }
+              }
+            } else {
 #pragma unroll
             for (int k = 0; k < kPart; ++k) {
               const int tile = half * kPart + k;
@@ -853,6 +1003,7 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
               f[k][1] = codes_to_half2((uint16_t)(w0 >> 16));
               f[k][2] = codes_to_half2((uint16_t)w1);
               f[k][3] = codes_to_half2((uint16_t)(w1 >> 16));
+            }
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -1000,25 +1151,43 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
   }
 }
 
-template <int D, int NT, int ST>
-int launch_tile(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a,
+template <int D, int NT, int ST, int kBits>
+int launch_tile(const typename CacheOf<kBits>::Args& c, const BatchArgs& b, const AttentionArgs& a,
                 cudaStream_t stream) {
-  constexpr size_t most = sizeof(Shared<D, NT, ST>) + sizeof(int64_t) * (EXACT_TOPK_MAX_SEQS + 1) +
+  using Smem = Shared<D, NT, ST, kBits>;
+  constexpr size_t most = sizeof(Smem) + sizeof(int64_t) * (EXACT_TOPK_MAX_SEQS + 1) +
                           EXACT_TOPK_MAX_LISTED_WIDTH;
   static_assert(most <= kMostShared, "every call that the checks let through");
-  const size_t smem = sizeof(Shared<D, NT, ST>) + sizeof(int64_t) * ((size_t)b.num_seqs + 1) +
+  const size_t smem = sizeof(Smem) + sizeof(int64_t) * ((size_t)b.num_seqs + 1) +
                       (a.blocks != nullptr ? ((size_t)b.width + 3) / 4 * 4 : 0);
   // Set on every call: a host-side table entry, cheaper than remembering it per device. The limit
   // belongs to the kernel and not to the call, so it is the largest call's: another thread's
   // launch may come between this thread's setting and its own launch.
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(attention_kernel<D, NT, ST>,
+  if (smem > 48 * 1024 && cudaFuncSetAttribute(attention_kernel<D, NT, ST, kBits>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)most) != cudaSuccess) {
     cudaGetLastError();
     return EXACT_TOPK_ERR_CUDA;
   }
-  attention_kernel<D, NT, ST><<<a.workers, kThreads, smem, stream>>>(c, b, a);
+  attention_kernel<D, NT, ST, kBits><<<a.workers, kThreads, smem, stream>>>(c, b, a);
   return launch_status();
+}
+
+template <int D, int ST, int kBits>
+int launch_columns(const typename CacheOf<kBits>::Args& c, const BatchArgs& b,
+                   const AttentionArgs& a, cudaStream_t stream) {
+  if (a.columns == 8) return launch_tile<D, 1, ST, kBits>(c, b, a, stream);
+  if (a.columns == 16) return launch_tile<D, 2, ST, kBits>(c, b, a, stream);
+  return launch_tile<D, 4, ST, kBits>(c, b, a, stream);
+}
+
+template <int kBits>
+int launch_bits(const typename CacheOf<kBits>::Args& c, const BatchArgs& b, const AttentionArgs& a,
+                cudaStream_t stream) {
+  if (c.dim == 128) return launch_columns<128, 1, kBits>(c, b, a, stream);
+  // Steps of 2 KB of keys and of values (in 8 bits). Pages of 16 tokens have half of that.
+  if (c.page == 16) return launch_columns<64, 1, kBits>(c, b, a, stream);
+  return launch_columns<64, 2, kBits>(c, b, a, stream);
 }
 
 }  // namespace
@@ -1029,20 +1198,16 @@ int launch_attention(const CacheArgs& c, const BatchArgs& b, const AttentionArgs
     const int rc = launch_prompt_attention(c, b, a, stream);
     if (rc != EXACT_TOPK_OK) return rc;
   }
-  if (c.dim == 128) {
-    if (a.columns == 8) return launch_tile<128, 1, 1>(c, b, a, stream);
-    if (a.columns == 16) return launch_tile<128, 2, 1>(c, b, a, stream);
-    return launch_tile<128, 4, 1>(c, b, a, stream);
+  return launch_bits<8>(c, b, a, stream);
+}
+
+int launch_attention4(const Cache4Args& c, const BatchArgs& b, const AttentionArgs& a,
+                      cudaStream_t stream) {
+  if (a.prompt_tokens > 0) {
+    const int rc = launch_prompt_attention4(c, b, a, stream);
+    if (rc != EXACT_TOPK_OK) return rc;
   }
-  // Steps of 2 KB of keys and of values. Pages of 16 tokens have half of that.
-  if (c.page == 16) {
-    if (a.columns == 8) return launch_tile<64, 1, 1>(c, b, a, stream);
-    if (a.columns == 16) return launch_tile<64, 2, 1>(c, b, a, stream);
-    return launch_tile<64, 4, 1>(c, b, a, stream);
-  }
-  if (a.columns == 8) return launch_tile<64, 1, 2>(c, b, a, stream);
-  if (a.columns == 16) return launch_tile<64, 2, 2>(c, b, a, stream);
-  return launch_tile<64, 4, 2>(c, b, a, stream);
+  return launch_bits<4>(c, b, a, stream);
 }
 
 }  // namespace etk

@@ -15,7 +15,9 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 bool page_size_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 
-int check_cache(const exact_topk_cache* cache, CacheArgs* out) {
+// What the caches of 8 and of 4 bits have in common.
+template <class Cache>
+int check_pages(const Cache* cache, uintptr_t scale_alignment, CacheArgs* out) {
   if (cache == nullptr || cache->k == nullptr || cache->v == nullptr ||
       cache->k_scale == nullptr || cache->v_scale == nullptr)
     return EXACT_TOPK_ERR_NULL_POINTER;
@@ -25,12 +27,12 @@ int check_cache(const exact_topk_cache* cache, CacheArgs* out) {
       (cache->type != EXACT_TOPK_TYPE_BF16 && cache->type != EXACT_TOPK_TYPE_FP16))
     return EXACT_TOPK_ERR_BAD_CACHE;
   if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(cache->key_bounds, 16) ||
-      !aligned(cache->k_scale, 4) || !aligned(cache->v_scale, 4))
+      !aligned(cache->k_scale, scale_alignment) || !aligned(cache->v_scale, scale_alignment))
     return EXACT_TOPK_ERR_MISALIGNED;
   out->k = static_cast<uint8_t*>(cache->k);
   out->v = static_cast<uint8_t*>(cache->v);
-  out->k_scale = cache->k_scale;
-  out->v_scale = cache->v_scale;
+  out->k_scale = static_cast<float*>(cache->k_scale);
+  out->v_scale = static_cast<float*>(cache->v_scale);
   out->bounds = cache->key_bounds;
   out->num_pages = cache->num_pages;
   out->heads = cache->kv_heads;
@@ -39,6 +41,25 @@ int check_cache(const exact_topk_cache* cache, CacheArgs* out) {
   while ((1 << out->page_shift) < cache->page_size) ++out->page_shift;
   out->dim = cache->head_dim;
   out->fp16 = cache->type == EXACT_TOPK_TYPE_FP16;
+  return EXACT_TOPK_OK;
+}
+
+int check_cache(const exact_topk_cache* cache, CacheArgs* out) {
+  return check_pages(cache, 4, out);
+}
+
+bool unit_ok(float unit) {
+  int e;
+  return std::frexp(unit, &e) == 0.5f && e - 1 >= EXACT_TOPK_SCALE_MIN_EXP &&
+         e - 1 <= EXACT_TOPK_SCALE_MAX_EXP;
+}
+
+int check_cache(const exact_topk_cache4* cache, Cache4Args* out) {
+  const int rc = check_pages(cache, 16, out);
+  if (rc != EXACT_TOPK_OK) return rc;
+  if (!unit_ok(cache->k_unit) || !unit_ok(cache->v_unit)) return EXACT_TOPK_ERR_BAD_CACHE;
+  out->k_unit = cache->k_unit;
+  out->v_unit = cache->v_unit;
   return EXACT_TOPK_OK;
 }
 
@@ -99,14 +120,132 @@ bool heads_ok(int q_heads, int kv_heads) {
 }
 
 // What the cache's writer and reader check alike.
-int check_move(const exact_topk_cache* cache, const exact_topk_batch* batch, int64_t num_tokens,
-               const exact_topk_rows* k, const exact_topk_rows* v, CacheArgs* c, BatchArgs* b,
+template <class Cache, class Args>
+int check_move(const Cache* cache, const exact_topk_batch* batch, int64_t num_tokens,
+               const exact_topk_rows* k, const exact_topk_rows* v, Args* c, BatchArgs* b,
                RowArgs* kr, RowArgs* vr) {
   int rc = check_cache(cache, c);
   if (rc == EXACT_TOPK_OK) rc = check_batch(batch, num_tokens, c->page, b);
   if (rc == EXACT_TOPK_OK) rc = check_rows(k, num_tokens, kr);
   if (rc == EXACT_TOPK_OK) rc = check_rows(v, num_tokens, vr);
   return rc;
+}
+
+// Page scores are of the bounds alone: the same for every cache that has them.
+template <class Args, class Cache>
+int block_scores(const Cache* cache, const exact_topk_batch* batch, int64_t num_tokens, int q_heads,
+                 const exact_topk_rows* q, int keep_first, int keep_last, float* scores,
+                 int64_t row_pitch, int32_t* ke, int32_t* num_valid_rows,
+                 struct CUstream_st* stream) {
+  Args c;
+  BatchArgs b;
+  ScoreArgs a;
+  int rc = check_cache(cache, &c);
+  if (rc == EXACT_TOPK_OK) rc = check_batch(batch, num_tokens, c.page, &b);
+  if (rc == EXACT_TOPK_OK) rc = check_rows(q, num_tokens, &a.q);
+  if (rc != EXACT_TOPK_OK) return rc;
+  if (c.bounds == nullptr || (num_tokens > 0 && (scores == nullptr || ke == nullptr)))
+    return EXACT_TOPK_ERR_NULL_POINTER;
+  if (!heads_ok(q_heads, c.heads)) return EXACT_TOPK_ERR_BAD_HEADS;
+  if (row_pitch < b.width || keep_first < 0 || keep_last < 0 ||
+      num_tokens * c.heads > 0x7FFFFFFF)
+    return EXACT_TOPK_ERR_BAD_SHAPE;
+  if (!aligned(scores, 4) || !aligned(ke, 4) || !aligned(num_valid_rows, 4))
+    return EXACT_TOPK_ERR_MISALIGNED;
+  a.scores = scores;
+  a.ke = ke;
+  a.num_valid_rows = num_valid_rows;
+  a.row_pitch = row_pitch;
+  a.group = q_heads / c.heads;
+  a.keep_first = keep_first;
+  a.keep_last = keep_last;
+  if (num_tokens == 0) {  // no rows: only their count is asked for
+    if (num_valid_rows != nullptr &&
+        cudaMemsetAsync(num_valid_rows, 0, sizeof(int32_t),
+                        reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return EXACT_TOPK_ERR_CUDA;
+    return EXACT_TOPK_OK;
+  }
+  return launch_block_scores(c, b, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+float key_unit(const CacheArgs&) { return 1.f; }
+float key_unit(const Cache4Args& c) { return c.k_unit; }
+
+int launch(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a, cudaStream_t stream) {
+  return launch_attention(c, b, a, stream);
+}
+int launch(const Cache4Args& c, const BatchArgs& b, const AttentionArgs& a, cudaStream_t stream) {
+  return launch_attention4(c, b, a, stream);
+}
+
+template <class Args, class Cache>
+int attention_run(const exact_topk_attention_plan* plan, const Cache* cache,
+                  const exact_topk_batch* batch, const exact_topk_rows* q,
+                  const exact_topk_rows* out, const int32_t* blocks, float scale, void* counters,
+                  size_t counter_bytes, void* workspace, size_t workspace_bytes,
+                  struct CUstream_st* stream) {
+  Args c;
+  BatchArgs b;
+  AttentionArgs a;
+  if (plan == nullptr || counters == nullptr || workspace == nullptr)
+    return EXACT_TOPK_ERR_NULL_POINTER;
+  int rc = check_cache(cache, &c);
+  if (rc == EXACT_TOPK_OK) rc = check_batch(batch, plan->num_tokens, c.page, &b);
+  if (rc == EXACT_TOPK_OK) rc = check_rows(q, plan->num_tokens, &a.q);
+  if (rc == EXACT_TOPK_OK) rc = check_rows(out, plan->num_tokens, &a.out);
+  if (rc != EXACT_TOPK_OK) return rc;
+  if (plan->num_blocks > 0 && blocks == nullptr) return EXACT_TOPK_ERR_NULL_POINTER;
+  if (!heads_ok(plan->q_heads, c.heads) || plan->num_tokens * plan->q_heads > 0x7FFFFFFF)
+    return EXACT_TOPK_ERR_BAD_HEADS;
+  if (plan->num_blocks < 0 || plan->num_blocks > EXACT_TOPK_MAX_K) return EXACT_TOPK_ERR_BAD_K;
+  const int group = plan->q_heads / c.heads;
+  a.scale_log2 = scale * 1.4426950408889634f * key_unit(c);
+  if (plan->kv_heads != c.heads || plan->head_dim != c.dim || plan->page_size != c.page ||
+      plan->table_width != b.width || plan->num_seqs != b.num_seqs ||
+      (plan->num_blocks == 0 && blocks != nullptr) ||
+      (plan->num_blocks > 0 && b.width > EXACT_TOPK_MAX_LISTED_WIDTH) ||
+      (plan->columns != 8 && plan->columns != 16 && plan->columns != 32) || plan->tile_heads < 1 ||
+      plan->tile_heads > group || plan->tile_tokens < 1 || plan->tile_tokens > 8 ||
+      plan->tile_tokens * plan->tile_heads > plan->columns || plan->workers < 1 ||
+      plan->workers > most_workers(plan->columns, c.dim) || plan->min_units < 1 ||
+      !std::isfinite(a.scale_log2) || plan->prompt_tokens < 0 ||
+      plan->prompt_tokens > kPromptTokens)
+    return EXACT_TOPK_ERR_BAD_PLAN;
+  // A tile of the kernel that runs behind the prompt's lies within one of that one's.
+  if (plan->prompt_tokens > 0 &&
+      (plan->prompt_heads < 1 || plan->prompt_heads > group ||
+       plan->prompt_tokens * plan->prompt_heads > kPromptRows ||
+       (plan->prompt_heads != group && plan->prompt_heads % plan->tile_heads != 0) ||
+       (plan->num_blocks > 0 && b.width > kPromptListedWidth)))
+    return EXACT_TOPK_ERR_BAD_PLAN;
+  if (counter_bytes < plan->counter_bytes || counter_bytes < (size_t)plan->workers * 4)
+    return EXACT_TOPK_ERR_COUNTERS_TOO_SMALL;
+  const uint64_t partial = partial_bytes(*plan, c.dim);
+  if (workspace_bytes < plan->workspace_bytes ||
+      workspace_bytes < partial + again_bytes(*plan, group))
+    return EXACT_TOPK_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(counters, 16) || !aligned(workspace, 16) || !aligned(blocks, 4))
+    return EXACT_TOPK_ERR_MISALIGNED;
+  if (plan->num_tokens == 0) return EXACT_TOPK_OK;
+  a.blocks = blocks;
+  a.counters = static_cast<int32_t*>(counters);
+  a.partial = static_cast<float*>(workspace);
+  a.num_blocks = plan->num_blocks;
+  a.group = group;
+  a.columns = plan->columns;
+  a.tile_tokens = plan->tile_tokens;
+  a.tile_heads = plan->tile_heads;
+  a.workers = plan->workers;
+  a.min_units = plan->min_units;
+  a.prompt_tokens = plan->prompt_tokens;
+  a.prompt_heads = plan->prompt_heads;
+  a.again = plan->prompt_tokens > 0 ? static_cast<uint8_t*>(workspace) + partial : nullptr;
+  a.group_parts = (group + plan->tile_heads - 1) / plan->tile_heads;
+  // a part of a listed tile: at least 128 tokens, 32 for each warp
+  a.max_cut = plan->num_blocks * c.page / 128;
+  if (a.max_cut < 1) a.max_cut = 1;
+  return launch(c, b, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
 std::atomic<uint32_t> g_wait_limit{kWaitLimit};
@@ -147,36 +286,39 @@ int exact_topk_block_scores(const exact_topk_cache* cache, const exact_topk_batc
                             int64_t num_tokens, int q_heads, const exact_topk_rows* q,
                             int keep_first, int keep_last, float* scores, int64_t row_pitch,
                             int32_t* ke, int32_t* num_valid_rows, struct CUstream_st* stream) {
-  CacheArgs c;
+  return block_scores<CacheArgs>(cache, batch, num_tokens, q_heads, q, keep_first, keep_last,
+                                 scores, row_pitch, ke, num_valid_rows, stream);
+}
+
+int exact_topk_cache4_write(const exact_topk_cache4* cache, const exact_topk_batch* batch,
+                            int64_t num_tokens, const exact_topk_rows* k,
+                            const exact_topk_rows* v, struct CUstream_st* stream) {
+  Cache4Args c;
   BatchArgs b;
-  ScoreArgs a;
-  int rc = check_cache(cache, &c);
-  if (rc == EXACT_TOPK_OK) rc = check_batch(batch, num_tokens, c.page, &b);
-  if (rc == EXACT_TOPK_OK) rc = check_rows(q, num_tokens, &a.q);
-  if (rc != EXACT_TOPK_OK) return rc;
-  if (c.bounds == nullptr || (num_tokens > 0 && (scores == nullptr || ke == nullptr)))
-    return EXACT_TOPK_ERR_NULL_POINTER;
-  if (!heads_ok(q_heads, c.heads)) return EXACT_TOPK_ERR_BAD_HEADS;
-  if (row_pitch < b.width || keep_first < 0 || keep_last < 0 ||
-      num_tokens * c.heads > 0x7FFFFFFF)
-    return EXACT_TOPK_ERR_BAD_SHAPE;
-  if (!aligned(scores, 4) || !aligned(ke, 4) || !aligned(num_valid_rows, 4))
-    return EXACT_TOPK_ERR_MISALIGNED;
-  a.scores = scores;
-  a.ke = ke;
-  a.num_valid_rows = num_valid_rows;
-  a.row_pitch = row_pitch;
-  a.group = q_heads / c.heads;
-  a.keep_first = keep_first;
-  a.keep_last = keep_last;
-  if (num_tokens == 0) {  // no rows: only their count is asked for
-    if (num_valid_rows != nullptr &&
-        cudaMemsetAsync(num_valid_rows, 0, sizeof(int32_t),
-                        reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
-      return EXACT_TOPK_ERR_CUDA;
-    return EXACT_TOPK_OK;
-  }
-  return launch_block_scores(c, b, a, reinterpret_cast<cudaStream_t>(stream));
+  RowArgs kr, vr;
+  const int rc = check_move(cache, batch, num_tokens, k, v, &c, &b, &kr, &vr);
+  if (rc != EXACT_TOPK_OK || num_tokens == 0) return rc;
+  return launch_cache4_write(c, b, kr, vr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int exact_topk_cache4_read(const exact_topk_cache4* cache, const exact_topk_batch* batch,
+                           int64_t num_tokens, const exact_topk_rows* k, const exact_topk_rows* v,
+                           struct CUstream_st* stream) {
+  Cache4Args c;
+  BatchArgs b;
+  RowArgs kr, vr;
+  const int rc = check_move(cache, batch, num_tokens, k, v, &c, &b, &kr, &vr);
+  if (rc != EXACT_TOPK_OK || num_tokens == 0) return rc;
+  return launch_cache4_read(c, b, kr, vr, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int exact_topk_cache4_block_scores(const exact_topk_cache4* cache, const exact_topk_batch* batch,
+                                   int64_t num_tokens, int q_heads, const exact_topk_rows* q,
+                                   int keep_first, int keep_last, float* scores,
+                                   int64_t row_pitch, int32_t* ke, int32_t* num_valid_rows,
+                                   struct CUstream_st* stream) {
+  return block_scores<Cache4Args>(cache, batch, num_tokens, q_heads, q, keep_first, keep_last,
+                                  scores, row_pitch, ke, num_valid_rows, stream);
 }
 
 int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_rows, int q_heads,
@@ -253,67 +395,18 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
                              const exact_topk_rows* out, const int32_t* blocks, float scale,
                              void* counters, size_t counter_bytes, void* workspace,
                              size_t workspace_bytes, struct CUstream_st* stream) {
-  CacheArgs c;
-  BatchArgs b;
-  AttentionArgs a;
-  if (plan == nullptr || counters == nullptr || workspace == nullptr)
-    return EXACT_TOPK_ERR_NULL_POINTER;
-  int rc = check_cache(cache, &c);
-  if (rc == EXACT_TOPK_OK) rc = check_batch(batch, plan->num_tokens, c.page, &b);
-  if (rc == EXACT_TOPK_OK) rc = check_rows(q, plan->num_tokens, &a.q);
-  if (rc == EXACT_TOPK_OK) rc = check_rows(out, plan->num_tokens, &a.out);
-  if (rc != EXACT_TOPK_OK) return rc;
-  if (plan->num_blocks > 0 && blocks == nullptr) return EXACT_TOPK_ERR_NULL_POINTER;
-  if (!heads_ok(plan->q_heads, c.heads) || plan->num_tokens * plan->q_heads > 0x7FFFFFFF)
-    return EXACT_TOPK_ERR_BAD_HEADS;
-  if (plan->num_blocks < 0 || plan->num_blocks > EXACT_TOPK_MAX_K) return EXACT_TOPK_ERR_BAD_K;
-  const int group = plan->q_heads / c.heads;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  if (plan->kv_heads != c.heads || plan->head_dim != c.dim || plan->page_size != c.page ||
-      plan->table_width != b.width || plan->num_seqs != b.num_seqs ||
-      (plan->num_blocks == 0 && blocks != nullptr) ||
-      (plan->num_blocks > 0 && b.width > EXACT_TOPK_MAX_LISTED_WIDTH) ||
-      (plan->columns != 8 && plan->columns != 16 && plan->columns != 32) || plan->tile_heads < 1 ||
-      plan->tile_heads > group || plan->tile_tokens < 1 || plan->tile_tokens > 8 ||
-      plan->tile_tokens * plan->tile_heads > plan->columns || plan->workers < 1 ||
-      plan->workers > most_workers(plan->columns, c.dim) || plan->min_units < 1 ||
-      !std::isfinite(a.scale_log2) || plan->prompt_tokens < 0 ||
-      plan->prompt_tokens > kPromptTokens)
-    return EXACT_TOPK_ERR_BAD_PLAN;
-  // A tile of the kernel that runs behind the prompt's lies within one of that one's.
-  if (plan->prompt_tokens > 0 &&
-      (plan->prompt_heads < 1 || plan->prompt_heads > group ||
-       plan->prompt_tokens * plan->prompt_heads > kPromptRows ||
-       (plan->prompt_heads != group && plan->prompt_heads % plan->tile_heads != 0) ||
-       (plan->num_blocks > 0 && b.width > kPromptListedWidth)))
-    return EXACT_TOPK_ERR_BAD_PLAN;
-  if (counter_bytes < plan->counter_bytes || counter_bytes < (size_t)plan->workers * 4)
-    return EXACT_TOPK_ERR_COUNTERS_TOO_SMALL;
-  const uint64_t partial = partial_bytes(*plan, c.dim);
-  if (workspace_bytes < plan->workspace_bytes ||
-      workspace_bytes < partial + again_bytes(*plan, group))
-    return EXACT_TOPK_ERR_WORKSPACE_TOO_SMALL;
-  if (!aligned(counters, 16) || !aligned(workspace, 16) || !aligned(blocks, 4))
-    return EXACT_TOPK_ERR_MISALIGNED;
-  if (plan->num_tokens == 0) return EXACT_TOPK_OK;
-  a.blocks = blocks;
-  a.counters = static_cast<int32_t*>(counters);
-  a.partial = static_cast<float*>(workspace);
-  a.num_blocks = plan->num_blocks;
-  a.group = group;
-  a.columns = plan->columns;
-  a.tile_tokens = plan->tile_tokens;
-  a.tile_heads = plan->tile_heads;
-  a.workers = plan->workers;
-  a.min_units = plan->min_units;
-  a.prompt_tokens = plan->prompt_tokens;
-  a.prompt_heads = plan->prompt_heads;
-  a.again = plan->prompt_tokens > 0 ? static_cast<uint8_t*>(workspace) + partial : nullptr;
-  a.group_parts = (group + plan->tile_heads - 1) / plan->tile_heads;
-  // a part of a listed tile: at least 128 tokens, 32 for each warp
-  a.max_cut = plan->num_blocks * c.page / 128;
-  if (a.max_cut < 1) a.max_cut = 1;
-  return launch_attention(c, b, a, reinterpret_cast<cudaStream_t>(stream));
+  return attention_run<CacheArgs>(plan, cache, batch, q, out, blocks, scale, counters,
+                                  counter_bytes, workspace, workspace_bytes, stream);
+}
+
+int exact_topk_cache4_attention_run(const exact_topk_attention_plan* plan,
+                                    const exact_topk_cache4* cache, const exact_topk_batch* batch,
+                                    const exact_topk_rows* q, const exact_topk_rows* out,
+                                    const int32_t* blocks, float scale, void* counters,
+                                    size_t counter_bytes, void* workspace, size_t workspace_bytes,
+                                    struct CUstream_st* stream) {
+  return attention_run<Cache4Args>(plan, cache, batch, q, out, blocks, scale, counters,
+                                   counter_bytes, workspace, workspace_bytes, stream);
 }
 
 int exact_topk_set_wait_limit(int64_t polls) {

@@ -22,6 +22,22 @@ struct CacheArgs {
   int num_pages, heads, page, page_shift, dim, fp16;
 };
 
+// The 4-bit cache: k and v hold two codes a byte, k_scale and v_scale point to e4m3 scales of 16
+// channels each. (A type of its own: the 8-bit kernels' arguments stay as they are.)
+struct Cache4Args : CacheArgs {
+  float k_unit, v_unit;
+};
+
+// By the bits of a code.
+template <int kBits>
+struct CacheOf {
+  using Args = CacheArgs;
+};
+template <>
+struct CacheOf<4> {
+  using Args = Cache4Args;
+};
+
 struct BatchArgs {
   const int32_t* table;
   const int32_t* kv_len;
@@ -94,9 +110,16 @@ int launch_cache_write(const CacheArgs&, const BatchArgs&, const RowArgs& k, con
                        cudaStream_t);
 int launch_cache_read(const CacheArgs&, const BatchArgs&, const RowArgs& k, const RowArgs& v,
                       cudaStream_t);
+int launch_cache4_write(const Cache4Args&, const BatchArgs&, const RowArgs& k, const RowArgs& v,
+                        cudaStream_t);
+int launch_cache4_read(const Cache4Args&, const BatchArgs&, const RowArgs& k, const RowArgs& v,
+                       cudaStream_t);
 int launch_block_scores(const CacheArgs&, const BatchArgs&, const ScoreArgs&, cudaStream_t);
 int launch_prompt_attention(const CacheArgs&, const BatchArgs&, const AttentionArgs&,
                             cudaStream_t);
 int launch_attention(const CacheArgs&, const BatchArgs&, const AttentionArgs&, cudaStream_t);
+int launch_prompt_attention4(const Cache4Args&, const BatchArgs&, const AttentionArgs&,
+                             cudaStream_t);
+int launch_attention4(const Cache4Args&, const BatchArgs&, const AttentionArgs&, cudaStream_t);
 
 }  // namespace etk

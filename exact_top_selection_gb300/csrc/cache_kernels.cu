@@ -18,29 +18,6 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 
-// The part of a page that a slot's sequence reaches with its rows.
-struct PagePart {
-  SeqRows rows;
-  int seq, block, first, end;  // offsets [first, end) of page `block` of the sequence
-  int index;                   // 0: the sequence's first part
-};
-
-// False where the slot has no part (first == end may still hold for index 0).
-__device__ __forceinline__ bool page_part(const BatchArgs& b, int page_shift, int64_t slot,
-                                          PagePart* part) {
-  const int P = 1 << page_shift;
-  part->seq = sequence_of_slot(b, slot, P, 2);
-  part->rows = sequence_rows(b, page_shift, part->seq);
-  part->index = (int)(slot - first_slot(b, part->seq, P, 2));
-  const int begin = part->rows.pos0 > 0 ? part->rows.pos0 : 0;
-  part->block = (begin >> page_shift) + part->index;
-  const int64_t base = (int64_t)part->block << page_shift;
-  const int64_t left = (int64_t)part->rows.len - base;
-  part->first = part->index == 0 ? begin & (P - 1) : 0;
-  part->end = left < P ? (int)left : P;
-  return part->index >= 0 && part->rows.count > 0 && part->end > part->first;
-}
-
 // 2^e with the smallest e in range for which amax <= 448 * 2^e.  448 = 1.75 * 2^8,
 // so a magnitude 1.m * 2^x needs e = x - 8, one more where 1.m > 1.75.
 __device__ __forceinline__ float scale_for(float amax) {
@@ -66,55 +43,6 @@ __device__ __forceinline__ uint2 encode8(const uint4& x, float by) {
   return make_uint2(
       encode2<kSpecial>(a.x * by, a.y * by) | encode2<kSpecial>(b.x * by, b.y * by) << 16,
       encode2<kSpecial>(c.x * by, c.y * by) | encode2<kSpecial>(d.x * by, d.y * by) << 16);
-}
-
-__device__ __forceinline__ float finite_magnitude(float x) {
-  const float a = fabsf(x);
-  return a < __uint_as_float(0x7F800000u) ? a : 0.f;
-}
-
-// Pairs of the rows' type.
-template <bool kFp16>
-__device__ __forceinline__ uint32_t larger2(uint32_t x, uint32_t y) {
-  if (kFp16) {
-    const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&x),
-                                   *reinterpret_cast<__nv_bfloat162*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-template <bool kFp16>
-__device__ __forceinline__ uint32_t smaller2(uint32_t x, uint32_t y) {
-  if (kFp16) {
-    const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&x),
-                                   *reinterpret_cast<__nv_bfloat162*>(&y));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// Bit patterns: the type's infinity, in both halves.
-template <bool kFp16>
-constexpr uint32_t infinities() {
-  return kFp16 ? 0x7C007C00u : 0x7F807F80u;
-}
-
-// NaN as 0 and infinities as the type's largest number, in both halves.
-template <bool kFp16>
-__device__ __forceinline__ uint32_t finite2(uint32_t w) {
-  uint32_t r = 0u;
-#pragma unroll
-  for (int s = 0; s < 32; s += 16) {
-    uint32_t x = w >> s & 0xFFFFu;
-    const uint32_t a = x & 0x7FFFu, inf = infinities<kFp16>() & 0xFFFFu;
-    if (a == inf) x -= 1u;  // the pattern before infinity
-    if (a > inf) x = 0u;
-    r |= x << s;
-  }
-  return r;
 }
 
 // One pass over the rows: a page's part is held in registers (8 channels a thread

@@ -137,9 +137,11 @@ struct Shared {
 // kPartShift: log2 of the parts of a block (1 of pages of 64 and 128 tokens, 2 of 32, 4 of 16).
 // wait_limit stands apart from the other arguments: one field more among them cost 4% of the sparse
 // chunk's time by the order that instructions then came in.
-template <int D, int kPartShift>
+// kBits: of a code.
+template <int D, int kPartShift, int kBits>
 __global__ void __launch_bounds__(kThreads, 2)
-    prompt_attention_kernel(CacheArgs c, BatchArgs b, AttentionArgs a, uint32_t wait_limit) {
+    prompt_attention_kernel(typename CacheOf<kBits>::Args c, BatchArgs b, AttentionArgs a,
+                            uint32_t wait_limit) {
   using Smem = Shared<D>;
   constexpr int kLines = D / 64;
   // tensor memory: O, then two blocks' S, each of which its P replaces
@@ -368,6 +370,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const int64_t tile = (int64_t)page * c.heads + head;
       e.offset = ((tile << c.page_shift) + (e.pos & (c.page - 1))) * D;
+      if constexpr (kBits == 4) {  // scales are part of the operands, and the unit of the outputs
+        e.k_scale = e.v_part = 1.f;
+        continue;
+      }
       e.k_scale = __ldg(c.k_scale + tile);
       const uint32_t v = __float_as_uint(__ldg(c.v_scale + tile));
       e.v_part = __uint_as_float((v & 0x7FFFFFu) | 127u << 23);
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0 && high > unit_before) atomicMax(&sm.unit, high);
     __syncthreads();
     const int unit = sm.unit;
-    for (int i = tid; i < entries; i += kThreads) {
+    for (int i = tid; kBits == 8 && i < entries; i += kThreads) {
       Entry& e = sm.entry[i];
       if (e.offset < 0) continue;
       const int below = unit - (int)e.v_power;
@@ -514,23 +520,32 @@ __global__ void __launch_bounds__(kThreads, 2)
       // channels. Of a token's line they write every other piece of 16 bytes, of an odd token's
       // the other ones, so that a quarter of a warp touches every bank once.
       const int first = (warp - kRows / 32) * 16 + (lane >> 2), chunk = lane & 3;
-      uint4 k[2][kLines], v[2][kLines];  // tokens first, first + 8
+      // tokens first, first + 8; 4-bit codes with their scale in the third word
+      uint4 k[2][kLines], v[2][kLines];
       const auto entry_of = [&](int block, int i) -> const Entry& {
         return sm.entry[(block << per_block_shift) + ((first + i * 8) >> part_tokens_shift)];
       };
       // Loads without branches, so that nothing waits for them: of an absent part they take the
       // cache's first page, behind the last block its last one, behind the sequence's end what
       // the page holds. `clear` puts zeros for the first and the last.
-      const auto load = [&](int block, const uint8_t* codes, uint4 (&x)[2][kLines]) {
+      const auto load = [&](int block, const uint8_t* codes, const float* scales,
+                            uint4 (&x)[2][kLines]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const Entry& e = entry_of(block < blocks ? block : blocks - 1, i);
           const int in_part = (first + i * 8) & ((1 << part_tokens_shift) - 1);
-          const uint8_t* const at =
-              codes + (e.offset < 0 ? 0 : e.offset) + in_part * D + chunk * 16;
+          const int64_t at = (e.offset < 0 ? 0 : e.offset) + in_part * D + chunk * 16;
 #pragma unroll
-          for (int line = 0; line < kLines; ++line)
-            x[i][line] = __ldg(reinterpret_cast<const uint4*>(at + line * 64));
+          for (int line = 0; line < kLines; ++line) {
+            if constexpr (kBits == 8) {
+              x[i][line] = __ldg(reinterpret_cast<const uint4*>(codes + at + line * 64));
+            } else {
+              const int64_t group = at / 16 + line * 4;
+              const uint2 both = __ldg(reinterpret_cast<const uint2*>(codes + group * 8));
+              x[i][line] = make_uint4(
+                  both.x, both.y, __ldg(reinterpret_cast<const uint8_t*>(scales) + group), 0u);
+            }
+          }
         }
       };
       const auto there = [&](int block, int i) {
@@ -553,14 +568,23 @@ __global__ void __launch_bounds__(kThreads, 2)
                              const uint4 (&x)[kLines], uint32_t power) {
 #pragma unroll
         for (int line = 0; line < kLines; ++line) {
-          const uint32_t w[4] = {x[line].x, x[line].y, x[line].z, x[line].w};
           uint32_t y[8];
+          if constexpr (kBits == 4) {
+            uint32_t z[2][4];
+            codes4_to_half2(x[line].x, z[0]);
+            codes4_to_half2(x[line].y, z[1]);
+            const uint32_t by = scale_to_half2(x[line].z);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            y[2 * n] = codes_to_half2((uint16_t)w[n]);
-            y[2 * n + 1] = codes_to_half2((uint16_t)(w[n] >> 16));
+            for (int n = 0; n < 8; ++n) y[n] = times2(z[n >> 2][n & 3], by);
+          } else {
+            const uint32_t w[4] = {x[line].x, x[line].y, x[line].z, x[line].w};
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+              y[2 * n] = codes_to_half2((uint16_t)w[n]);
+              y[2 * n + 1] = codes_to_half2((uint16_t)(w[n] >> 16));
+            }
           }
-          if (power != 0x3C003C00u) {
+          if (kBits == 8 && power != 0x3C003C00u) {
             const __half2 by = *reinterpret_cast<const __half2*>(&power);
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
@@ -583,10 +607,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int i = 0; i < 2; ++i) place(sm.k[buffer], i, k[i], 0x3C003C00u);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         barrier_arrive(&sm.k_full[buffer]);
-        load(block + 1, c.k, k);
+        load(block + 1, c.k, c.k_scale, k);
       };
-      load(0, c.k, k);
-      load(0, c.v, v);
+      load(0, c.k, c.k_scale, k);
+      load(0, c.v, c.v_scale, v);
       keys(0);
       for (int block = 0; block < blocks; ++block) {
         // keys are a block ahead: their place is free as soon as the scores are there, the
@@ -598,10 +622,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         clear(block, v);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          place(sm.v[buffer], i, v[i], entry_of(block, i).v_power);
+          place(sm.v[buffer], i, v[i], kBits == 8 ? entry_of(block, i).v_power : 0u);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         barrier_arrive(&sm.v_full[buffer]);
-        load(block + 1, c.v, v);
+        load(block + 1, c.v, c.v_scale, v);
       }
     } else {
       // ---- products ----
@@ -668,7 +692,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       ok = __all_sync(~0u, ok);
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     }
-    const float by = l == 0.f ? 0.f : exp2f((float)(done > 0 ? sm.unit : 0)) / l;
+    float by = l == 0.f ? 0.f : 1.f / l;
+    if constexpr (kBits == 4)
+      by *= c.v_unit;
+    else
+      by = l == 0.f ? 0.f : exp2f((float)(done > 0 ? sm.unit : 0)) / l;
     uint16_t* const at =
         static_cast<uint16_t*>(a.out.data) + (row0 + row_token) * a.out.token_stride +
         ((int64_t)head * a.group + head0 + row - row_token * heads) * a.out.head_stride;
@@ -718,13 +746,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                  : "memory");
 }
 
-template <int D, int kPartShift>
-int launch(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a, cudaStream_t stream) {
+template <int D, int kPartShift, int kBits>
+int launch(const typename CacheOf<kBits>::Args& c, const BatchArgs& b, const AttentionArgs& a,
+           cudaStream_t stream) {
   constexpr size_t most = sizeof(Shared<D>) + 1024 + (size_t)kPromptListedWidth * 4;
   static_assert(most <= kMostShared, "every call that the checks let through");
   const size_t smem =
       sizeof(Shared<D>) + 1024 + (a.blocks != nullptr ? (size_t)b.width * 4 : 0);
-  const auto kernel = prompt_attention_kernel<D, kPartShift>;
+  const auto kernel = prompt_attention_kernel<D, kPartShift, kBits>;
   // the largest call's size: the limit is the kernel's, whichever thread launches it
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) !=
       cudaSuccess) {
@@ -737,19 +766,26 @@ int launch(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a, cudaS
   return launch_status();
 }
 
-template <int D>
-int launch_parts(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a,
-                 cudaStream_t stream) {
-  if (c.page == 16) return launch<D, 2>(c, b, a, stream);
-  if (c.page == 32) return launch<D, 1>(c, b, a, stream);
-  return launch<D, 0>(c, b, a, stream);
+template <int D, int kBits>
+int launch_parts(const typename CacheOf<kBits>::Args& c, const BatchArgs& b,
+                 const AttentionArgs& a, cudaStream_t stream) {
+  if (c.page == 16) return launch<D, 2, kBits>(c, b, a, stream);
+  if (c.page == 32) return launch<D, 1, kBits>(c, b, a, stream);
+  return launch<D, 0, kBits>(c, b, a, stream);
 }
 
 }  // namespace
 
 int launch_prompt_attention(const CacheArgs& c, const BatchArgs& b, const AttentionArgs& a,
                             cudaStream_t stream) {
-  return c.dim == 128 ? launch_parts<128>(c, b, a, stream) : launch_parts<64>(c, b, a, stream);
+  return c.dim == 128 ? launch_parts<128, 8>(c, b, a, stream)
+                      : launch_parts<64, 8>(c, b, a, stream);
+}
+
+int launch_prompt_attention4(const Cache4Args& c, const BatchArgs& b, const AttentionArgs& a,
+                             cudaStream_t stream) {
+  return c.dim == 128 ? launch_parts<128, 4>(c, b, a, stream)
+                      : launch_parts<64, 4>(c, b, a, stream);
 }
 
 }  // namespace etk

@@ -11,6 +11,13 @@
  *   exact_topk_attention_run   queries x cache (all pages, or the pages listed
  *                              for each token and key head) -> outputs
  *
+ * The same four over a cache held in 4 bits (exact_topk_cache4_*), and what comes
+ * before them in a step:
+ *
+ *   exact_topk_update_tables   sequences grow and shrink: lengths, row ranges,
+ *                              pages from a ring of free ones and back to it
+ *   exact_topk_rotary          queries and keys turned by their positions
+ *
  * Conventions are those of exact_topk.h: every entry point returns 0 or a
  * negative exact_topk_status and launches nothing on error, allocates nothing,
  * never synchronizes, enqueues on the given stream only and can be captured in
@@ -195,6 +202,149 @@ int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_
                              const exact_topk_rows* out, const int32_t* blocks, float scale,
                              void* counters, size_t counter_bytes, void* workspace,
                              size_t workspace_bytes, struct CUstream_st* stream);
+
+/* A paged cache in 4 bits. 16 neighbouring channels of one token and head share a
+ * scale: a stored number is code * scale * unit, exact in FP16 but for the unit (code *
+ * scale has at most 6 significant bits and lies between 2^-10 and 2688).
+ *   k, v        device e2m1 codes [num_pages][kv_heads][page_size][head_dim / 2], two a byte,
+ *               the channel of even number in the lower four bits; 16-byte aligned
+ *   k_scale, v_scale  device e4m3 scales [num_pages][kv_heads][page_size][head_dim / 16], not
+ *               negative; 16-byte aligned
+ *   key_bounds  as of exact_topk_cache
+ *   k_unit, v_unit  powers of two between 2^EXACT_TOPK_SCALE_MIN_EXP and
+ *               2^EXACT_TOPK_SCALE_MAX_EXP. Groups whose largest magnitude lies between 0.1 and
+ *               2688 units keep the codes' precision; smaller ones lose it, larger ones saturate.
+ *   the rest as of exact_topk_cache */
+typedef struct exact_topk_cache4 {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  void* key_bounds;
+  int32_t num_pages;
+  int32_t kv_heads;
+  int32_t page_size;
+  int32_t head_dim;
+  int32_t type;
+  float k_unit;
+  float v_unit;
+} exact_topk_cache4;
+
+/* As exact_topk_cache_write. Each group of 16 channels is quantised by itself: its scale
+ * is the e4m3 number nearest to max |x| / (6 unit), at least 2^-9 and at most 448, its codes
+ * the e2m1 numbers nearest to x / (scale * unit), both to nearest even, saturating. A group
+ * with an infinity or a NaN gets the scale NaN: all 16 numbers are NaN. Nothing of earlier tokens
+ * changes but their page's bounds. Errors: as exact_topk_cache_write. */
+int exact_topk_cache4_write(const exact_topk_cache4* cache, const exact_topk_batch* batch,
+                            int64_t num_tokens, const exact_topk_rows* k,
+                            const exact_topk_rows* v, struct CUstream_st* stream);
+
+/* As exact_topk_cache_read: code * scale * unit, rounded to the cache's type. */
+int exact_topk_cache4_read(const exact_topk_cache4* cache, const exact_topk_batch* batch,
+                           int64_t num_tokens, const exact_topk_rows* k, const exact_topk_rows* v,
+                           struct CUstream_st* stream);
+
+/* As exact_topk_block_scores. A stored key is off by up to a third of its group's largest
+ * magnitude over 2, and may lie beyond the bounds, which are of the keys as they were written. */
+int exact_topk_cache4_block_scores(const exact_topk_cache4* cache, const exact_topk_batch* batch,
+                                   int64_t num_tokens, int q_heads, const exact_topk_rows* q,
+                                   int keep_first, int keep_last, float* scores,
+                                   int64_t row_pitch, int32_t* ke, int32_t* num_valid_rows,
+                                   struct CUstream_st* stream);
+
+/* As exact_topk_attention_run, with the same plan. scale * k_unit must be finite as scale must. */
+int exact_topk_cache4_attention_run(const exact_topk_attention_plan* plan,
+                                    const exact_topk_cache4* cache, const exact_topk_batch* batch,
+                                    const exact_topk_rows* q, const exact_topk_rows* out,
+                                    const int32_t* blocks, float scale, void* counters,
+                                    size_t counter_bytes, void* workspace, size_t workspace_bytes,
+                                    struct CUstream_st* stream);
+
+#define EXACT_TOPK_MAX_ROTARY_DIM 512
+
+/* Rotary positions. Of each head's head_dim channels the first rotary_dim turn, in pairs
+ * (i, i + rotary_dim / 2), or (2 i, 2 i + 1) where neighbours is nonzero; pair i at position
+ * p by p * turns[i] / 2^64 turns, modulo one (exact for every position), times amplitude.
+ *   turns       device [rotary_dim / 2]
+ *   head_dim    a multiple of 8 up to 1024;  rotary_dim even, 2 to head_dim and at most 512
+ *   type        of all rows */
+typedef struct exact_topk_rotary_spec {
+  const uint64_t* turns;
+  float amplitude;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t neighbours;
+  int32_t type;
+} exact_topk_rotary_spec;
+
+/* Turns q [num_tokens][q_heads][head_dim] into q_out and k [num_tokens][k_heads][head_dim] into
+ * k_out; cosines, sines and sums are FP32, rounded once. Each may be its own output (the same data
+ * and strides), in no other way may they overlap. k_heads may be 0 (k and k_out are ignored).
+ *   batch       the rows' positions are those of their tokens (the page table is not looked at);
+ *               rows of no sequence or without a token are left as they were
+ *   positions   device int32 [num_tokens] instead of the batch (one of the two is NULL): any
+ *               numbers, negative ones turn back
+ *   inverse     nonzero: by the negative angles. That is the gradient of q and k by what comes
+ *               back for q_out and k_out.
+ * Errors: NULL_POINTER, BAD_BATCH, BAD_HEADS, BAD_SHAPE (the spec, the amplitude not finite),
+ * MISALIGNED, CUDA. */
+int exact_topk_rotary(const exact_topk_rotary_spec* spec, const exact_topk_batch* batch,
+                      const int32_t* positions, int64_t num_tokens, int q_heads,
+                      const exact_topk_rows* q, const exact_topk_rows* q_out, int k_heads,
+                      const exact_topk_rows* k, const exact_topk_rows* k_out, int inverse,
+                      struct CUstream_st* stream);
+
+/* Sequences on the GPU: their page tables, lengths and row ranges (an exact_topk_batch is made
+ * of them), and the pages that no sequence has.
+ *   page_table  device int32 [num_seqs][table_pitch]; entries behind a sequence's pages are not looked at
+ *   kv_len      device int32 [num_seqs]
+ *   q_start     device int32 [num_seqs + 1], written
+ *   applied     device int32 [num_seqs], written; may be NULL
+ *   slots, positions  device int32 [max_tokens], written; may be NULL
+ *   free_pages  device int32 [num_pages], a ring of page ids
+ *   free_range  device int32 [2]: the first free page's place in the ring, and how many there are
+ *   workspace   device, >= exact_topk_tables_workspace bytes, 4-byte aligned, contents ignored
+ * num_pages * page_size must be below 2^31. A page's id stands once: in the ring or in a table. */
+typedef struct exact_topk_page_tables {
+  int32_t* page_table;
+  int32_t* kv_len;
+  int32_t* q_start;
+  int32_t* applied;
+  int32_t* slots;
+  int32_t* positions;
+  int32_t* free_pages;
+  int32_t* free_range;
+  void* workspace;
+  size_t workspace_bytes;
+  int64_t table_pitch;
+  int64_t max_tokens;
+  int32_t num_seqs;
+  int32_t table_width;
+  int32_t num_pages;
+  int32_t page_size;
+} exact_topk_page_tables;
+
+/* Bytes of workspace for num_seqs sequences. Errors: NULL_POINTER, BAD_BATCH. */
+int exact_topk_tables_workspace(int num_seqs, size_t* bytes);
+
+/* Sequence b grows by change[b] tokens (negative: loses its last -change[b], all it has where it
+ * has fewer; with negate nonzero by -change[b]). Pages that are no longer reached go to the end of
+ * the ring, in the sequences' order and each sequence's in ascending place; pages for new tokens
+ * are taken from the front, in the same order, those given back in this call last. A sequence
+ * gets all its tokens or none:
+ * none where they do not fit its table, where it needs pages and they and those asked for
+ * by the sequences before it are more than there are, or where its tokens and those asked for
+ * before it are more than max_tokens. (What a refused sequence asked for counts for those
+ * behind it; one that does not fit its table asks for nothing.)
+ *   kv_len, free_pages, free_range, and the tables' new entries: as they are after the call
+ *   q_start     ranges of the new tokens' rows, in the sequences' order
+ *   applied     the change that was made, 0 for a refused sequence; may be `change` itself
+ *   slots, positions  of each new row: page * page_size + offset, and its place in the
+ *               sequence; rows behind the last are left as they were
+ * change is device int32 [num_seqs]. Results do not depend on the order in which CTAs run.
+ * Errors: NULL_POINTER, BAD_CACHE (pages), BAD_BATCH, WORKSPACE_TOO_SMALL, MISALIGNED, CUDA. */
+int exact_topk_update_tables(const exact_topk_page_tables* tables, const int32_t* change,
+                             int negate, struct CUstream_st* stream);
 
 /* How many times the issuing threads of the prompts' kernels (page scores and attention) poll for
  * their operands before they give up, for the calls that this process makes from now on: at most
