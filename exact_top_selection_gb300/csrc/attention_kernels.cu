@@ -640,27 +640,37 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
                 copy16(to + kTokens * D + line * 128 + pv * 16, c.v + at + j * 512, there);
               }
             } else {
-              // A line of 128 bytes is 2 tokens of 128 channels or 4 of 64.
-              const int64_t at = (offset + row * D) / 2 + lane * 16;
-#pragma unroll
-              for (int j = 0; j < kTokens * D / 1024; ++j) {
-                const int piece = lane + 32 * j, line = piece >> 3, p = piece & 7;
-                const bool there = (D == 128 ? piece >> 2 : piece >> 1) < rows;
-                const int pv = p ^ ((line & (D == 128 ? 3 : 1)) << 1);
-                copy16(to + line * 128 + p * 16, c.k + at + j * 512, there);
-                copy16(to + Smem::kCodes + line * 128 + pv * 16, c.v + at + j * 512, there);
-              }
-              // A piece of scales is 2 (4) tokens, zeros behind the last that anyone sees.
+              // A line of 128 bytes is 2 tokens of 128 channels or 4 of 64; a piece of scales is 2
+              // (4) tokens. Zeros behind the last token that anyone sees.
               constexpr int kPieces = Smem::kScales / 16, kBytes = D / 16;
               static_assert(kPieces * 2 <= 32, "a piece a lane");
-              if (lane < 2 * kPieces) {
-                const int piece = lane % kPieces;
-                const int bytes = (rows - piece * (16 / kBytes)) * kBytes;
-                const uint8_t* const scales =
-                    reinterpret_cast<const uint8_t*>(lane < kPieces ? c.k_scale : c.v_scale);
-                copy16(to + 2 * Smem::kCodes + lane * 16,
-                       scales + (offset + row * D) / 16 + piece * 16,
-                       bytes < 0 ? 0 : (bytes < 16 ? bytes : 16));
+              const int64_t first = offset + row * D;
+              const uint8_t* const ks = c.k + first / 2 + lane * 16;
+              const uint8_t* const vs = c.v + first / 2 + lane * 16;
+              const uint8_t* const scales =
+                  reinterpret_cast<const uint8_t*>(lane < kPieces ? c.k_scale : c.v_scale) +
+                  first / 16 + (lane % kPieces) * 16;
+              const uint32_t k_to = to + lane * 16;
+              const uint32_t v_to =
+                  to + Smem::kCodes + ((lane ^ ((lane >> 3 & (D == 128 ? 3 : 1)) << 1)) * 16);
+              if (rows >= kTokens) {
+#pragma unroll
+                for (int j = 0; j < kTokens * D / 1024; ++j) {
+                  copy16(k_to + j * 512, ks + j * 512, 16);
+                  copy16(v_to + j * 512, vs + j * 512, 16);
+                }
+                if (lane < 2 * kPieces) copy16(k_to + 2 * Smem::kCodes, scales, 16);
+              } else {
+#pragma unroll
+                for (int j = 0; j < kTokens * D / 1024; ++j) {
+                  const bool there = (lane + 32 * j) / (D / 32) < rows;
+                  copy16(k_to + j * 512, ks + j * 512, there);
+                  copy16(v_to + j * 512, vs + j * 512, there);
+                }
+                const int bytes = (rows - lane % kPieces * (16 / kBytes)) * kBytes;
+                if (lane < 2 * kPieces)
+                  copy16(k_to + 2 * Smem::kCodes, scales,
+                         bytes < 0 ? 0 : (bytes < 16 ? bytes : 16));
               }
             }
           }
@@ -752,6 +762,24 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (!takes[n]) continue;
+            if constexpr (kBits == 4 && ST > 1) {  // the chains of ST blocks overlap
+              float(&sum)[4] = reinterpret_cast<float(&)[4]>(x[n][st * 4]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) sum[r] = 0.f;
+#pragma unroll
+              for (int p = 0; p < kHalf; ++p)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint4 q = kHoldQ ? held[n][p][k]
+                                         : *reinterpret_cast<const uint4*>(
+                                               &sm.q[n * 8 + g][p * 64 + q4 * 16 + k * 8]);
+                  const uint32_t(&f0)[4] = f[p * 4 + k * 2];
+                  const uint32_t(&f1)[4] = f[p * 4 + k * 2 + 1];
+                  mma(sum, f0[0], f0[1], f0[2], f0[3], q.x, q.y);
+                  mma(sum, f1[0], f1[1], f1[2], f1[3], q.z, q.w);
+                }
+              continue;
+            }
             // two sums, for shorter chains
             float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -798,8 +826,12 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
           float high = -infinity();
 #pragma unroll
           for (int r = 0; r < 4 * ST; ++r) {
-            x[n][r] *= r & 1 ? fy : fx;
-            y[r] = x[n][r] - m[n][r & 1];
+            if constexpr (kBits == 4) {
+              y[r] = fmaf(x[n][r], r & 1 ? fy : fx, -m[n][r & 1]);
+            } else {
+              x[n][r] *= r & 1 ? fy : fx;
+              y[r] = x[n][r] - m[n][r & 1];
+            }
           }
           if (masked) {
 #pragma unroll
@@ -815,6 +847,11 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
 #pragma unroll
           for (int r = 0; r < 4 * ST; ++r) high = fmaxf(high, y[r]);
           if (__any_sync(~0u, high > kMost)) {
+            if constexpr (kBits == 4) {  // the scores themselves are needed here alone
+#pragma unroll
+              for (int r = 0; r < 4 * ST; ++r)
+                if (x[n][r] != -infinity()) x[n][r] *= r & 1 ? fy : fx;
+            }
             float by[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -1024,9 +1061,14 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
         for (int step = 0; step < per_page; ++step) {
           copy_wait<Smem::kRing - 2>();
           __syncwarp();
-          compute(e, step, now);
-          __syncwarp();
-          fetch(behind);
+          if constexpr (kBits == 4) {  // short rings: the next step is on its way at once
+            fetch(behind);
+            compute(e, step, now);
+          } else {
+            compute(e, step, now);
+            __syncwarp();
+            fetch(behind);
+          }
           behind = now;
           now = now + 1 == Smem::kRing ? 0 : now + 1;
         }
@@ -1184,7 +1226,10 @@ int launch_columns(const typename CacheOf<kBits>::Args& c, const BatchArgs& b,
 template <int kBits>
 int launch_bits(const typename CacheOf<kBits>::Args& c, const BatchArgs& b, const AttentionArgs& a,
                 cudaStream_t stream) {
-  if (c.dim == 128) return launch_columns<128, 1, kBits>(c, b, a, stream);
+  if (c.dim == 128) {
+    if (kBits == 4 && c.page > 16) return launch_columns<128, 2, kBits>(c, b, a, stream);
+    return launch_columns<128, 1, kBits>(c, b, a, stream);
+  }
   // Steps of 2 KB of keys and of values (in 8 bits). Pages of 16 tokens have half of that.
   if (c.page == 16) return launch_columns<64, 1, kBits>(c, b, a, stream);
   return launch_columns<64, 2, kBits>(c, b, a, stream);
