@@ -62,6 +62,10 @@ def _lib():
 
 def _apart(a, b, name):
     """Rows a and b share no memory. Both may be slices of one wider tensor of tokens."""
+    if a.is_contiguous() and b.is_contiguous():
+        a0, b0 = a.data_ptr(), b.data_ptr()
+        if a0 >= b0 + b.nbytes or b0 >= a0 + a.nbytes:
+            return
     (a0, a1), (b0, b1) = _cache._span(a), _cache._span(b)
     if a0 >= b1 or b0 >= a1 or a.numel() == 0 or b.numel() == 0:
         return
@@ -77,6 +81,21 @@ def _apart(a, b, name):
             if at >= a.shape[2] * size and at + b.shape[2] * size <= head:
                 return
     raise ValueError(f"{name} must not share memory with another row argument")
+
+
+def _rows_like(t, name, like, x, xr):
+    """As _cache._rows, of an output with the shape of the rows x that are described already."""
+    if t.shape == x.shape and t.dtype is x.dtype and t.device == x.device and t.is_contiguous():
+        return _cache._Rows(t.data_ptr(), x.shape[1] * x.shape[2], x.shape[2])
+    return _cache._rows(t, name, like, x.shape[1], x.shape[0])
+
+
+def _check_places(x, xr, y, yr):
+    """Outputs y are the rows x themselves, or apart from them; no two of their rows overlap."""
+    if not y.is_contiguous():
+        _cache._written(y, "out", y[:0])
+    if xr.data != yr.data or xr.token_stride != yr.token_stride or xr.head_stride != yr.head_stride:
+        _apart(y, x, "out")
 
 
 class Rotary:
@@ -174,21 +193,16 @@ class Rotary:
             ko = _cache._rows(k_out, "out", like, k_heads, T) if pair else None
         else:
             q_out, k_out = out if pair else (out, None)
-            qo = _cache._rows(q_out, "out" if not pair else "out[0]", like, heads, T)
-            inputs = [(q, qr, q_out, qo)]
+            qo = _rows_like(q_out, "out" if not pair else "out[0]", like, q, qr)
+            ko = _rows_like(k_out, "out[1]", like, k, kr) if pair else None
+            _check_places(q, qr, q_out, qo)
             if pair:
-                ko = _cache._rows(k_out, "out[1]", like, k_heads, T)
-                inputs.append((k, kr, k_out, ko))
+                _check_places(k, kr, k_out, ko)
                 _apart(q_out, k_out, "out[0]")
-                _apart(q_out, k, "out[0]")
-                _apart(k_out, q, "out[1]")
-            for x, xr, y, yr in inputs:
-                if (xr.data, xr.token_stride, xr.head_stride) == (yr.data, yr.token_stride, yr.head_stride):
-                    if not y.is_contiguous():
-                        _cache._written(y, "out", y[:0])
-                else:
-                    _cache._written(y, "out", y[:0])
-                    _apart(y, x, "out")
+                if ko.data != kr.data:  # in place, k is what the line above looked at
+                    _apart(q_out, k, "out[0]")
+                if qo.data != qr.data:
+                    _apart(k_out, q, "out[1]")
         _cache._call(self, stream, _lib().exact_topk_rotary, ctypes.byref(spec), None if batch is None else batch._ref,
                      None if positions is None else positions.data_ptr(), T, heads, qr, qo, k_heads if pair else 0,
                      kr if pair else None, ko if pair else None, int(bool(inverse)))

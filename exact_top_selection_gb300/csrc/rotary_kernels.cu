@@ -75,10 +75,13 @@ __device__ __forceinline__ bool position_of(const RotaryArgs& a, const BatchArgs
   return *position >= 0;
 }
 
-// V pairs a thread: V channels and the V of their partners.
+// A thread has 2 V channels of a row at a time: V pairs, or, behind the channels that turn, 2 V
+// neighbours that are copied. It keeps to its place in the rows and goes from row to row; `lanes`,
+// a power of two, are as many threads as stand on a row.
 template <bool kFp16, int V, bool kNeighbours>
 __global__ void __launch_bounds__(kThreads)
-    rotary_kernel(RotaryArgs a, BatchArgs b, int tokens_of_cta) {
+    rotary_kernel(RotaryArgs a, BatchArgs b, int tokens_of_cta, int lane_shift) {
+  constexpr int kTwo = V > 1 ? 2 : 1;
   __shared__ __align__(16) float2 turn[kMostTokens * kMostPairs];  // cosine and sine, see below
   __shared__ int position[kMostTokens];
   __shared__ int there[kMostTokens];
@@ -86,14 +89,64 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t token0 = (int64_t)blockIdx.x * tokens_of_cta;
   const int64_t left = a.num_tokens - token0;
   const int tokens = left < tokens_of_cta ? (int)left : tokens_of_cta;
+  const int turning = a.pairs / V;  // parts of a row that turn
+  const int parts = turning + (a.copy_q || a.copy_k ? (a.dim - 2 * a.pairs + 2 * V - 1) / (2 * V) : 0);
+  const int heads = a.q_heads + a.k_heads;
+  // heads are spread over blockIdx.y where there are few tokens
+  const int mine = (heads - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
+  const int rows = tokens * mine, row0 = tid >> lane_shift, row_step = kThreads >> lane_shift;
+  const int lane = tid & ((1 << lane_shift) - 1);
+
+  struct Item {
+    const uint16_t* from;
+    uint16_t* to;
+    int token;
+    bool copied;  // its rows go elsewhere
+  };
+  const auto item = [&](int row) {
+    const int t = (row >= mine) + (row >= 2 * mine) + (row >= 3 * mine);
+    const int head = (row - t * mine) * (int)gridDim.y + (int)blockIdx.y;
+    const bool query = head < a.q_heads;
+    const RowArgs& in = query ? a.q : a.k;
+    const RowArgs& out = query ? a.q_out : a.k_out;
+    const int64_t h = query ? head : head - a.q_heads, token = token0 + t;
+    return Item{
+        static_cast<const uint16_t*>(in.data) + token * in.token_stride + h * in.head_stride,
+        static_cast<uint16_t*>(out.data) + token * out.token_stride + h * out.head_stride, t,
+        (query ? a.copy_q : a.copy_k) != 0};
+  };
+  // First channels of a part's two halves; the second one may lie behind the head's last channel.
+  const auto first_of = [&](int part) {
+    return part < turning ? (kNeighbours ? part * 2 * V : part * V)
+                          : 2 * a.pairs + (part - turning) * 2 * V;
+  };
+  const auto second_of = [&](int part) {
+    return part < turning && !kNeighbours ? part * V + a.pairs : first_of(part) + V;
+  };
+  const auto read = [&](const Item& i, int part, Part<V>* x, Part<V>* y) {
+    *x = load<V>(i.from + first_of(part));
+    const int second = second_of(part);
+    *y = load<V>(i.from + (second < a.dim ? second : first_of(part)));
+  };
+
+  // the first rows are on their way while the angles are worked out
+  Part<V> x[kBatch], y[kBatch];
+  const auto read_batch = [&](int from, int part) {
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      const int row = from + n * row_step;
+      read(item(row < rows ? row : rows - 1), part, &x[n], &y[n]);
+    }
+  };
+  if (lane < parts) read_batch(row0, lane);
+
   if (tid < tokens) {
     int p = 0;
     there[tid] = position_of(a, b, token0 + tid, &p);
     position[tid] = p;
   }
   __syncthreads();
-  const int parts = a.pairs / V;  // threads of a row
-  // Pairs of one thread lie `parts` apart in shared memory, two at a time: a warp's reads touch
+  // Pairs of one thread lie `turning` apart in shared memory, two at a time: a warp's reads touch
   // each bank once.
   for (int i = tid; i < tokens * a.pairs; i += kThreads) {
     const int t = i / a.pairs, pair = i - t * a.pairs;
@@ -101,106 +154,78 @@ __global__ void __launch_bounds__(kThreads)
     const uint64_t angle = a.turns[pair] * (a.inverse ? 0ull - p : p);
     float sine, cosine;
     sincospif(__ll2float_rn((int64_t)angle) * 0x1p-63f, &sine, &cosine);
-    constexpr int kTwo = V > 1 ? 2 : 1;
     const int part = pair / V, in = pair % V;
-    turn[t * a.pairs + (in / kTwo * parts + part) * kTwo + in % kTwo] =
+    turn[t * a.pairs + (in / kTwo * turning + part) * kTwo + in % kTwo] =
         make_float2(cosine * a.amplitude, sine * a.amplitude);
   }
   __syncthreads();
 
-  const int heads = a.q_heads + a.k_heads;
-  // heads are spread over blockIdx.y where there are few tokens
-  const int mine = (heads - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
-  const int items = tokens * mine * parts;
-  const auto place = [&](int item, const uint16_t** from, uint16_t** to, int* t, int* part) {
-    const int row = item / parts;
-    *part = item - row * parts;
-    *t = row / mine;
-    const int head = (row - *t * mine) * (int)gridDim.y + (int)blockIdx.y;
-    const bool query = head < a.q_heads;
-    const RowArgs& in = query ? a.q : a.k;
-    const RowArgs& out = query ? a.q_out : a.k_out;
-    const int64_t h = query ? head : head - a.q_heads;
-    const int64_t token = token0 + *t;
-    *from = static_cast<const uint16_t*>(in.data) + token * in.token_stride + h * in.head_stride;
-    *to = static_cast<uint16_t*>(out.data) + token * out.token_stride + h * out.head_stride;
-  };
-  for (int item0 = tid; item0 < items; item0 += kThreads * kBatch) {
-    Part<V> x[kBatch], y[kBatch];
-    uint16_t* to[kBatch];
-    int t[kBatch], part[kBatch];
+  for (int part = lane; part < parts; part += 1 << lane_shift) {
+    for (int from = row0; from < rows; from += row_step * kBatch) {
+      if (part != lane || from != row0) read_batch(from, part);
 #pragma unroll
-    for (int n = 0; n < kBatch; ++n) {
-      const int item = item0 + n * kThreads < items ? item0 + n * kThreads : item0;
-      const uint16_t* from;
-      place(item, &from, &to[n], &t[n], &part[n]);
-      const int first = kNeighbours ? part[n] * 2 * V : part[n] * V;
-      x[n] = load<V>(from + first);
-      y[n] = load<V>(from + first + (kNeighbours ? V : a.pairs));
-    }
+      for (int n = 0; n < kBatch; ++n) {
+        const int row = from + n * row_step;
+        if (row >= rows) break;
+        const Item i = item(row);
+        if (!there[i.token]) continue;
+        if (part < turning) {
+          float u[2 * V];  // x's numbers, then y's
 #pragma unroll
-    for (int n = 0; n < kBatch; ++n) {
-      if (item0 + n * kThreads >= items || !there[t[n]]) continue;
-      float u[2 * V];  // x's numbers, then y's
+          for (int k = 0; k < (V > 1 ? V / 2 : 1); ++k) {
+            const float2 f = unpack2<kFp16>(x[n].w[k]), g = unpack2<kFp16>(y[n].w[k]);
+            u[kTwo * k] = f.x;
+            u[V + kTwo * k] = g.x;
+            if (V > 1) {
+              u[kTwo * k + kTwo - 1] = f.y;
+              u[V + kTwo * k + kTwo - 1] = g.y;
+            }
+          }
+          const float2* const at = &turn[i.token * a.pairs + part * kTwo];
 #pragma unroll
-      for (int i = 0; i < (V > 1 ? V / 2 : 1); ++i) {
-        const float2 f = unpack2<kFp16>(x[n].w[i]), g = unpack2<kFp16>(y[n].w[i]);
-        u[2 * i] = f.x;
-        if (V > 1) u[2 * i + 1] = f.y;
-        u[V + 2 * i] = g.x;
-        if (V > 1) u[V + 2 * i + 1] = g.y;
-      }
-      float2 by_of[V];
-      if constexpr (V > 1) {
+          for (int k = 0; k < V; k += kTwo) {
+            float2 by[kTwo];
+            if constexpr (V > 1) {
+              const float4 two = *reinterpret_cast<const float4*>(at + k * turning);
+              by[0] = make_float2(two.x, two.y);
+              by[kTwo - 1] = make_float2(two.z, two.w);
+            } else {
+              by[0] = at[0];
+            }
 #pragma unroll
-        for (int i = 0; i < V; i += 2) {
-          const float4 two = *reinterpret_cast<const float4*>(
-              &turn[t[n] * a.pairs + (i / 2 * parts + part[n]) * 2]);
-          by_of[i] = make_float2(two.x, two.y);
-          by_of[i + 1] = make_float2(two.z, two.w);
+            for (int j = 0; j < kTwo; ++j) {
+              float& p = kNeighbours ? u[2 * (k + j)] : u[k + j];
+              float& q = kNeighbours ? u[2 * (k + j) + 1] : u[V + k + j];
+              const float p0 = p, q0 = q;
+              p = p0 * by[j].x - q0 * by[j].y;
+              q = q0 * by[j].x + p0 * by[j].y;
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < (V > 1 ? V / 2 : 1); ++k) {
+            x[n].w[k] = pack2<kFp16>(u[kTwo * k], V > 1 ? u[kTwo * k + kTwo - 1] : 0.f);
+            y[n].w[k] = pack2<kFp16>(u[V + kTwo * k], V > 1 ? u[V + kTwo * k + kTwo - 1] : 0.f);
+          }
+        } else if (!i.copied) {
+          continue;
         }
-      } else {
-        by_of[0] = turn[t[n] * a.pairs + part[n]];
+        store<V>(i.to + first_of(part), x[n]);
+        const int second = second_of(part);
+        if (second < a.dim) store<V>(i.to + second, y[n]);
       }
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float2 by = by_of[i];
-        float& p = kNeighbours ? u[2 * i] : u[i];
-        float& q = kNeighbours ? u[2 * i + 1] : u[V + i];
-        const float p0 = p, q0 = q;
-        p = p0 * by.x - q0 * by.y;
-        q = q0 * by.x + p0 * by.y;
-      }
-#pragma unroll
-      for (int i = 0; i < (V > 1 ? V / 2 : 1); ++i) {
-        x[n].w[i] = pack2<kFp16>(u[2 * i], V > 1 ? u[2 * i + 1] : 0.f);
-        y[n].w[i] = pack2<kFp16>(u[V + 2 * i], V > 1 ? u[V + 2 * i + 1] : 0.f);
-      }
-      const int first = kNeighbours ? part[n] * 2 * V : part[n] * V;
-      store<V>(to[n] + first, x[n]);
-      store<V>(to[n] + first + (kNeighbours ? V : a.pairs), y[n]);
     }
   }
+}
 
-  // ---- channels that do not turn, where the rows go elsewhere ----
-  if (!a.copy_q && !a.copy_k) return;
-  constexpr int kCopy = V < 4 ? V : 8;  // 2 * pairs and the head's channels are multiples of it
-  const int rest = (a.dim - 2 * a.pairs) / kCopy;
-  if (rest == 0) return;
-  for (int i = tid; i < tokens * mine * rest; i += kThreads) {
-    const int row = i / rest, t = row / mine;
-    const int head = (row - t * mine) * (int)gridDim.y + (int)blockIdx.y;
-    const bool query = head < a.q_heads;
-    if (!there[t] || !(query ? a.copy_q : a.copy_k)) continue;
-    const RowArgs& in = query ? a.q : a.k;
-    const RowArgs& out = query ? a.q_out : a.k_out;
-    const int64_t h = query ? head : head - a.q_heads;
-    const int first = 2 * a.pairs + (i - row * rest) * kCopy;
-    store<kCopy>(static_cast<uint16_t*>(out.data) + (token0 + t) * out.token_stride +
-                     h * out.head_stride + first,
-                 load<kCopy>(static_cast<const uint16_t*>(in.data) + (token0 + t) * in.token_stride +
-                             h * in.head_stride + first));
-  }
+template <bool kFp16, int V, bool kNeighbours>
+int launch_parts(const RotaryArgs& a, const BatchArgs& b, dim3 grid, int tokens,
+                 cudaStream_t stream) {
+  const int parts =
+      a.pairs / V + (a.copy_q || a.copy_k ? (a.dim - 2 * a.pairs + 2 * V - 1) / (2 * V) : 0);
+  int shift = 0;
+  while ((1 << shift) < parts && (1 << shift) < kThreads) ++shift;
+  rotary_kernel<kFp16, V, kNeighbours><<<grid, kThreads, 0, stream>>>(a, b, tokens, shift);
+  return launch_status();
 }
 
 template <bool kFp16, bool kNeighbours>
@@ -213,15 +238,10 @@ int launch(const RotaryArgs& a, const BatchArgs& b, cudaStream_t stream) {
   int split = 1;
   while (split * 2 <= heads && ctas * split * 2 <= waves) split *= 2;
   const dim3 grid((unsigned)ctas, (unsigned)split);
-  if (a.pairs % 8 == 0)
-    rotary_kernel<kFp16, 8, kNeighbours><<<grid, kThreads, 0, stream>>>(a, b, tokens);
-  else if (a.pairs % 4 == 0)
-    rotary_kernel<kFp16, 4, kNeighbours><<<grid, kThreads, 0, stream>>>(a, b, tokens);
-  else if (a.pairs % 2 == 0)
-    rotary_kernel<kFp16, 2, kNeighbours><<<grid, kThreads, 0, stream>>>(a, b, tokens);
-  else
-    rotary_kernel<kFp16, 1, kNeighbours><<<grid, kThreads, 0, stream>>>(a, b, tokens);
-  return launch_status();
+  if (a.pairs % 8 == 0) return launch_parts<kFp16, 8, kNeighbours>(a, b, grid, tokens, stream);
+  if (a.pairs % 4 == 0) return launch_parts<kFp16, 4, kNeighbours>(a, b, grid, tokens, stream);
+  if (a.pairs % 2 == 0) return launch_parts<kFp16, 2, kNeighbours>(a, b, grid, tokens, stream);
+  return launch_parts<kFp16, 1, kNeighbours>(a, b, grid, tokens, stream);
 }
 
 }  // namespace

@@ -195,7 +195,7 @@ def test_empty_calls_and_overlaps():
     x = torch.zeros(8, 4, 64, dtype=BF16, device="cuda")
     positions = torch.zeros(4, dtype=torch.int32, device="cuda")
     for q, k, out in ((x[:4], None, x[1:5]), (x[:4, :2], x[:4, 2:], (x[4:, :2], x[4:, 1:3])), (x[:4, :2], x[:4, 2:], (x[:4, 2:], x[:4, :2])),
-                      (x[:4], x[:4], (x[:4], x[:4])), (x[:4, :, :], None, x[:1].expand(4, 4, 64))):
+                      (x[:4], x[:4], (x[:4], x[:4])), (x[:4], x[:4], (x[:4], x[4:])), (x[:4], x[:4], (x[4:], x[:4])), (x[:4, :, :], None, x[:1].expand(4, 4, 64))):
         with pytest.raises(ValueError):
             rotary(q, k, positions=positions, out=out)
     rotary(x[:4, :2], x[:4, 2:], positions=positions, out=(x[:4, :2], x[4:, 1:3]))
