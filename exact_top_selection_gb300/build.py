@@ -22,11 +22,12 @@ LIBRARY = os.path.join(BUILD_DIR, "libexact_topk.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["topk_kernels.cu", "cache_kernels.cu", "score_kernels.cu",
-                "attention_kernels.cu", "prompt_attention_kernels.cu", "cache4_kernels.cu",
+                "attention_kernels.cu", "prompt_attention_kernels.cu", "prompt_pair_kernels.cu",
+                "cache4_kernels.cu",
                 "rotary_kernels.cu", "table_kernels.cu"]
 HOST_SOURCES = ["exact_topk_api.cpp", "cache_api.cpp", "batch_api.cpp"]
 HEADERS = ["etk_internal.h", "cache_internal.h", "batch_internal.h", "cache_device.cuh",
-           "tensor_device.cuh"]
+           "tensor_device.cuh", "prompt_device.cuh"]
 PUBLIC_HEADERS = ["exact_topk.h", "exact_topk_cache.h"]
 
 

@@ -1249,7 +1249,10 @@ int launch_attention(const CacheArgs& c, const BatchArgs& b, const AttentionArgs
 int launch_attention4(const Cache4Args& c, const BatchArgs& b, const AttentionArgs& a,
                       cudaStream_t stream) {
   if (a.prompt_tokens > 0) {
-    const int rc = launch_prompt_attention4(c, b, a, stream);
+    const bool pair = a.prompt_tokens * 2 <= kPromptTokens &&
+                      (a.blocks == nullptr || b.width <= kPairListedWidth);
+    const int rc = pair ? launch_prompt_pair(c, b, a, stream)
+                        : launch_prompt_attention4(c, b, a, stream);
     if (rc != EXACT_TOPK_OK) return rc;
   }
   return launch_bits<4>(c, b, a, stream);

@@ -90,6 +90,7 @@ constexpr int64_t partial_floats(int columns, int dim) {
 constexpr int kPromptRows = 128;
 constexpr int kPromptTokens = 32;
 constexpr int kPromptListedWidth = 24576;
+constexpr int kPairListedWidth = 16384;  // of the kernel of two tiles over the 4-bit cache
 
 // Shared memory that a CTA may have.
 constexpr size_t kMostShared = 227 * 1024;
@@ -120,6 +121,7 @@ int launch_prompt_attention(const CacheArgs&, const BatchArgs&, const AttentionA
 int launch_attention(const CacheArgs&, const BatchArgs&, const AttentionArgs&, cudaStream_t);
 int launch_prompt_attention4(const Cache4Args&, const BatchArgs&, const AttentionArgs&,
                              cudaStream_t);
+int launch_prompt_pair(const Cache4Args&, const BatchArgs&, const AttentionArgs&, cudaStream_t);
 int launch_attention4(const Cache4Args&, const BatchArgs&, const AttentionArgs&, cudaStream_t);
 
 }  // namespace etk

@@ -32,7 +32,7 @@
 // tile's union: 133 us in a graph (520 TFLOP/s of the products that count), 137 by calls.
 
 #include "cache_device.cuh"
-#include "tensor_device.cuh"
+#include "prompt_device.cuh"
 
 namespace etk {
 namespace {
@@ -46,69 +46,6 @@ constexpr int kEntries = 128;        // parts of pages held at a time
 constexpr float kRoom = 6.f;         // see attention_kernels.cu; with the part of a value's scale
 constexpr float kMost = 14.f;        // that is no power of two, below 2, all stays under 2^15
 constexpr int kFarthest = 12;        // powers of two between scales of values
-
-__device__ __forceinline__ float infinity() { return __uint_as_float(0x7F800000u); }
-
-__device__ __forceinline__ float exp2_fast(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ float max3(float x, float y, float z) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-  return r;
-}
-
-__device__ __forceinline__ float2 fma2(float2 x, float y, float z) {
-  const float2 yy = make_float2(y, y), zz = make_float2(z, z);
-  float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t&>(r))
-      : "l"(reinterpret_cast<const uint64_t&>(x)), "l"(reinterpret_cast<const uint64_t&>(yy)),
-        "l"(reinterpret_cast<const uint64_t&>(zz)));
-  return r;
-}
-
-__device__ __forceinline__ float2 add2(float2 x, float2 y) {
-  float2 r;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t&>(r))
-      : "l"(reinterpret_cast<const uint64_t&>(x)), "l"(reinterpret_cast<const uint64_t&>(y)));
-  return r;
-}
-
-// Operand whose contraction runs over the lines: 64 channels to a line, `chunk` bytes from one
-// 64 channels to the next.
-__device__ __forceinline__ uint64_t operand_across(uint32_t address, uint32_t chunk) {
-  return (uint64_t)((address & 0x3FFFFu) >> 4) | (uint64_t)(chunk >> 4) << 16 |
-         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-
-// As tensor_mma, with the first operand in tensor memory.
-__device__ __forceinline__ void tensor_mma_from(uint32_t d, uint32_t a, uint64_t b,
-                                                uint32_t kind, bool add) {
-  asm volatile(
-      "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kind), "r"((uint32_t)add)
-      : "memory");
-}
-
-__device__ __forceinline__ void tensor_store32(uint32_t address, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-      "r"(r[30]), "r"(r[31]), "r"(address)
-      : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
 
 // A part of a page: at most 64 tokens.
 struct alignas(16) Entry {
