@@ -11,6 +11,14 @@
 // Scales are part of the FP16 operands (a code times its scale is exact in FP16), units part of the
 // scores' factor and of the outputs. A NaN scale shows as a NaN among a row's sums or outputs; its tile is
 // left to the kernel that runs behind, as is one whose wait ran out.
+//
+// What bounds it: 664 clocks of products for a block and tile (8 of 50, limited by shared memory's
+// reads of both operands, and 4 of 66), so 1328 of the 2200 that a block of both takes; issue
+// slots and latency of the softmax beside them. 2048 tokens x 16 query heads (2 key heads of
+// 128 channels) over 16384: 286 us (900 TFLOP/s); 4096 over 32 pages of 64 tokens each: 131 us.
+// Measured and not kept: two threads a row (355 us: twice the votes and barriers); looking for the
+// maximum only where a block's sum is too large (307); converted pieces exchanged between lanes against
+// bank conflicts, where lanes by token have none (301).
 
 #include "cache_device.cuh"
 #include "prompt_device.cuh"
@@ -381,15 +389,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kSoftmaxWarps + kConvertWarps) {
       // ---- codes to operands: four warps for keys, four for values ----
       // A warp has 16 tokens of the block, 8 at a time: 4 lanes for a token, a lane with D / 4
-      // neighbouring channels. It writes its pieces of 16 bytes in an order by its place and its
-      // token, so that a quarter of a warp touches every bank once.
+      // neighbouring channels. A quarter of the warp has the same channels of 8 tokens, whose
+      // swizzled pieces of 16 bytes touch every bank once.
       const bool keys = warp < kSoftmaxWarps + kConvertWarps / 2;
       const uint8_t* const codes = keys ? c.k : c.v;
       const uint8_t* const scales =
           reinterpret_cast<const uint8_t*>(keys ? c.k_scale : c.v_scale);
       uint64_t* const full = keys ? sm.k_full : sm.v_full;
       uint64_t* const free_again = keys ? sm.k_free : sm.v_free;
-      const int first = (warp & 3) * 16 + (lane >> 2), quarter = lane & 3;
+      const int first = (warp & 3) * 16 + (lane & 7), quarter = lane >> 3;
       uint4 x[2];         // 32 (16) codes of tokens first, first + 8
       uint32_t scale[2];  // and their two scales (one)
       const auto entry_of = [&](int block, int i) -> const Entry& {
@@ -434,26 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < kPieces; ++j)
 #pragma unroll
           for (int n = 0; n < 4; ++n) y[j][n] = times2(y[j][n], by[j >> 1]);
-        // Pieces j of one access: 2 tokens x 4 lanes, lanes 0 and 2 (1 and 3) the same places of two
-        // lines. Exchanging by line and by token puts them on 8 different ones.
-        const int turn = D == 128 ? (quarter >> 1) ^ ((token & 1) << 1) : token & 1;
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-          uint4 w;
-          if constexpr (D == 128) {
-            const bool odd = (turn & 1) != 0, far = (turn & 2) != 0;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-              const uint32_t near = odd ? y[j ^ 1][n] : y[j][n];
-              const uint32_t away = odd ? y[j ^ 3][n] : y[j ^ 2][n];
-              (&w.x)[n] = far ? away : near;
-            }
-          } else {
-#pragma unroll
-            for (int n = 0; n < 4; ++n) (&w.x)[n] = turn ? y[j ^ 1][n] : y[j][n];
-          }
-          *reinterpret_cast<uint4*>(to + (((piece0 + (j ^ turn)) ^ (token & 7)) << 4)) = w;
-        }
+        for (int j = 0; j < kPieces; ++j)
+          *reinterpret_cast<uint4*>(to + (((piece0 + j) ^ (token & 7)) << 4)) =
+              make_uint4(y[j][0], y[j][1], y[j][2], y[j][3]);
       };
       load(0);
       for (int block = 0; block < blocks; ++block) {

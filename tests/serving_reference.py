@@ -177,3 +177,50 @@ class Tables:
             self.kv_len[b] = old + c
         self.q_start[-1] = row
         self.range = [(head + taken) % n, free - taken]
+
+
+def attention(cache, batch, q, blocks, scale, fill):
+    """cache_reference.attention and its tolerance, many rows at a time: for calls of thousands of rows."""
+    q = q.detach().cpu().double()
+    T, QH, D = q.shape
+    G = QH // cache.heads
+    out, tol = torch.full(q.shape, fill, dtype=torch.float64), torch.zeros(q.shape, dtype=torch.float64)
+    eps = torch.finfo(cache.dtype).eps / 2
+    tiny = torch.finfo(cache.dtype).smallest_normal * eps * 2
+    for b, lo, n, length in ref.spans(batch, T, cache.page):
+        if n == 0:
+            continue
+        if length == 0:
+            out[lo:lo + n] = 0.0
+            continue
+        pos = length - n + torch.arange(n)
+        at = list(range(length))
+        for h in range(cache.heads):
+            k, there = cache.rows("k", batch[0][b], h, at)
+            v, _ = cache.rows("v", batch[0][b], h, at)
+            seen = (torch.arange(length) <= pos[:, None]) & there
+            if blocks is not None:
+                lists = blocks.detach().cpu().reshape(-1, cache.heads, blocks.shape[1])[lo:lo + n, h].long()
+                width = -(-length // cache.page) + 1
+                taken = torch.zeros(n, width, dtype=torch.bool)
+                good = (lists >= 0) & (lists <= pos[:, None].div(cache.page, rounding_mode="floor"))
+                taken.scatter_(1, torch.where(good, lists, width - 1), True)
+                taken[:, -1] = False
+                seen &= taken[:, torch.arange(length) // cache.page]
+            u = q[lo:lo + n, h * G:(h + 1) * G]
+            bad_v = v.isnan().any(-1)  # a NaN value reaches the rows that see it, and no other
+            x = torch.where(seen[:, None], u @ k.T * scale, -math.inf)
+            p = torch.softmax(x, -1)
+            none = ~seen.any(-1)
+            p = torch.where(none[:, None, None], 0.0, p)
+            fine = v.nan_to_num(0.0)
+            y = p @ fine
+            hit = (seen & bad_v).double() @ v.isnan().double() > 0  # [n, D]
+            out[lo:lo + n, h * G:(h + 1) * G] = torch.where(hit[:, None], math.nan, y)
+            count = seen.sum(-1).double()[:, None, None]
+            terms = torch.where(seen[:, None], u.abs() @ k.abs().T, 0.0).nan_to_num(0.0).amax(-1, keepdim=True) * abs(scale)
+            rel = 2.0 ** -11 + 2.0 ** -21 + terms * (D + 3) * 2.0 ** -23
+            rel = 2 * rel + (count + 40) * 2.0 ** -24
+            most = torch.where(seen[:, :, None], fine.abs(), 0.0).amax(1)[:, None]
+            tol[lo:lo + n, h * G:(h + 1) * G] = rel * (p.nan_to_num(0.0) @ fine.abs()) + count * 2.0 ** -25 * most * 2
+    return out, tol + out.abs().nan_to_num(0.0, 0.0, 0.0) * eps + tiny

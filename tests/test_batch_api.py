@@ -203,3 +203,18 @@ def test_reference_rotary_keeps_lengths():
     assert torch.equal(got[0], x[0].double()) and torch.allclose(got.norm(dim=-1), x.double().norm(dim=-1), rtol=1e-12)
     back, _ = srv.rotary(got.half(), [0, 7, 10 ** 6], [0.5 ** i for i in range(32)], 1.0, False, 0.0, inverse=True)
     assert ((back - x.double()).abs() <= 4 * 2.0 ** -11 * (1 + x.double().abs().amax())).all()
+
+
+def test_reference_attention_of_many_rows_is_the_other_one():
+    lens, new = [40, 7, 90], [3, 9, 20]
+    tensors, batch = srv.make(1, lens, new, 2, 16, 64, torch.float16)
+    tensors[3].view(torch.uint8)[batch[0][2, 1].long(), 0, 5, 2] = 0x7F
+    batch[0][2, 0] = -1
+    q = ref.rows(2, 34, 4, 64, torch.float16)
+    blocks = torch.randint(-1, 7, (68, 4), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    for lists in (None, blocks):
+        want, tol = ref.attention(srv.Cache4(*tensors), batch, q, lists, 0.125, -7.0)
+        got, got_tol = srv.attention(srv.Cache4(*tensors), batch, q, lists, 0.125, -7.0)
+        assert torch.allclose(got, want, rtol=1e-12, equal_nan=True) and torch.equal(got.isnan(), want.isnan()) and want.isnan().any()
+        fine = ~want.isnan()
+        assert torch.allclose(got_tol[fine], tol[fine], rtol=1e-9)

@@ -484,3 +484,55 @@ def test_empty_calls_do_nothing():
     out = torch.full((4, 4, 64), MARK, dtype=BF16, device="cuda")
     etk.CacheAttention(cache, 2, 4, 4, b.table_width)(torch.full_like(out, math.nan), b, out=out)
     assert (out == MARK).all()
+
+
+# More tiles of 128 rows than SMs, so that two of them share a CTA: 160, 160, 348, 156, 170 and 510 of them.
+@pytest.mark.parametrize("page,dim,heads,group,dtype", [(16, 64, 10, 8, BF16), (64, 128, 5, 16, FP16), (128, 64, 4, 40, BF16),
+                                                        (32, 128, 6, 12, FP16), (64, 128, 10, 9, BF16), (16, 128, 1, 130, BF16)])
+@pytest.mark.parametrize("listed", [False, True])
+def test_two_tiles_a_cta(page, dim, heads, group, dtype, listed):
+    """Sequences that end in a tile's first tokens, in its second half and in a first tile alone; NaN scales; waits that run out."""
+    lens, new = [330, 0, 200, 40, 700, 64], [150, 2, 90, 21, 1, 3]
+    tensors, batch = srv.make(120, lens, new, heads, page, dim, dtype)
+    T = sum(new)
+    q = ref.rows(121, T, heads * group, dim, dtype, 3.0)
+    blocks = some_lists(122, lens, T * heads, page, 12) if listed else None
+    lib = binding._lib()
+    for nan in (False, True):
+        if nan:
+            tensors[3].view(torch.uint8)[batch[0][0, 250 // page].long(), heads - 1, 250 % page, 1] = 0x7F
+            tensors[2].view(torch.uint8)[batch[0][2, 150 // page].long(), 0, 150 % page, 3] = 0x7F
+        units = (2.0, 2.0 ** -3)
+        want, tol = srv.attention(srv.Cache4(*tensors, *units), batch, q, blocks, 1 / math.sqrt(dim), MARK)
+        cache, b = device_cache(tensors, *units), device_batch(batch)
+        attend = etk.CacheAttention(cache, len(lens), T, heads * group, b.table_width, 0 if blocks is None else 12, prompt=1)
+        for limit in (-1, 0, -1):
+            out = torch.full(q.shape, MARK, dtype=dtype, device="cuda")
+            try:
+                assert lib.exact_topk_set_wait_limit(limit) == 0
+                attend(q.cuda(), b, blocks=None if blocks is None else blocks.cuda(), out=out)
+            finally:
+                assert lib.exact_topk_set_wait_limit(-1) == 0
+            got = out.cpu().double()
+            assert torch.equal(got.isnan(), want.isnan()) and want.isnan().any() == nan
+            fine = ~want.isnan()
+            bad = ((got - want).abs() > tol) & fine
+            assert not bad.any(), (limit, bad.nonzero()[:4].tolist(), got[bad][:4].tolist(), want[bad][:4].tolist())
+            assert not attend.counters.any()
+
+
+def test_two_tiles_a_cta_over_long_caches():
+    """More parts of pages than are held at a time, running maxima that rise late, queries of a size that needs it."""
+    lens, new, heads, group, page, dim = [16 * 150 + 5, 700], [200, 100], 10, 8, 16, 64
+    tensors, batch = srv.make(125, lens, new, heads, page, dim, FP16)
+    for j in range(150):
+        s = tensors[2].view(torch.uint8)[batch[0][0, j].long()]
+        s[s != 0x7F] = torch.tensor(2.0 ** (j // 15 - 6)).to(torch.float8_e4m3fn).view(torch.uint8)
+        tensors[2].view(torch.uint8)[batch[0][0, j].long()] = s
+    q = ref.rows(126, 300, heads * group, dim, FP16, 2.0)
+    for blocks in (None, torch.stack([torch.randperm(151, generator=torch.Generator().manual_seed(i))[:140] for i in range(3000)]).to(torch.int32)):
+        want, tol = srv.attention(srv.Cache4(*tensors), batch, q, blocks, 0.125, MARK)
+        cache, b = device_cache(tensors), device_batch(batch)
+        attend = etk.CacheAttention(cache, 2, 300, heads * group, b.table_width, 0 if blocks is None else 140, prompt=1)
+        got = attend(q.cuda(), b, blocks=None if blocks is None else blocks.cuda()).cpu().double()
+        assert ((got - want).abs() <= tol).all()
