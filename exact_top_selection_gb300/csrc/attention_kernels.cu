@@ -35,10 +35,21 @@
 // tile that several CTAs share is joined from their partial results by the last of
 // them to arrive, in the order of their parts, so that results do not depend on timing.
 //
+// The 4-bit cache (kBits = 4). A code times its group's scale is exact in FP16, so operands are
+// products of both, and the rest is as of 8 bits with scales of 1; the unit of the keys is part of the
+// queries' factor, that of the values of the outputs. For the first product a lane's channels
+// are 32 neighbours (of 64: 16), so its codes are one load and its scales another; for the second, codes
+// of two tokens are put side by side in a byte, and a scale of each in a pair of halves. A step
+// is 32 tokens where the page allows it, and the next one is asked for before a step is
+// computed. A step takes as many conversions as of 8 bits and a product for each: issue slots (57% used,
+// conversions at half rate) bound it beside HBM.
+//
 // Measured: 64 sequences of 2048 to 65536 tokens, 4 key heads x 8 query heads of 128 channels
 // (2.4 GB): 360 to 370 us from GPU to GPU, 95 to 98% of the rate of a copy. 8 sequences of 512 K
 // tokens, 3 new ones, 2 x 4 heads of 64 channels (1.06 GB): 209 us. 32 listed pages of 64
-// sequences (134 MB): 34 us.
+// sequences (134 MB): 34 us. In 4 bits: 238 us (1.35 GB, 5.6 TB/s) for the first, 211 for the second
+// (604 MB), 28 for the third. Steps of 16 tokens took 317 us for the first; a fifth CTA an SM
+// changed nothing there (240) and cost 5 us of the third.
 
 #include <climits>
 
