@@ -40,8 +40,8 @@ class _Spec(ctypes.Structure):
 
 class _Tables(ctypes.Structure):
     _fields_ = [(name, ctypes.c_void_p) for name in ("page_table", "kv_len", "q_start", "applied", "slots",
-                                                     "positions", "free_pages", "free_range", "workspace")] + [
-        ("workspace_bytes", ctypes.c_size_t), ("table_pitch", ctypes.c_int64), ("max_tokens", ctypes.c_int64),
+                                                     "positions", "free_pages", "free_range", "counters")] + [
+        ("counter_bytes", ctypes.c_size_t), ("table_pitch", ctypes.c_int64), ("max_tokens", ctypes.c_int64),
         ("num_seqs", ctypes.c_int32), ("table_width", ctypes.c_int32), ("num_pages", ctypes.c_int32),
         ("page_size", ctypes.c_int32)]
 
@@ -54,7 +54,6 @@ def _lib():
         batch, rows, tables = (ctypes.POINTER(t) for t in (_cache._Batch, _cache._Rows, _Tables))
         lib.exact_topk_rotary.argtypes = [ctypes.POINTER(_Spec), batch, p, i64, i32, rows, rows, i32, rows, rows,
                                           i32, p]
-        lib.exact_topk_tables_workspace.argtypes = [i32, ctypes.POINTER(ctypes.c_size_t)]
         lib.exact_topk_update_tables.argtypes = [tables, p, i32, p]
         _bound = lib
     return _bound
@@ -237,9 +236,7 @@ class PageTables:
             slots, positions = (torch.zeros(max_tokens, dtype=torch.int32, device=dev) if t is None else t
                                 for t in (slots, positions))
             self.applied = torch.zeros(B, dtype=torch.int32, device=dev)
-            size = ctypes.c_size_t()
-            _etk._check(_lib().exact_topk_tables_workspace(B, ctypes.byref(size)), "exact_topk_tables_workspace")
-            self.workspace = torch.zeros(size.value // 4, dtype=torch.int32, device=dev)
+            self.counters = torch.zeros(16, dtype=torch.uint8, device=dev)
             _cache._wait_for_buffers()
         self.batch = _cache.SequenceBatch(page_table, kv_len, q_start)
         for t, name, size in ((free_pages, "free_pages", None), (free_range, "free_range", 2),
@@ -256,7 +253,7 @@ class PageTables:
         self.device, self._index = dev, dev.index
         self._c = _Tables(page_table.data_ptr(), kv_len.data_ptr(), q_start.data_ptr(), self.applied.data_ptr(),
                           slots.data_ptr(), positions.data_ptr(), free_pages.data_ptr(), free_range.data_ptr(),
-                          self.workspace.data_ptr(), self.workspace.numel() * 4, self.batch._c.table_pitch, max_tokens,
+                          self.counters.data_ptr(), self.counters.numel(), self.batch._c.table_pitch, max_tokens,
                           B, self.batch.table_width, pages, page_size)
         self._ref = ctypes.byref(self._c)
 

@@ -35,8 +35,7 @@ HEAD_DIMS = (64, 128)
 CACHE_SYMBOLS = ("exact_topk_cache_write", "exact_topk_cache_read", "exact_topk_block_scores",
                  "exact_topk_make_attention_plan", "exact_topk_attention_run", "exact_topk_set_wait_limit",
                  "exact_topk_cache4_write", "exact_topk_cache4_read", "exact_topk_cache4_block_scores",
-                 "exact_topk_cache4_attention_run", "exact_topk_rotary", "exact_topk_tables_workspace",
-                 "exact_topk_update_tables")
+                 "exact_topk_cache4_attention_run", "exact_topk_rotary", "exact_topk_update_tables")
 GROUP = 16  # channels that share a scale in 4 bits
 
 

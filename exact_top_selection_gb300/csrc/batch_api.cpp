@@ -89,18 +89,11 @@ int exact_topk_rotary(const exact_topk_rotary_spec* spec, const exact_topk_batch
   return launch_rotary(a, b, reinterpret_cast<cudaStream_t>(stream));
 }
 
-int exact_topk_tables_workspace(int num_seqs, size_t* bytes) {
-  if (bytes == nullptr) return EXACT_TOPK_ERR_NULL_POINTER;
-  if (num_seqs < 1 || num_seqs > EXACT_TOPK_MAX_SEQS) return EXACT_TOPK_ERR_BAD_BATCH;
-  *bytes = (size_t)table_work_words(num_seqs) * 4;
-  return EXACT_TOPK_OK;
-}
-
 int exact_topk_update_tables(const exact_topk_page_tables* t, const int32_t* change, int negate,
                              struct CUstream_st* stream) {
   if (t == nullptr || change == nullptr || t->page_table == nullptr || t->kv_len == nullptr ||
       t->q_start == nullptr || t->free_pages == nullptr || t->free_range == nullptr ||
-      t->workspace == nullptr)
+      t->counters == nullptr)
     return EXACT_TOPK_ERR_NULL_POINTER;
   const int P = t->page_size;
   if ((P != 16 && P != 32 && P != 64 && P != 128) || t->num_pages < 1 ||
@@ -110,12 +103,11 @@ int exact_topk_update_tables(const exact_topk_page_tables* t, const int32_t* cha
       (int64_t)t->table_width * P > ((int64_t)1 << 30) || t->table_pitch < t->table_width ||
       t->max_tokens < 0 || t->max_tokens > kMostTokens)
     return EXACT_TOPK_ERR_BAD_BATCH;
-  if (t->workspace_bytes < (size_t)table_work_words(t->num_seqs) * 4)
-    return EXACT_TOPK_ERR_WORKSPACE_TOO_SMALL;
+  if (t->counter_bytes < 4) return EXACT_TOPK_ERR_COUNTERS_TOO_SMALL;
   for (const void* p : {(const void*)t->page_table, (const void*)t->kv_len,
                         (const void*)t->q_start, (const void*)t->applied, (const void*)t->slots,
                         (const void*)t->positions, (const void*)t->free_pages,
-                        (const void*)t->free_range, (const void*)t->workspace,
+                        (const void*)t->free_range, (const void*)t->counters,
                         (const void*)change})
     if (!aligned(p, 4)) return EXACT_TOPK_ERR_MISALIGNED;
   TableArgs a{};
@@ -127,7 +119,7 @@ int exact_topk_update_tables(const exact_topk_page_tables* t, const int32_t* cha
   a.positions = t->positions;
   a.free_pages = t->free_pages;
   a.free_range = t->free_range;
-  a.work = static_cast<int32_t*>(t->workspace);
+  a.arrived = static_cast<int32_t*>(t->counters);
   a.change = change;
   a.pitch = t->table_pitch;
   a.max_tokens = t->max_tokens;

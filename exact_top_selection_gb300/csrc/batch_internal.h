@@ -27,16 +27,12 @@ struct TableArgs {
   int32_t* positions;
   int32_t* free_pages;
   int32_t* free_range;
-  int32_t* work;
+  int32_t* arrived;  // CTAs of the call that have read its inputs
   const int32_t* change;
   int64_t pitch;
   int64_t max_tokens;
   int num_seqs, width, num_pages, page_shift, negate;
 };
-
-// Words of the tables' workspace: for each sequence its length before, its first place among the
-// pages taken and among those given back; then where the ring was.
-constexpr int64_t table_work_words(int num_seqs) { return 3 * ((int64_t)num_seqs + 1) + 2; }
 
 int launch_rotary(const RotaryArgs&, const BatchArgs&, cudaStream_t);
 int launch_update_tables(const TableArgs&, cudaStream_t);

@@ -3,12 +3,15 @@
 //
 // Everything a sequence needs to know of the others is four sums over the sequences before it:
 // of the pages asked for, of the pages given back, of the rows asked for and of the rows granted.
-// One CTA forms them. A page taken is then a place in the ring, or, behind the pages that
-// were free, one that another sequence gives back in this call; that sequence's table still
-// names it. So all pages and rows can be filled in at once, in any order, and no page is
-// counted by an atomic: results do not depend on timing.
+// Every CTA forms them for itself, in shared memory. A page taken is then a place in the ring, or,
+// behind the pages that were free, one that another sequence gives back in this call; that
+// sequence's table still names it. So all pages and rows can be filled in at once, in any order, and
+// no page is counted by an atomic: results do not depend on timing. The last CTA to have read the
+// lengths and the ring's place writes the new ones.
 //
-// Little is moved (4 bytes for a page, 8 for a row): a decoding step is bound by its latency.
+// Little is moved (4 bytes for a page, 8 for a row): a call is bound by its latency, 3.2 us for a
+// decoding step of 64 sequences, 7.4 for 1000 prompts of 1 M tokens in pages of 16. (A CTA that
+// forms the sums ahead of a second kernel that fills in took 11.4.)
 
 #include <climits>
 
@@ -18,10 +21,11 @@
 namespace etk {
 namespace {
 
-constexpr int kMostThreads = 1024;
-constexpr int kFill = 256;  // threads and units of a CTA that fills in
-constexpr int kAloneUnits = 1024;  // one CTA does it all up to here
-constexpr int kOwnRows = 4;        // a unit's rows that its own thread writes
+constexpr int kAloneThreads = 256;  // one CTA does it all where there are few units
+constexpr int kAloneUnits = 1024;
+constexpr int kThreads = 512;       // else
+constexpr int kMostCtas = 304;
+constexpr int kOwnRows = 4;         // a unit's rows that its own thread writes
 
 __device__ __forceinline__ int pages_of(int length, int shift) {
   return (int)(((int64_t)length + (1 << shift) - 1) >> shift);
@@ -33,14 +37,16 @@ __device__ __forceinline__ int length_of(const TableArgs& a, int seq) {
   return n < 0 ? 0 : (n > most ? (int)most : n);
 }
 
-// Where the sums and the ring's place before the call are kept, and the row ranges: in the workspace,
-// or, where one CTA does it all, in its shared memory.
+// In shared memory: of each sequence its length before the call, its first place among the pages
+// taken and among those given back, and its first row; and where the ring was.
 struct Work {
-  int32_t *length, *take, *give, *ring, *q_start;
-  __device__ Work(int32_t* at, int num_seqs, int32_t* starts)
+  int32_t *length, *take, *give, *start, *ring;
+  __device__ Work(int32_t* at, int num_seqs)
       : length(at), take(length + num_seqs + 1), give(take + num_seqs + 1),
-        ring(give + num_seqs + 1), q_start(starts) {}
+        start(give + num_seqs + 1), ring(start + num_seqs + 1) {}
 };
+
+size_t work_bytes(int num_seqs) { return (4 * ((size_t)num_seqs + 1) + 2) * 4; }
 
 // Sums over the CTA's threads before each, and over all of them.
 template <int N>
@@ -73,11 +79,12 @@ __device__ __forceinline__ void sums_before(int64_t (&x)[N], int64_t (&all)[N],
   }
 }
 
-// Lengths, row ranges, the ring's new place, and what the filling needs to know.
+// What the filling needs to know; then, by the last CTA to come so far, lengths, row ranges and the
+// ring's new place.
 template <int kEach>
 __device__ __forceinline__ void plan(const TableArgs& a, const Work& work) {
-  __shared__ int64_t shared3[kMostThreads / 32][3];
-  __shared__ int64_t shared2[kMostThreads / 32][2];
+  __shared__ int64_t shared3[32][3], shared2[32][2];
+  __shared__ int s_last;
   const int tid = threadIdx.x;
   const int64_t most = (int64_t)a.width << a.page_shift;
   int head = a.free_range[0] % a.num_pages;
@@ -112,10 +119,10 @@ __device__ __forceinline__ void plan(const TableArgs& a, const Work& work) {
   const int64_t there = have + given;
   int64_t take = sum[0], give = sum[1], asked = sum[2];
   int64_t got[2] = {0, 0}, all_got[2];  // rows granted, pages taken
-  int64_t first_take[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    first_take[i] = take;
+    const int seq = tid * kEach + i;
+    const int64_t first = take;
     take += need[i];
     asked += change[i] > 0 ? change[i] : 0;
     if (change[i] > 0 && ((need[i] > 0 && take > there) || asked > a.max_tokens)) change[i] = 0;
@@ -123,30 +130,49 @@ __device__ __forceinline__ void plan(const TableArgs& a, const Work& work) {
       got[0] += change[i];
       got[1] += need[i];
     }
+    if (seq < a.num_seqs) {
+      work.length[seq] = length[i];
+      work.take[seq] = (int)(first < a.num_pages ? first : a.num_pages);
+      work.give[seq] = (int)(give < a.num_pages ? give : a.num_pages);
+    }
+    give += back[i];
   }
   sums_before<2>(got, all_got, shared2);
   int64_t row = got[0];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int seq = tid * kEach + i;
-    if (seq >= a.num_seqs) continue;
-    a.kv_len[seq] = (int)(length[i] + change[i]);
-    if (a.applied != nullptr) a.applied[seq] = (int)change[i];
-    a.q_start[seq] = work.q_start[seq] = (int)row;
+    if (seq < a.num_seqs) work.start[seq] = (int)row;
     row += change[i] > 0 ? change[i] : 0;
-    work.length[seq] = length[i];
-    work.take[seq] = (int)(first_take[i] < a.num_pages ? first_take[i] : a.num_pages);
-    work.give[seq] = (int)(give < a.num_pages ? give : a.num_pages);
-    give += back[i];
   }
   if (tid == 0) {
-    a.q_start[a.num_seqs] = work.q_start[a.num_seqs] = (int)all_got[0];
+    work.start[a.num_seqs] = (int)all_got[0];
     work.give[a.num_seqs] = (int)given;
     work.ring[0] = head;
     work.ring[1] = have;
+    // every thread has read what it needs (sums_before waits for all)
+    s_last = gridDim.x == 1;
+    if (gridDim.x > 1) {
+      __threadfence();
+      s_last = atomicAdd(a.arrived, 1) == (int)gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int seq = tid * kEach + i;
+    if (seq >= a.num_seqs) continue;
+    a.kv_len[seq] = (int)(length[i] + change[i]);
+    a.q_start[seq] = work.start[seq];
+    if (a.applied != nullptr) a.applied[seq] = (int)change[i];
+  }
+  if (tid == 0) {
     const int64_t free = have + given - all_got[1];
+    a.q_start[a.num_seqs] = (int)all_got[0];
     a.free_range[0] = (int)((head + all_got[1]) % a.num_pages);
     a.free_range[1] = (int)(free < a.num_pages ? free : a.num_pages);
+    if (gridDim.x > 1) *a.arrived = 0;
   }
 }
 
@@ -165,29 +191,30 @@ __device__ __forceinline__ int giver(const Work& w, int num_seqs, int q) {
 
 __device__ __forceinline__ int page_given(const TableArgs& a, const Work& w, int q) {
   const int seq = giver(w, a.num_seqs, q);
-  const int kept = pages_of(a.kv_len[seq], a.page_shift);
+  const int kept = pages_of(w.length[seq], a.page_shift) - (w.give[seq + 1] - w.give[seq]);
   return a.table[(int64_t)seq * a.pitch + kept + (q - w.give[seq])];
 }
 
-// Pages and rows of `units` units from `unit0` on: a unit is the part of a page that a sequence's
-// new rows reach, its slots laid out by first_slot. With all threads of the CTA.
-__device__ __forceinline__ void fill(const TableArgs& a, const Work& work, int64_t unit0,
-                                     int units) {
-  __shared__ int s_row[kFill], s_count[kFill], s_slot[kFill], s_position[kFill];
+// Pages and rows, a CTA's units by its index: a unit is the part of a page that a sequence's new rows
+// reach, its slots laid out by first_slot. With all threads of the CTA.
+template <int kUnits>
+__device__ __forceinline__ void fill(const TableArgs& a, const Work& work, int64_t units) {
+  __shared__ int s_row[kUnits], s_count[kUnits], s_slot[kUnits], s_position[kUnits];
   const int P = 1 << a.page_shift, tid = threadIdx.x;
   const int head = work.ring[0], have = work.ring[1];
   BatchArgs b{};
-  b.q_start = work.q_start;
+  b.q_start = work.start;
   b.num_tokens = a.max_tokens;
   b.num_seqs = a.num_seqs;
-  for (int base = 0; base < units; base += kFill) {
-    const int count = units - base < kFill ? units - base : kFill;
+  for (int64_t base = (int64_t)blockIdx.x * kUnits; base < units;
+       base += (int64_t)gridDim.x * kUnits) {
+    const int count = units - base < kUnits ? (int)(units - base) : kUnits;
     bool many = false;
     if (tid < count) {
-      const int64_t unit = unit0 + base + tid;
+      const int64_t unit = base + tid;
       const int seq = sequence_of_slot(b, unit, P, 2);
       const int index = (int)(unit - first_slot(b, seq, P, 2));
-      const int begin = work.q_start[seq], rows = work.q_start[seq + 1] - begin;
+      const int begin = work.start[seq], rows = work.start[seq + 1] - begin;
       const int length = work.length[seq];
       const int place = (length >> a.page_shift) + index;  // of the page in the sequence
       const int64_t from = (int64_t)place << a.page_shift;
@@ -241,28 +268,29 @@ __device__ __forceinline__ void give_back(const TableArgs& a, const Work& work, 
     a.free_pages[(begin + q) % a.num_pages] = page_given(a, work, (int)q);
 }
 
-template <int kEach>
-__global__ void __launch_bounds__(kMostThreads) plan_tables_kernel(TableArgs a) {
-  plan<kEach>(a, Work(a.work, a.num_seqs, a.q_start));
+template <int kUnits, int kEach>
+__global__ void __launch_bounds__(kUnits) update_tables_kernel(TableArgs a, int64_t units) {
+  extern __shared__ int32_t words[];
+  const Work work(words, a.num_seqs);
+  plan<kEach>(a, work);
+  if (work.give[a.num_seqs] > 0)
+    give_back(a, work, (int64_t)blockIdx.x * kUnits + threadIdx.x, (int64_t)gridDim.x * kUnits);
+  if (work.start[a.num_seqs] > 0) fill<kUnits>(a, work, units);
 }
 
-__global__ void __launch_bounds__(kFill) fill_tables_kernel(TableArgs a, int64_t units) {
-  const Work work(a.work, a.num_seqs, a.q_start);
-  give_back(a, work, (int64_t)blockIdx.x * kFill + threadIdx.x, (int64_t)gridDim.x * kFill);
-  const int64_t unit0 = (int64_t)blockIdx.x * kFill;
-  const int64_t left = units - unit0;
-  if (left > 0) fill(a, work, unit0, left < kFill ? (int)left : kFill);
-}
-
-// Both in one CTA, of few units: so of at most kAloneUnits / 2 sequences.
-__global__ void __launch_bounds__(kAloneUnits / 2) update_tables_kernel(TableArgs a, int units) {
-  constexpr int kSeqs = kAloneUnits / 2 + 1;
-  __shared__ int32_t words[3 * kSeqs + 2], starts[kSeqs];
-  const Work work(words, a.num_seqs, starts);
-  plan<1>(a, work);
-  __syncthreads();
-  if (work.give[a.num_seqs] > 0) give_back(a, work, threadIdx.x, blockDim.x);
-  if (starts[a.num_seqs] > 0) fill(a, work, 0, units);
+template <int kUnits, int kEach>
+int launch(const TableArgs& a, int64_t units, int64_t ctas, cudaStream_t stream) {
+  constexpr size_t most = (4 * ((size_t)EXACT_TOPK_MAX_SEQS + 1) + 2) * 4;
+  const auto kernel = update_tables_kernel<kUnits, kEach>;
+  const size_t bytes = work_bytes(a.num_seqs);
+  // the largest call's size: the limit is the kernel's, whichever thread launches it
+  if (bytes > 32 * 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                (int)most) != cudaSuccess) {
+    cudaGetLastError();
+    return EXACT_TOPK_ERR_CUDA;
+  }
+  kernel<<<(unsigned)ctas, kUnits, bytes, stream>>>(a, units);
+  return launch_status();
 }
 
 }  // namespace
@@ -270,20 +298,16 @@ __global__ void __launch_bounds__(kAloneUnits / 2) update_tables_kernel(TableArg
 int launch_update_tables(const TableArgs& a, cudaStream_t stream) {
   // units of the new rows, at most
   const int64_t units = (a.max_tokens >> a.page_shift) + 2 * (int64_t)a.num_seqs;
-  const int threads = (a.num_seqs + 31) / 32 * 32;
   if (units <= kAloneUnits) {
-    update_tables_kernel<<<1, threads < kFill ? kFill : threads, 0, stream>>>(a, (int)units);
-    return launch_status();
+    if (a.num_seqs <= kAloneThreads) return launch<kAloneThreads, 1>(a, units, 1, stream);
+    return launch<kAloneThreads, 2>(a, units, 1, stream);
   }
-  if (threads <= kMostThreads)
-    plan_tables_kernel<1><<<1, threads, 0, stream>>>(a);
-  else
-    plan_tables_kernel<4><<<1, kMostThreads, 0, stream>>>(a);
-  int64_t ctas = (units + kFill - 1) / kFill;
-  if (ctas < 64) ctas = 64;  // to give pages back
-  if (cudaPeekAtLastError() == cudaSuccess)
-    fill_tables_kernel<<<(unsigned)ctas, kFill, 0, stream>>>(a, units);
-  return launch_status();
+  const int64_t ctas = (units + kThreads - 1) / kThreads;
+  const int64_t some = ctas < kMostCtas ? ctas : kMostCtas;
+  if (a.num_seqs <= kThreads) return launch<kThreads, 1>(a, units, some, stream);
+  if (a.num_seqs <= 2 * kThreads) return launch<kThreads, 2>(a, units, some, stream);
+  if (a.num_seqs <= 4 * kThreads) return launch<kThreads, 4>(a, units, some, stream);
+  return launch<kThreads, 8>(a, units, some, stream);
 }
 
 }  // namespace etk

@@ -244,8 +244,9 @@ int exact_topk_cache4_read(const exact_topk_cache4* cache, const exact_topk_batc
                            int64_t num_tokens, const exact_topk_rows* k, const exact_topk_rows* v,
                            struct CUstream_st* stream);
 
-/* As exact_topk_block_scores. A stored key is off by up to a third of its group's largest
- * magnitude over 2, and may lie beyond the bounds, which are of the keys as they were written. */
+/* As exact_topk_block_scores. A stored key is off by up to 0.18 of its group's largest magnitude
+ * (by more where that is below 0.1 units or beyond 2688), and may lie beyond the bounds, which are
+ * of the keys as they were written. */
 int exact_topk_cache4_block_scores(const exact_topk_cache4* cache, const exact_topk_batch* batch,
                                    int64_t num_tokens, int q_heads, const exact_topk_rows* q,
                                    int keep_first, int keep_last, float* scores,
@@ -303,7 +304,7 @@ int exact_topk_rotary(const exact_topk_rotary_spec* spec, const exact_topk_batch
  *   slots, positions  device int32 [max_tokens], written; may be NULL
  *   free_pages  device int32 [num_pages], a ring of page ids
  *   free_range  device int32 [2]: the first free page's place in the ring, and how many there are
- *   workspace   device, >= exact_topk_tables_workspace bytes, 4-byte aligned, contents ignored
+ *   counters    device, 4 bytes or more, 4-byte aligned, all-zero on entry and on return
  * num_pages * page_size must be below 2^31. A page's id stands once: in the ring or in a table. */
 typedef struct exact_topk_page_tables {
   int32_t* page_table;
@@ -314,8 +315,8 @@ typedef struct exact_topk_page_tables {
   int32_t* positions;
   int32_t* free_pages;
   int32_t* free_range;
-  void* workspace;
-  size_t workspace_bytes;
+  void* counters;
+  size_t counter_bytes;
   int64_t table_pitch;
   int64_t max_tokens;
   int32_t num_seqs;
@@ -323,9 +324,6 @@ typedef struct exact_topk_page_tables {
   int32_t num_pages;
   int32_t page_size;
 } exact_topk_page_tables;
-
-/* Bytes of workspace for num_seqs sequences. Errors: NULL_POINTER, BAD_BATCH. */
-int exact_topk_tables_workspace(int num_seqs, size_t* bytes);
 
 /* Sequence b grows by change[b] tokens (negative: loses its last -change[b], all it has where it
  * has fewer; with negate nonzero by -change[b]). Pages that are no longer reached go to the end of
@@ -341,8 +339,9 @@ int exact_topk_tables_workspace(int num_seqs, size_t* bytes);
  *   applied     the change that was made, 0 for a refused sequence; may be `change` itself
  *   slots, positions  of each new row: page * page_size + offset, and its place in the
  *               sequence; rows behind the last are left as they were
- * change is device int32 [num_seqs]. Results do not depend on the order in which CTAs run.
- * Errors: NULL_POINTER, BAD_CACHE (pages), BAD_BATCH, WORKSPACE_TOO_SMALL, MISALIGNED, CUDA. */
+ * change is device int32 [num_seqs]. Results do not depend on the order in which CTAs run. Calls on
+ * the same tables or counters must not overlap on the GPU.
+ * Errors: NULL_POINTER, BAD_CACHE (pages), BAD_BATCH, COUNTERS_TOO_SMALL, MISALIGNED, CUDA. */
 int exact_topk_update_tables(const exact_topk_page_tables* tables, const int32_t* change,
                              int negate, struct CUstream_st* stream);
 

@@ -92,28 +92,22 @@ def test_rotary_refuses_bad_arguments():
 
 def test_tables_refuse_bad_arguments():
     lib, byref = binding._lib(), ctypes.byref
-    size = ctypes.c_size_t()
-    assert lib.exact_topk_tables_workspace(4, byref(size)) == 0 and size.value >= 4 * 3 * 4
-    assert lib.exact_topk_tables_workspace(4, None) == -1
-    assert lib.exact_topk_tables_workspace(0, byref(size)) == -10 and lib.exact_topk_tables_workspace(4097, byref(size)) == -10
-    lib.exact_topk_tables_workspace(4, byref(size))
-
     def call(change=fake(20), **fields):
-        t = binding._Tables(*(fake(i) for i in range(1, 10)), size.value, 8, 100, 4, 8, 10, 16)
+        t = binding._Tables(*(fake(i) for i in range(1, 10)), 16, 8, 100, 4, 8, 10, 16)
         for name, value in fields.items():
             setattr(t, name, value)
         return lib.exact_topk_update_tables(byref(t), change, 0, None)
 
     assert lib.exact_topk_update_tables(None, fake(20), 0, None) == -1 and call(change=None) == -1
-    for name in ("page_table", "kv_len", "q_start", "free_pages", "free_range", "workspace"):
+    for name in ("page_table", "kv_len", "q_start", "free_pages", "free_range", "counters"):
         assert call(**{name: None}) == -1, name
     for bad in (dict(page_size=8), dict(page_size=48), dict(num_pages=0), dict(num_pages=1 << 27)):
         assert call(**bad) == -9, bad
     for bad in (dict(num_seqs=0), dict(num_seqs=4097), dict(table_width=0), dict(table_width=9), dict(table_width=1 << 27, table_pitch=1 << 27),
                 dict(max_tokens=-1), dict(max_tokens=(1 << 24) + 1)):
         assert call(**bad) == -10, bad
-    assert call(workspace_bytes=size.value - 4) == -5
-    for name in ("page_table", "kv_len", "q_start", "applied", "slots", "positions", "free_pages", "free_range", "workspace"):
+    assert call(counter_bytes=3) == -4
+    for name in ("page_table", "kv_len", "q_start", "applied", "slots", "positions", "free_pages", "free_range", "counters"):
         assert call(**{name: fake(3) + 2}) == -6, name
     assert call(change=fake(20) + 1) == -6
 

@@ -18,7 +18,7 @@ def check(tables, plain):
     for name in ("kv_len", "q_start", "applied", "slots", "positions"):
         assert getattr(tables, name).tolist() == getattr(plain, name), name
     assert tables.free_pages.tolist() == plain.ring and tables.free_range.tolist() == plain.range
-    assert tables.page_table.tolist() == plain.table
+    assert tables.page_table.tolist() == plain.table and not tables.counters.any()
 
 
 def pair(pages, seqs, width, page, max_tokens, strided=False, head=0):
