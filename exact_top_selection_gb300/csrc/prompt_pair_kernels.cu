@@ -13,12 +13,15 @@
 // left to the kernel that runs behind, as is one whose wait ran out.
 //
 // What bounds it: 664 clocks of products for a block and tile (8 of 50, limited by shared memory's
-// reads of both operands, and 4 of 66), so 1328 of the 2200 that a block of both takes; issue
-// slots and latency of the softmax beside them. 2048 tokens x 16 query heads (2 key heads of
-// 128 channels) over 16384: 286 us (900 TFLOP/s); 4096 over 32 pages of 64 tokens each: 131 us.
-// Measured and not kept: two threads a row (355 us: twice the votes and barriers); looking for the
-// maximum only where a block's sum is too large (307); converted pieces exchanged between lanes against
-// bank conflicts, where lanes by token have none (301).
+// reads of both operands, and 4 of 66), so 1328 of the 2150 that a block of both takes, and the
+// softmax warps, two for each scheduler, whose instructions wait for one another. 2048 tokens x 16
+// query heads (2 key heads of 128 channels) over 16384: 280 us (920 TFLOP/s); 4096 over 32 pages of 64
+// tokens each: 131 us. Measured and not kept: two threads a row (355 us: twice the votes
+// and barriers); looking for the maximum only where a block's sum is too large (+20); the next block's
+// scores asked for before the probabilities are stored (+45: registers); scores and outputs issued
+// by warps of their own (no difference); probabilities stored 64 tokens at a time (286);
+// converted pieces exchanged between lanes against bank conflicts, where lanes by token have none
+// (301).
 
 #include "cache_device.cuh"
 #include "prompt_device.cuh"
@@ -36,6 +39,17 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kBlock = 64;                       // cached tokens of a block
 constexpr int kEntries = 128;                    // parts of pages held at a time
 constexpr float kRoom = 6.f, kMost = 14.f;       // see attention_kernels.cu
+
+__device__ __forceinline__ void tensor_store16(uint32_t address, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(address)
+      : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
 
 // A part of a page: at most 64 tokens.
 struct alignas(16) Entry {
@@ -252,6 +266,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   };
 
+  // 32 tokens' probabilities times a power of two: what falls below FP16's normal numbers is off by
+  // 2^-25, against a largest one of 2^kRoom
+  const auto scale_probabilities = [&](uint32_t at, float by) {
+    float v[16];
+    uint32_t w[16];
+    tensor_load16(at, v);
+    tensor_wait(v);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 x = unpack2<true>(__float_as_uint(v[k]));
+      w[k] = pack2<true>(x.x * by, x.y * by);
+    }
+    tensor_store16(at, w);
+  };
+
   for (int chunk0 = 0; chunk0 < (count << part_shift); chunk0 += kEntries) {
     const int left = (count << part_shift) - chunk0;
     const int entries = left < kEntries ? left : kEntries;
@@ -315,66 +344,79 @@ __global__ void __launch_bounds__(kThreads, 1)
           cuts |= takes && seen[k] < 1 << part_tokens_shift;
         }
         cuts = __any_sync(~0u, cuts);
-        // Probabilities under the running maximum, 16 tokens at a time, the next ones' scores on
-        // their way. Where a score turns out too far above the maximum, that is raised and
-        // the block done again: it is seldom.
-        uint32_t p[32];
-        float2 sum;
+        // Probabilities under the running maximum, 32 tokens at a time. They take the place of
+        // scores that have been read. Where a score turns out too far above the maximum, that is
+        // raised by a whole number and the 32 are done again: it is seldom.
         float by = 1.f;
         bool some = false;
-        for (int attempt = 0; attempt < 2; ++attempt) {
-          const float base = m == -infinity() ? 0.f : m;
-          float high = -infinity();
-          sum = make_float2(0.f, 0.f);
-          float s[2][16];
-          tensor_load16(from, s[0]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            constexpr int kPartGroups = 4 >> kPartShift;  // 16 tokens of a part
-            const int part = k / kPartGroups;
-            const float(&x)[16] = s[k & 1];
-            tensor_wait(s[k & 1]);
-            if (k < 3) tensor_load16(from + (k + 1) * 16, s[(k + 1) & 1]);
-            const float offset = seen[part] > 0 ? -base : -infinity();
-            float2 y[8];
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[16];
+          float2 sum;
+          for (int attempt = 0; attempt < 2; ++attempt) {
+            const float base = m == -infinity() ? 0.f : m;
+            float high = -infinity();
+            sum = make_float2(0.f, 0.f);
+            float s[2][16];
+            tensor_load16(from + half * 32, s[0]);
+            tensor_load16(from + half * 32 + 16, s[1]);
+            tensor_wait(s[0]);
+            tensor_wait(s[1]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              y[i] = fma2(make_float2(x[2 * i], x[2 * i + 1]), row_factor, offset);
-            if (cuts) {
-              const int left = seen[part] - k % kPartGroups * 16;
+            for (int k = 0; k < 2; ++k) {
+              constexpr int kPartGroups = 4 >> kPartShift;  // 16 tokens of a part
+              const int group = half * 2 + k, part = group / kPartGroups;
+              const float(&x)[16] = s[k];
+              const float offset = seen[part] > 0 ? -base : -infinity();
+              float2 y[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                y[i] = fma2(make_float2(x[2 * i], x[2 * i + 1]), row_factor, offset);
+              if (cuts) {
+                const int left = seen[part] - group % kPartGroups * 16;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  y[i].x = 2 * i < left ? y[i].x : -infinity();
+                  y[i].y = 2 * i + 1 < left ? y[i].y : -infinity();
+                }
+              }
+              const float high0 =
+                  max3(max3(y[0].x, y[0].y, y[1].x), y[1].y, max3(y[2].x, y[2].y, y[3].x));
+              const float high1 =
+                  max3(max3(y[3].y, y[4].x, y[4].y), y[5].x, max3(y[5].y, y[6].x, y[6].y));
+              high = max3(high, max3(high0, y[7].x, y[7].y), high1);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                y[i].x = 2 * i < left ? y[i].x : -infinity();
-                y[i].y = 2 * i + 1 < left ? y[i].y : -infinity();
+                y[i].x = exp2_fast(y[i].x);
+                y[i].y = exp2_fast(y[i].y);
               }
-            }
-            const float high0 =
-                max3(max3(y[0].x, y[0].y, y[1].x), y[1].y, max3(y[2].x, y[2].y, y[3].x));
-            const float high1 =
-                max3(max3(y[3].y, y[4].x, y[4].y), y[5].x, max3(y[5].y, y[6].x, y[6].y));
-            high = max3(high, max3(high0, y[7].x, y[7].y), high1);
+              const float2 sum0 = add2(add2(y[0], y[1]), add2(y[2], y[3]));
+              const float2 sum1 = add2(add2(y[4], y[5]), add2(y[6], y[7]));
+              sum = add2(sum, add2(sum0, sum1));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              y[i].x = exp2_fast(y[i].x);
-              y[i].y = exp2_fast(y[i].y);
+              for (int i = 0; i < 8; ++i) p[k * 8 + i] = pack2<true>(y[i].x, y[i].y);
             }
-            const float2 sum0 = add2(add2(y[0], y[1]), add2(y[2], y[3]));
-            const float2 sum1 = add2(add2(y[4], y[5]), add2(y[6], y[7]));
-            sum = add2(sum, add2(sum0, sum1));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[k * 8 + i] = pack2<true>(y[i].x, y[i].y);
+            const bool raise = high > (m == -infinity() ? m : kMost);
+            if (!__any_sync(~0u, raise)) break;
+            some = true;
+            float less = 1.f;
+            if (raise) {
+              if (m == -infinity()) {
+                m = high - kRoom;
+                less = 0.f;
+              } else {
+                const float up = floorf(high - kRoom);
+                m += up;
+                less = exp2_fast(-up);  // a power of two
+              }
+              l *= less;
+              by *= less;
+            }
+            if (half > 0) scale_probabilities(from, less);
           }
-          const bool raise = high > (m == -infinity() ? m : kMost);
-          if (!__any_sync(~0u, raise)) break;
-          some = true;
-          if (raise) {
-            const float best = base + high - kRoom;
-            by = m == -infinity() ? 0.f : exp2_fast(m - best);
-            m = best;
-            l *= by;
-          }
+          l += sum.x + sum.y;
+          tensor_store16(from + half * 16, p);
         }
-        l += sum.x + sum.y;
         if (some && n > 0) {  // O is in place up to the block before
           ok = was_added(n - 1);
           ok = __all_sync(~0u, ok);
@@ -382,7 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           scale_outputs(by);
         }
-        tensor_store32(from, p);
         asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
         barrier_arrive(&sm.weighed[tile][n & 1]);  // a warp may be a block ahead of another
       }
