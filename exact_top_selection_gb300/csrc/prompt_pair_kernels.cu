@@ -17,7 +17,7 @@
 // softmax warps, two for each scheduler, whose instructions wait for one another. 2048 tokens x 16
 // query heads (2 key heads of 128 channels) over 16384: 280 us (920 TFLOP/s); 4096 over 32 pages of 64
 // tokens each: 131 us. Measured and not kept: two threads a row (355 us: twice the votes
-// and barriers); looking for the maximum only where a block's sum is too large (+20); the next block's
+// and barriers); two groups of softmax warps for a tile, a block each in turn (331); looking for the maximum only where a block's sum is too large (+20); the next block's
 // scores asked for before the probabilities are stored (+45: registers); scores and outputs issued
 // by warps of their own (no difference); probabilities stored 64 tokens at a time (286);
 // converted pieces exchanged between lanes against bank conflicts, where lanes by token have none
