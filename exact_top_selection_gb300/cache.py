@@ -35,7 +35,7 @@ HEAD_DIMS = (64, 128)
 CACHE_SYMBOLS = ("exact_topk_cache_write", "exact_topk_cache_read", "exact_topk_block_scores",
                  "exact_topk_make_attention_plan", "exact_topk_attention_run", "exact_topk_set_wait_limit",
                  "exact_topk_cache4_write", "exact_topk_cache4_read", "exact_topk_cache4_block_scores",
-                 "exact_topk_cache4_attention_run", "exact_topk_rotary", "exact_topk_update_tables")
+                 "exact_topk_cache4_make_attention_plan", "exact_topk_cache4_attention_run", "exact_topk_rotary", "exact_topk_update_tables")
 GROUP = 16  # channels that share a scale in 4 bits
 
 
@@ -111,8 +111,8 @@ def _lib():
             getattr(lib, prefix + "_block_scores").argtypes = [cache, batch, i64, i32, rows, i32, i32, p, i64, p, p, p]
             getattr(lib, prefix + "_attention_run").argtypes = [plan, cache, batch, rows, rows, p, ctypes.c_float,
                                                                 p, sz, p, sz, p]
-        lib.exact_topk_make_attention_plan.argtypes = [i64] + [i32] * 9 + [
-            ctypes.POINTER(_etk.DeviceInfo), plan]
+        for name in ("exact_topk_make_attention_plan", "exact_topk_cache4_make_attention_plan"):
+            getattr(lib, name).argtypes = [i64] + [i32] * 9 + [ctypes.POINTER(_etk.DeviceInfo), plan]
         lib.exact_topk_set_wait_limit.argtypes = [i64]
         for name in CACHE_SYMBOLS:
             getattr(lib, name).restype = ctypes.c_int
@@ -204,6 +204,7 @@ class KVCache:
     are used in place and kept alive by this object.
     """
 
+    bits = 8
     _functions = ("exact_topk_cache_write", "exact_topk_cache_read", "exact_topk_block_scores",
                   "exact_topk_attention_run")
 
@@ -263,6 +264,7 @@ class KVCache4:
     two: groups whose largest magnitude lies between 0.1 and 2688 units keep the codes' precision.
     Takes KVCache's place in every call."""
 
+    bits = 4
     _functions = ("exact_topk_cache4_write", "exact_topk_cache4_read", "exact_topk_cache4_block_scores",
                   "exact_topk_cache4_attention_run")
 
@@ -437,16 +439,20 @@ def block_scores(cache, batch, q, keep_first=0, keep_last=0, scores=None, ke=Non
 
 
 def make_attention_plan(num_tokens, num_seqs, q_heads, kv_heads, head_dim, page_size, table_width, num_blocks=0,
-                        single_rows=False, device_info=None, prompt=-1) -> AttentionPlan:
+                        single_rows=False, device_info=None, prompt=-1, bits=8) -> AttentionPlan:
     """The attention's launch plan (pure host logic; needs a DeviceInfo, queried when omitted).
-    prompt: whether the kernel for prompts runs: -1 the planner's choice, 0 no, 1 yes."""
+    prompt: whether the kernel for prompts runs: -1 the planner's choice, 0 no, 1 yes.  bits: of the
+    cache's codes, 8 (KVCache) or 4 (KVCache4)."""
+    if bits not in (4, 8):
+        raise ValueError(f"bits must be 4 or 8, got {bits}")
     if device_info is None:
         device_info = _etk.query_device()
     plan = AttentionPlan()
-    _etk._check(_lib().exact_topk_make_attention_plan(
+    name = "exact_topk_make_attention_plan" if bits == 8 else "exact_topk_cache4_make_attention_plan"
+    _etk._check(getattr(_lib(), name)(
         int(num_tokens), int(num_seqs), int(bool(single_rows)), int(q_heads), int(kv_heads), int(head_dim),
         int(page_size), int(table_width), int(num_blocks), int(prompt), ctypes.byref(device_info), ctypes.byref(plan)),
-        "exact_topk_make_attention_plan")
+        name)
     return plan
 
 
@@ -465,7 +471,7 @@ class CacheAttention:
         with torch.cuda.device(cache.device):
             self.plan = make_attention_plan(num_tokens, num_seqs, q_heads, cache.kv_heads, cache.head_dim,
                                             cache.page_size, table_width, num_blocks,
-                                            single_rows=num_tokens == num_seqs, **overrides)
+                                            single_rows=num_tokens == num_seqs, bits=cache.bits, **overrides)
             self.counters = torch.zeros(max(16, self.plan.counter_bytes), dtype=torch.uint8, device=cache.device)
             self.workspace = torch.empty(max(16, self.plan.workspace_bytes), dtype=torch.uint8,
                                          device=cache.device)

@@ -169,6 +169,78 @@ int block_scores(const Cache* cache, const exact_topk_batch* batch, int64_t num_
   return launch_block_scores(c, b, a, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// The plan of both caches; bits: of a code.
+int make_plan(int64_t num_tokens, int num_seqs, int single_rows, int q_heads, int kv_heads,
+              int head_dim, int page_size, int table_width, int num_blocks, int prompt, int bits,
+              const exact_topk_device_info* info, exact_topk_attention_plan* plan) {
+  if (info == nullptr || plan == nullptr) return EXACT_TOPK_ERR_NULL_POINTER;
+  if (!page_size_ok(page_size) || (head_dim != 64 && head_dim != 128) || kv_heads < 1 ||
+      kv_heads > 1024 || info->sm_count < 1)
+    return EXACT_TOPK_ERR_BAD_CACHE;
+  const int rc = check_batch_shape(num_tokens, num_seqs, single_rows, table_width, page_size);
+  if (rc != EXACT_TOPK_OK) return rc;
+  if (!heads_ok(q_heads, kv_heads) || num_tokens * q_heads > 0x7FFFFFFF)
+    return EXACT_TOPK_ERR_BAD_HEADS;
+  if (num_blocks < 0 || num_blocks > EXACT_TOPK_MAX_K) return EXACT_TOPK_ERR_BAD_K;
+  if (num_blocks > 0 && table_width > EXACT_TOPK_MAX_LISTED_WIDTH) return EXACT_TOPK_ERR_BAD_BATCH;
+  exact_topk_attention_plan p{};
+  p.num_tokens = num_tokens;
+  p.num_seqs = num_seqs;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.head_dim = head_dim;
+  p.page_size = page_size;
+  p.table_width = table_width;
+  p.num_blocks = num_blocks;
+  // Columns of a tile: 8 as a rule, more only where a key head has more query heads. Wider
+  // tiles share pages between tokens, but are fewer and their products and joins longer. Over
+  // listed pages 8 columns were the fastest or within 4% of it from 1 to 256 tokens of a sequence
+  // (8 tokens of 32 sequences x 16 heads over 32 pages: 50 us, 16 columns 58, 32 columns 56; 32
+  // tokens of one: 17, 21 and 30; 256: 44, 53 and 49; 512: 84, 88 and 75). Over the whole cache
+  // 16 columns win once passes of 8 would read 256 MB (65 MB: 20.5 us with 8, 23.3 with 16; 262 MB:
+  // 43.7 and 44.4; 524 MB: 67.2 and 60.3; 2.1 GB: 230 and 161), and 32 lose to them (94 and 170).
+  const int group = q_heads / kv_heads;
+  const int64_t mean = single_rows ? 1 : (num_tokens + num_seqs - 1) / num_seqs;
+  const int64_t passes = (mean * group + 7) / 8;
+  const double read = (double)num_seqs * kv_heads * table_width * page_size * 2 * head_dim *
+                      (double)passes;
+  p.columns = group > 16 ? 32 : (group > 8 ? 16 : 8);
+  if (group <= 8 && num_blocks == 0 && passes > 1 && read >= 256e6) p.columns = 16;
+  p.tile_heads = group < p.columns ? group : p.columns;
+  p.tile_tokens = p.columns / p.tile_heads < 8 ? p.columns / p.tile_heads : 8;
+  if (single_rows) p.tile_tokens = 1;
+  p.workers = info->sm_count * attention_ctas_per_sm(p.columns, head_dim);
+  if (p.workers > most_workers(p.columns, head_dim)) p.workers = most_workers(p.columns, head_dim);
+  // A CTA's four warps take 32 tokens each at a time; with 128 tokens a CTA its part of the join
+  // outweighs its own work (four short sequences: 21.3 us, 17.0 with 256, 18.0 with 512).
+  p.min_units = 256 / page_size;
+  p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;
+  // The prompt's kernel takes 128 rows (tokens x heads) at a time and does not split a tile: it
+  // wants tiles that a sequence fills, and enough of them. Over the whole cache it wins from about
+  // 5000 rows on (16 heads x 256 tokens over 8192: 132 us against 110, 512 tokens: 133 against
+  // 203). Over listed pages it also depends on how many of them neighbours share: 16 heads x 512
+  // tokens over 32 pages of 512 each take 54 us against 84 where most are shared, and 198 against
+  // 84 where none are; 1024 tokens 55 against 138, 2048 tokens without any shared 248 against 288.
+  // In 4 bits its conversions take longer than those of the other kernel, which skips what it does not
+  // need: it wins from 7168 rows on (5120 rows 155 us against 118, 6144 154 and 136, 8192 153 and
+  // 176), and over lists as in 8 bits (8192 rows 60 against 71 where most are shared, 126 against
+  // 71 where none are; 16384 rows 63 and 123 against 116).
+  const int prompt_heads = group < kPromptRows ? group : kPromptRows;
+  const int prompt_tokens =
+      kPromptRows / prompt_heads < kPromptTokens ? kPromptRows / prompt_heads : kPromptTokens;
+  const int64_t prompt_rows = num_blocks > 0 ? 16384 : (bits == 4 ? 7168 : 5120);
+  const bool prompt_fits = num_blocks == 0 || table_width <= kPromptListedWidth;
+  if (prompt > 0 && !prompt_fits) return EXACT_TOPK_ERR_BAD_PLAN;
+  if (prompt > 0 || (prompt < 0 && prompt_fits && !single_rows && mean >= prompt_tokens &&
+                     num_tokens * q_heads >= prompt_rows)) {
+    p.prompt_tokens = prompt_tokens;
+    p.prompt_heads = prompt_heads;
+  }
+  p.workspace_bytes = partial_bytes(p, head_dim) + again_bytes(p, group);
+  *plan = p;
+  return EXACT_TOPK_OK;
+}
+
 float key_unit(const CacheArgs&) { return 1.f; }
 float key_unit(const Cache4Args& c) { return c.k_unit; }
 
@@ -326,68 +398,17 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
                                    int num_blocks, int prompt,
                                    const exact_topk_device_info* info,
                                    exact_topk_attention_plan* plan) {
-  if (info == nullptr || plan == nullptr) return EXACT_TOPK_ERR_NULL_POINTER;
-  if (!page_size_ok(page_size) || (head_dim != 64 && head_dim != 128) || kv_heads < 1 ||
-      kv_heads > 1024 || info->sm_count < 1)
-    return EXACT_TOPK_ERR_BAD_CACHE;
-  const int rc = check_batch_shape(num_tokens, num_seqs, single_rows, table_width, page_size);
-  if (rc != EXACT_TOPK_OK) return rc;
-  if (!heads_ok(q_heads, kv_heads) || num_tokens * q_heads > 0x7FFFFFFF)
-    return EXACT_TOPK_ERR_BAD_HEADS;
-  if (num_blocks < 0 || num_blocks > EXACT_TOPK_MAX_K) return EXACT_TOPK_ERR_BAD_K;
-  if (num_blocks > 0 && table_width > EXACT_TOPK_MAX_LISTED_WIDTH) return EXACT_TOPK_ERR_BAD_BATCH;
-  exact_topk_attention_plan p{};
-  p.num_tokens = num_tokens;
-  p.num_seqs = num_seqs;
-  p.q_heads = q_heads;
-  p.kv_heads = kv_heads;
-  p.head_dim = head_dim;
-  p.page_size = page_size;
-  p.table_width = table_width;
-  p.num_blocks = num_blocks;
-  // Columns of a tile: 8 as a rule, more only where a key head has more query heads. Wider
-  // tiles share pages between tokens, but are fewer and their products and joins longer. Over
-  // listed pages 8 columns were the fastest or within 4% of it from 1 to 256 tokens of a sequence
-  // (8 tokens of 32 sequences x 16 heads over 32 pages: 50 us, 16 columns 58, 32 columns 56; 32
-  // tokens of one: 17, 21 and 30; 256: 44, 53 and 49; 512: 84, 88 and 75). Over the whole cache
-  // 16 columns win once passes of 8 would read 256 MB (65 MB: 20.5 us with 8, 23.3 with 16; 262 MB:
-  // 43.7 and 44.4; 524 MB: 67.2 and 60.3; 2.1 GB: 230 and 161), and 32 lose to them (94 and 170).
-  const int group = q_heads / kv_heads;
-  const int64_t mean = single_rows ? 1 : (num_tokens + num_seqs - 1) / num_seqs;
-  const int64_t passes = (mean * group + 7) / 8;
-  const double read = (double)num_seqs * kv_heads * table_width * page_size * 2 * head_dim *
-                      (double)passes;
-  p.columns = group > 16 ? 32 : (group > 8 ? 16 : 8);
-  if (group <= 8 && num_blocks == 0 && passes > 1 && read >= 256e6) p.columns = 16;
-  p.tile_heads = group < p.columns ? group : p.columns;
-  p.tile_tokens = p.columns / p.tile_heads < 8 ? p.columns / p.tile_heads : 8;
-  if (single_rows) p.tile_tokens = 1;
-  p.workers = info->sm_count * attention_ctas_per_sm(p.columns, head_dim);
-  if (p.workers > most_workers(p.columns, head_dim)) p.workers = most_workers(p.columns, head_dim);
-  // A CTA's four warps take 32 tokens each at a time; with 128 tokens a CTA its part of the join
-  // outweighs its own work (four short sequences: 21.3 us, 17.0 with 256, 18.0 with 512).
-  p.min_units = 256 / page_size;
-  p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;
-  // The prompt's kernel takes 128 rows (tokens x heads) at a time and does not split a tile: it
-  // wants tiles that a sequence fills, and enough of them. Over the whole cache it wins from about
-  // 5000 rows on (16 heads x 256 tokens over 8192: 132 us against 110, 512 tokens: 133 against
-  // 203). Over listed pages it also depends on how many of them neighbours share: 16 heads x 512
-  // tokens over 32 pages of 512 each take 54 us against 84 where most are shared, and 198 against
-  // 84 where none are; 1024 tokens 55 against 138, 2048 tokens without any shared 248 against 288.
-  const int prompt_heads = group < kPromptRows ? group : kPromptRows;
-  const int prompt_tokens =
-      kPromptRows / prompt_heads < kPromptTokens ? kPromptRows / prompt_heads : kPromptTokens;
-  const int64_t prompt_rows = num_blocks > 0 ? 16384 : 5120;
-  const bool prompt_fits = num_blocks == 0 || table_width <= kPromptListedWidth;
-  if (prompt > 0 && !prompt_fits) return EXACT_TOPK_ERR_BAD_PLAN;
-  if (prompt > 0 || (prompt < 0 && prompt_fits && !single_rows && mean >= prompt_tokens &&
-                     num_tokens * q_heads >= prompt_rows)) {
-    p.prompt_tokens = prompt_tokens;
-    p.prompt_heads = prompt_heads;
-  }
-  p.workspace_bytes = partial_bytes(p, head_dim) + again_bytes(p, group);
-  *plan = p;
-  return EXACT_TOPK_OK;
+  return make_plan(num_tokens, num_seqs, single_rows, q_heads, kv_heads, head_dim, page_size,
+                   table_width, num_blocks, prompt, 8, info, plan);
+}
+
+int exact_topk_cache4_make_attention_plan(int64_t num_tokens, int num_seqs, int single_rows,
+                                          int q_heads, int kv_heads, int head_dim, int page_size,
+                                          int table_width, int num_blocks, int prompt,
+                                          const exact_topk_device_info* info,
+                                          exact_topk_attention_plan* plan) {
+  return make_plan(num_tokens, num_seqs, single_rows, q_heads, kv_heads, head_dim, page_size,
+                   table_width, num_blocks, prompt, 4, info, plan);
 }
 
 int exact_topk_attention_run(const exact_topk_attention_plan* plan, const exact_topk_cache* cache,

@@ -253,7 +253,16 @@ int exact_topk_cache4_block_scores(const exact_topk_cache4* cache, const exact_t
                                    int64_t row_pitch, int32_t* ke, int32_t* num_valid_rows,
                                    struct CUstream_st* stream);
 
-/* As exact_topk_attention_run, with the same plan. scale * k_unit must be finite as scale must. */
+/* As exact_topk_make_attention_plan, for exact_topk_cache4_attention_run: the prompt's kernel runs from
+ * more rows on. */
+int exact_topk_cache4_make_attention_plan(int64_t num_tokens, int num_seqs, int single_rows,
+                                          int q_heads, int kv_heads, int head_dim, int page_size,
+                                          int table_width, int num_blocks, int prompt,
+                                          const exact_topk_device_info* info,
+                                          exact_topk_attention_plan* plan);
+
+/* As exact_topk_attention_run; either function's plans will do. scale * k_unit must be finite as
+ * scale must. */
 int exact_topk_cache4_attention_run(const exact_topk_attention_plan* plan,
                                     const exact_topk_cache4* cache, const exact_topk_batch* batch,
                                     const exact_topk_rows* q, const exact_topk_rows* out,

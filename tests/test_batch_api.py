@@ -60,6 +60,18 @@ def test_cache4_entry_points_refuse_bad_arguments():
     check(-7, which=[3], scale=math.nan)
 
 
+@pytest.mark.parametrize("tokens,blocks,four,eight", [(300, 0, False, False), (320, 0, False, True), (447, 0, False, True), (448, 0, True, True),
+                                                      (1023, 32, False, False), (1024, 32, True, True)])
+def test_plans_of_prompts_by_bits(tokens, blocks, four, eight):
+    for bits, prompt in ((4, four), (8, eight)):
+        p = etk.make_attention_plan(tokens, 1, 16, 2, 128, 64, 2048, blocks, False, GB300, bits=bits)
+        assert (p.prompt_tokens > 0) == prompt, bits
+    with pytest.raises(ValueError):
+        etk.make_attention_plan(tokens, 1, 16, 2, 128, 64, 2048, blocks, False, GB300, bits=16)
+    with pytest.raises(etk.ExactTopKError):
+        etk.make_attention_plan(tokens, 1, 15, 2, 128, 64, 2048, blocks, False, GB300, bits=4)
+
+
 def test_rotary_refuses_bad_arguments():
     lib, byref = binding._lib(), ctypes.byref
 
