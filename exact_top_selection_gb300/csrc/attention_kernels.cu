@@ -49,7 +49,8 @@
 // tokens, 3 new ones, 2 x 4 heads of 64 channels (1.06 GB): 209 us. 32 listed pages of 64
 // sequences (134 MB): 34 us. In 4 bits: 238 us (1.35 GB, 5.6 TB/s) for the first, 211 for the second
 // (604 MB), 28 for the third. Steps of 16 tokens took 317 us for the first; a fifth CTA an SM
-// changed nothing there (240) and cost 5 us of the third.
+// changed nothing there (240) and cost 5 us of the third, as asking for all listed pages ahead of their
+// order cost it 3.
 
 #include <climits>
 
