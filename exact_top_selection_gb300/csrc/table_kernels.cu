@@ -155,6 +155,7 @@ __device__ __forceinline__ void plan(const TableArgs& a, const Work& work) {
     if (gridDim.x > 1) {
       __threadfence();
       s_last = atomicAdd(a.arrived, 1) == (int)gridDim.x - 1;
+      if (s_last) __threadfence();  // nothing is written before all have read
     }
   }
   __syncthreads();

@@ -34,7 +34,7 @@ def pair(pages, seqs, width, page, max_tokens, strided=False, head=0):
     return tables, srv.Tables(tables.page_table, tables.kv_len, tables.free_pages, tables.free_range, page, max_tokens)
 
 
-# pages, sequences, table width, page size, most rows: one CTA alone, then two kernels; pools and tables that run out
+# pages, sequences, table width, page size, most rows: one CTA alone, then many; pools and tables that run out
 CASES = [(40, 1, 30, 16, 300), (20, 7, 6, 16, 200), (300, 64, 12, 64, 700), (5000, 300, 40, 32, 20000), (900, 1030, 9, 16, 5000),
          (12000, 4096, 5, 128, 100000), (64, 3, 64, 128, 70), (1, 2, 3, 16, 16), (3000, 20, 400, 16, 60000)]
 
@@ -83,7 +83,7 @@ def test_what_a_call_took_is_given_back():
 
 
 def test_pages_given_back_serve_in_the_same_call():
-    """With nothing free: the pages of a sequence that ends go to one that begins, in one CTA and in two kernels."""
+    """With nothing free: the pages of a sequence that ends go to one that begins, in one CTA and in many."""
     for width, page, max_tokens in ((8, 16, 128), (400, 16, 30000)):
         tables, plain = pair(width, 2, width, page, max_tokens, head=3)
         for change in ([width * page, 0], [-2 ** 31, width * page - 5], [width * page, -2 ** 31], [-page * 3, 2 * page + 1], [0, page]):
