@@ -486,6 +486,40 @@ def test_empty_calls_do_nothing():
     assert (out == MARK).all()
 
 
+def far_rows(x, apart):
+    """x's rows, `apart` numbers from one token to the next."""
+    T, H, D = x.shape
+    wide = torch.empty((T - 1) * apart + H * D, dtype=x.dtype, device="cuda").as_strided((T, H, D), (apart, D, 1))
+    wide.copy_(x)
+    return wide
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_whose_offsets_pass_32_bits(dim):
+    """Every row argument of a step with its last tokens more than 2^32 numbers behind its first."""
+    T, heads, group, page, apart = 40, 2, 4, 16, 1 << 27
+    tensors, batch = srv.make(130, [T + 30], [T], heads, page, dim, BF16, poison=False)
+    plain, cache, b = srv.Cache4(*tensors), device_cache(tensors), device_batch(batch)
+    near = [ref.rows(131 + i, T, h, dim, BF16, 2.0) for i, h in enumerate((heads * group, heads, heads))]
+    q, k, v = (far_rows(x, apart) for x in near)
+    rotary = etk.Rotary(dim, device="cuda")
+    turned = rotary(near[0].cuda(), near[1].cuda(), batch=b)
+    rotary(q, k, batch=b, out=(q, k))
+    assert torch.equal(q, turned[0]) and torch.equal(k, turned[1])
+    etk.cache_write(cache, b, k, v)
+    srv.write(plain, batch, turned[1].cpu(), near[2])
+    check_cache(cache, plain)
+    scores = [etk.block_scores(cache, b, x, scores=torch.full((T * heads, b.table_width), MARK, device="cuda"))[0] for x in (q, turned[0])]
+    assert torch.equal(*scores)
+    want, tol = ref.attention(plain, batch, turned[0].cpu(), None, 1 / math.sqrt(dim), 0.0)
+    out = far_rows(torch.zeros_like(near[0]), apart)
+    for prompt in (0, 1):
+        etk.CacheAttention(cache, 1, T, heads * group, b.table_width, prompt=prompt)(q, b, out=out.fill_(MARK))
+        assert ((out.cpu().double() - want).abs() <= tol).all()
+    for x, y in zip(etk.cache_read(cache, b, out=(k.fill_(MARK), v.fill_(MARK))), ref.read(plain, batch, T)):
+        assert same(x, y)
+
+
 # More tiles of 128 rows than SMs, so that two of them share a CTA: 160, 160, 348, 156, 170 and 510 of them.
 @pytest.mark.parametrize("page,dim,heads,group,dtype", [(16, 64, 10, 8, BF16), (64, 128, 5, 16, FP16), (128, 64, 4, 40, BF16),
                                                         (32, 128, 6, 12, FP16), (64, 128, 10, 9, BF16), (16, 128, 1, 130, BF16)])
