@@ -5,23 +5,29 @@
 // blocks of 64 cached tokens on the fifth-generation tensor cores, a row a thread. There a
 // CTA has one tile, and two CTAs an SM each convert the same codes; with a product by a scale
 // for each pair of codes that conversion is as long as the softmax. Here a CTA has an SM to itself
-// and two tiles, of neighbouring tokens, with a warp each to issue their products, and eight
+// and two tiles, of neighbouring tokens, with two warps each to issue their products, and eight
 // warps convert each block once for both.
 //
 // Scales are part of the FP16 operands (a code times its scale is exact in FP16), units part of the
-// scores' factor and of the outputs. A NaN scale shows as a NaN among a row's sums or outputs; its tile is
-// left to the kernel that runs behind, as is one whose wait ran out.
+// scores' factor and of the outputs. A NaN scale shows as a NaN among a row's sums or outputs; its
+// tile is left to the kernel that runs behind, as is one whose wait ran out.
 //
 // What bounds it: 664 clocks of products for a block and tile (8 of 50, limited by shared memory's
-// reads of both operands, and 4 of 66), so 1328 of the 2150 that a block of both takes, and the
-// softmax warps, two for each scheduler, whose instructions wait for one another. 2048 tokens x 16
-// query heads (2 key heads of 128 channels) over 16384: 280 us (920 TFLOP/s); 4096 over 32 pages of 64
-// tokens each: 131 us. Measured and not kept: two threads a row (355 us: twice the votes
-// and barriers); two groups of softmax warps for a tile, a block each in turn (331); looking for the maximum only where a block's sum is too large (+20); the next block's
-// scores asked for before the probabilities are stored (+45: registers); scores and outputs issued
-// by warps of their own (no difference); probabilities stored 64 tokens at a time (286);
-// converted pieces exchanged between lanes against bank conflicts, where lanes by token have none
-// (301).
+// reads of both operands, and 4 of 66), so 1328 of the 1980 that a block of both takes, and the
+// chain of a tile's probabilities, outputs and scores of the block after the next, which take the
+// probabilities' place: tensor memory has no room for scores that would not wait. 2048 tokens x 16
+// query heads (2 key heads of 128 channels) over 16384: 267 us (965 TFLOP/s); 4096 over 32 pages of
+// 64 tokens each: 122 us. With a warp a tile for both kinds of products it took 274 us, and with 32
+// scores loaded at a time, none of them while others are weighed, 280.
+//
+// Measured and not kept: two threads a row (twice the votes and barriers); two groups of softmax
+// warps for a tile, a block each in turn; the next block's scores waited for while this one's are
+// weighed (+40: they are late as a rule); the maximum looked for only where a block's sum is too
+// large (+20); an arrival for each warp instead of each thread (+6); waits that poll without a pause
+// (+4); probabilities stored 64 tokens at a time (+7); converted pieces exchanged between lanes
+// against bank conflicts, where lanes by token have none (+22); the line of all tiles' blocks cut
+// evenly over the SMs, of which 128 CTAs leave 24 idle: to begin and to join parts of tiles, and
+// the registers for it, cost more than the 16% (290, over lists 168).
 
 #include "cache_device.cuh"
 #include "prompt_device.cuh"
@@ -34,7 +40,7 @@ constexpr int kRows = 128;                       // of a tile
 constexpr int kConvert = 128;                    // threads for keys, and as many for values
 constexpr int kSoftmaxWarps = kTiles * kRows / 32;
 constexpr int kConvertWarps = 2 * kConvert / 32;
-constexpr int kWarps = kSoftmaxWarps + kConvertWarps + kTiles;
+constexpr int kWarps = kSoftmaxWarps + kConvertWarps + 2 * kTiles;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBlock = 64;                       // cached tokens of a block
 constexpr int kEntries = 128;                    // parts of pages held at a time
@@ -48,6 +54,10 @@ __device__ __forceinline__ void tensor_store16(uint32_t address, const uint32_t 
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
       "r"(address)
       : "memory");
+}
+
+// Stores issued so far are complete.
+__device__ __forceinline__ void tensor_stored() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
@@ -66,7 +76,7 @@ struct Shared {
   Entry entry[kEntries];
   float factor[kTiles * kRows];
   uint64_t k_full[2], k_free[2], v_full[2], v_free[2];
-  uint64_t scored[kTiles][2], weighed[kTiles][2], added[kTiles][2], drained[kTiles];
+  uint64_t scored[kTiles][2], weighed[kTiles][2], added[kTiles][2], drained[2 * kTiles];
   uint32_t tensor;
   int scan[kWarps];
   int failed, again;
@@ -115,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         barrier_init(&sm.added[t][i], 1);
       }
     }
-    for (int t = 0; t < kTiles; ++t) barrier_init(&sm.drained[t], 1);
+    for (int t = 0; t < 2 * kTiles; ++t) barrier_init(&sm.drained[t], 1);
     sm.failed = 0;
     sm.again = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -126,6 +136,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                  "r"(kTensorColumns)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+
+  // ---- queries: 8 channels a lane, all of a warp's 16 rows on their way ----
+  constexpr int kLanes = D / 8, kStepRows = 32 / kLanes;  // lanes of a row, rows of a step
+  constexpr int kSteps = 16 / kStepRows;
+  const bool loads = warp < kTiles * kRows / 16;
+  const int chunk = lane % kLanes, loads_tile = warp / (kRows / 16);
+  const int first_row = warp * 16 % kRows + lane / kLanes;  // in its tile
+  uint32_t there = 0u;  // steps whose row has a token
+  uint4 w[kSteps];
+  if (loads) {
+    int token = first_row / heads, in_token = first_row - token * heads;
+    const uint16_t* const from =
+        static_cast<const uint16_t*>(a.q.data) +
+        (row0 + loads_tile * a.prompt_tokens) * a.q.token_stride +
+        ((int64_t)head * a.group + head0) * a.q.head_stride + chunk * 8;
+    const int have = tokens - loads_tile * a.prompt_tokens;
+    const int some = have < a.prompt_tokens ? have : a.prompt_tokens;
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      w[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (token < some) {
+        there |= 1u << k;
+        w[k] = __ldg(reinterpret_cast<const uint4*>(from + token * a.q.token_stride +
+                                                    in_token * a.q.head_stride));
+      }
+      in_token += kStepRows;
+      while (in_token >= heads) {
+        in_token -= heads;
+        ++token;
+      }
+    }
   }
 
   // ---- pages of a list: which tokens of the tiles take each ----
@@ -142,31 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
 
-  // ---- queries: 8 channels a lane, all of a warp's 16 rows on their way ----
-  if (warp < kTiles * kRows / 16) {
-    constexpr int kLanes = D / 8, kStepRows = 32 / kLanes;  // lanes of a row, rows of a step
-    constexpr int kSteps = 16 / kStepRows;
-    const int chunk = lane % kLanes;
-    const auto token_of = [&](int row) {  // in the CTA; -1 for a row without one
-      const int in_tile = (row & (kRows - 1)) / heads;
-      const int token = (row / kRows) * a.prompt_tokens + in_tile;
-      return in_tile < a.prompt_tokens && token < tokens ? token : -1;
-    };
-    uint4 w[kSteps];
+  if (loads) {
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
-      const int row = (warp * kSteps + k) * kStepRows + lane / kLanes;
-      const int token = token_of(row);
-      w[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (token >= 0)
-        w[k] = __ldg(reinterpret_cast<const uint4*>(
-            static_cast<const uint16_t*>(a.q.data) + (row0 + token) * a.q.token_stride +
-            ((int64_t)head * a.group + head0 + (row & (kRows - 1)) % heads) * a.q.head_stride +
-            chunk * 8));
-    }
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int row = (warp * kSteps + k) * kStepRows + lane / kLanes;
       const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
       float2 x[4];
       float top = 0.f;
@@ -189,13 +209,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         x[i].x *= by;
         x[i].y *= by;
       }
-      const int in_tile = row & (kRows - 1);
-      *reinterpret_cast<uint4*>(&sm.q[row / kRows][chunk / 8]
+      const int in_tile = first_row + k * kStepRows;
+      *reinterpret_cast<uint4*>(&sm.q[loads_tile][chunk / 8]
                                      [in_tile * 128 + (((chunk & 7) ^ (in_tile & 7)) << 4)]) =
           make_uint4(pack2<true>(x[0].x, x[0].y), pack2<true>(x[1].x, x[1].y),
                      pack2<true>(x[2].x, x[2].y), pack2<true>(x[3].x, x[3].y));
       if (chunk == 0)
-        sm.factor[row] = token_of(row) >= 0
+        sm.factor[loads_tile * kRows + in_tile] = (there >> k & 1u) != 0u
                              ? __uint_as_float((uint32_t)(127 - up) << 23) * fabsf(a.scale_log2)
                              : 0.f;
     }
@@ -238,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int row_token = tile * a.prompt_tokens + row / heads;
   const bool live = warp < kSoftmaxWarps && row / heads < a.prompt_tokens && row_token < tokens;
   const int row_pos = live ? pos0 + row_token : -1;
-  const uint32_t row_bit = live ? 1u << row_token : 0u;
+  const uint32_t row_bit = live ? 1u << (row_token & 31) : 0u;  // without lists any bit does
   const float row_factor = warp < kSoftmaxWarps ? sm.factor[tid] : 0.f;
   const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t outputs = tensor + tile * 128, scores_at = tensor + kS + tile * 2 * kBlock;
@@ -271,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto scale_probabilities = [&](uint32_t at, float by) {
     float v[16];
     uint32_t w[16];
+    tensor_stored();
     tensor_load16(at, v);
     tensor_wait(v);
 #pragma unroll
@@ -326,11 +347,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- softmax: a row a thread ----
       for (int block = 0; block < blocks && tile < tiles; ++block) {
         const int n = done + block;
-        ok = ok && barrier_wait(&sm.scored[tile][n & 1], (n >> 1) & 1, failed);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t from = scores_at + lane_base + (n & 1) * kBlock;
         // A part that this row does not take, and tokens behind its own, have probability 0: an
         // offset of -inf does it for whole parts.
         constexpr int kParts = 1 << kPartShift;
@@ -344,60 +360,71 @@ __global__ void __launch_bounds__(kThreads, 1)
           cuts |= takes && seen[k] < 1 << part_tokens_shift;
         }
         cuts = __any_sync(~0u, cuts);
+        ok = ok && barrier_wait(&sm.scored[tile][n & 1], (n >> 1) & 1, failed);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t from = scores_at + lane_base + (n & 1) * kBlock;
         // Probabilities under the running maximum, 32 tokens at a time. They take the place of
         // scores that have been read. Where a score turns out too far above the maximum, that is
         // raised by a whole number and the 32 are done again: it is seldom.
         float by = 1.f;
         bool some = false;
+        float s[2][16];
+        uint32_t p[16];
+        float high = 0.f, base = 0.f;
+        float2 sum = make_float2(0.f, 0.f);
+        // 16 tokens: the first or second half of p
+        const auto weigh = [&](const float (&x)[16], int group) {
+          constexpr int kPartGroups = 4 >> kPartShift;  // 16 tokens of a part
+          const int part = group / kPartGroups;
+          const float offset = seen[part] > 0 ? -base : -infinity();
+          float2 y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            y[i] = fma2(make_float2(x[2 * i], x[2 * i + 1]), row_factor, offset);
+          if (cuts) {
+            const int left = seen[part] - group % kPartGroups * 16;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              y[i].x = 2 * i < left ? y[i].x : -infinity();
+              y[i].y = 2 * i + 1 < left ? y[i].y : -infinity();
+            }
+          }
+          const float high0 =
+              max3(max3(y[0].x, y[0].y, y[1].x), y[1].y, max3(y[2].x, y[2].y, y[3].x));
+          const float high1 =
+              max3(max3(y[3].y, y[4].x, y[4].y), y[5].x, max3(y[5].y, y[6].x, y[6].y));
+          high = max3(high, max3(high0, y[7].x, y[7].y), high1);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y[i].x = exp2_fast(y[i].x);
+            y[i].y = exp2_fast(y[i].y);
+          }
+          const float2 sum0 = add2(add2(y[0], y[1]), add2(y[2], y[3]));
+          const float2 sum1 = add2(add2(y[4], y[5]), add2(y[6], y[7]));
+          sum = add2(sum, add2(sum0, sum1));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) p[group % 2 * 8 + i] = pack2<true>(y[i].x, y[i].y);
+        };
+        const auto begin = [&] {
+          base = m == -infinity() ? 0.f : m;
+          high = -infinity();
+          sum = make_float2(0.f, 0.f);
+        };
+        tensor_load16(from, s[0]);
+        tensor_wait(s[0]);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          uint32_t p[16];
-          float2 sum;
-          for (int attempt = 0; attempt < 2; ++attempt) {
-            const float base = m == -infinity() ? 0.f : m;
-            float high = -infinity();
-            sum = make_float2(0.f, 0.f);
-            float s[2][16];
-            tensor_load16(from + half * 32, s[0]);
-            tensor_load16(from + half * 32 + 16, s[1]);
-            tensor_wait(s[0]);
-            tensor_wait(s[1]);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              constexpr int kPartGroups = 4 >> kPartShift;  // 16 tokens of a part
-              const int group = half * 2 + k, part = group / kPartGroups;
-              const float(&x)[16] = s[k];
-              const float offset = seen[part] > 0 ? -base : -infinity();
-              float2 y[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                y[i] = fma2(make_float2(x[2 * i], x[2 * i + 1]), row_factor, offset);
-              if (cuts) {
-                const int left = seen[part] - group % kPartGroups * 16;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  y[i].x = 2 * i < left ? y[i].x : -infinity();
-                  y[i].y = 2 * i + 1 < left ? y[i].y : -infinity();
-                }
-              }
-              const float high0 =
-                  max3(max3(y[0].x, y[0].y, y[1].x), y[1].y, max3(y[2].x, y[2].y, y[3].x));
-              const float high1 =
-                  max3(max3(y[3].y, y[4].x, y[4].y), y[5].x, max3(y[5].y, y[6].x, y[6].y));
-              high = max3(high, max3(high0, y[7].x, y[7].y), high1);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                y[i].x = exp2_fast(y[i].x);
-                y[i].y = exp2_fast(y[i].y);
-              }
-              const float2 sum0 = add2(add2(y[0], y[1]), add2(y[2], y[3]));
-              const float2 sum1 = add2(add2(y[4], y[5]), add2(y[6], y[7]));
-              sum = add2(sum, add2(sum0, sum1));
-#pragma unroll
-              for (int i = 0; i < 8; ++i) p[k * 8 + i] = pack2<true>(y[i].x, y[i].y);
-            }
-            const bool raise = high > (m == -infinity() ? m : kMost);
-            if (!__any_sync(~0u, raise)) break;
+          // each 16 are on their way while those before them are weighed
+          begin();
+          tensor_load16(from + half * 32 + 16, s[1]);
+          weigh(s[0], half * 2);
+          tensor_wait(s[1]);
+          if (half == 0) tensor_load16(from + 32, s[0]);
+          weigh(s[1], half * 2 + 1);
+          const bool raise = high > (m == -infinity() ? m : kMost);
+          if (__any_sync(~0u, raise)) {
             some = true;
             float less = 1.f;
             if (raise) {
@@ -413,10 +440,20 @@ __global__ void __launch_bounds__(kThreads, 1)
               by *= less;
             }
             if (half > 0) scale_probabilities(from, less);
+            begin();
+            float again[16];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              tensor_load16(from + half * 32 + k * 16, again);
+              tensor_wait(again);
+              weigh(again, half * 2 + k);
+            }
           }
           l += sum.x + sum.y;
+          if (half == 0) tensor_wait(s[0]);
           tensor_store16(from + half * 16, p);
         }
+        tensor_stored();
         if (some && n > 0) {  // O is in place up to the block before
           ok = was_added(n - 1);
           ok = __all_sync(~0u, ok);
@@ -515,56 +552,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         load(block + 1);
       }
     } else if (tile < tiles) {
-      // ---- products, a warp for each tile ----
+      // ---- products, of scores and of outputs: a warp for each tile ----
       // The waits for operands are the ones whose limit the host sets: once one has run out, the
       // others give up as well.
       const bool leader = elected();
-      constexpr uint32_t kScores = 1u << 4 | (kBlock / 8) << 17 | (kRows / 16) << 24;
-      constexpr uint32_t kOutputs = 1u << 4 | 1u << 16 | (D / 8) << 17 | (kRows / 16) << 24;
-      const auto scores = [&](int block) {
-        const int n = done + block, buffer = n & 1;
-        ok = ok && barrier_wait(&sm.k_full[buffer], (n >> 1) & 1, failed, wait_limit);
-        // the P that these scores replace has been used; a chunk's first block waits for all
-        const int used = block == 0 ? n - 1 : n - 2;
-        if (used >= 0) ok = ok && was_added(used);
-        ok = __all_sync(~0u, ok);
-        if (!ok) return;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (leader) {
+      if (warp < kWarps - kTiles) {
+        constexpr uint32_t kScores = 1u << 4 | (kBlock / 8) << 17 | (kRows / 16) << 24;
+        constexpr int kLine = kBlock * 128 / 16;  // a line's place in an operand's
+        const uint64_t q = operand(shared_address(sm.q[tile][0]));
+        const uint64_t k0 = operand(shared_address(sm.k[0][0]));
+        for (int block = 0; block < blocks; ++block) {
+          const int n = done + block, buffer = n & 1;
+          ok = ok && barrier_wait(&sm.k_full[buffer], (n >> 1) & 1, failed, wait_limit);
+          if (n >= 2) ok = ok && was_added(n - 2);  // the P that these scores replace has been used
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (leader) {
+            const uint64_t k = k0 + buffer * (kLines * kLine);
 #pragma unroll
-          for (int line = 0; line < kLines; ++line) {
-            const uint64_t q = operand(shared_address(sm.q[tile][line]));
-            const uint64_t k = operand(shared_address(sm.k[buffer][line]));
+            for (int line = 0; line < kLines; ++line)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              tensor_mma(scores_at + buffer * kBlock, q + 2 * i, k + 2 * i, kScores,
-                         line > 0 || i > 0);
+              for (int i = 0; i < 4; ++i)
+                tensor_mma(scores_at + buffer * kBlock, q + line * (kRows * 128 / 16) + 2 * i,
+                           k + line * kLine + 2 * i, kScores, line > 0 || i > 0);
+            tensor_commit(&sm.scored[tile][buffer]);
+            tensor_commit(&sm.k_free[buffer]);
           }
-          tensor_commit(&sm.k_free[buffer]);
-          tensor_commit(&sm.scored[tile][buffer]);
+          __syncwarp();
         }
-        __syncwarp();
-      };
-      scores(0);
-      if (blocks > 1) scores(1);
-      for (int block = 0; block < blocks && ok; ++block) {
-        const int n = done + block, buffer = n & 1;
-        ok = barrier_wait(&sm.v_full[buffer], (n >> 1) & 1, failed, wait_limit);
-        ok = ok && barrier_wait(&sm.weighed[tile][buffer], (n >> 1) & 1, failed);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (leader) {
-          const uint64_t v = operand_across(shared_address(sm.v[buffer][0]), kBlock * 128);
+      } else {
+        constexpr uint32_t kOutputs = 1u << 4 | 1u << 16 | (D / 8) << 17 | (kRows / 16) << 24;
+        const uint64_t v0 = operand_across(shared_address(sm.v[0][0]), kBlock * 128);
+        for (int block = 0; block < blocks; ++block) {
+          const int n = done + block, buffer = n & 1;
+          ok = ok && barrier_wait(&sm.v_full[buffer], (n >> 1) & 1, failed, wait_limit);
+          ok = ok && barrier_wait(&sm.weighed[tile][buffer], (n >> 1) & 1, failed);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          if (leader) {
+            const uint64_t v = v0 + buffer * (kLines * kBlock * 128 / 16);
 #pragma unroll
-          for (int k = 0; k < kBlock / 16; ++k)  // 16 tokens: 8 columns of P, 2 KB of V
-            tensor_mma_from(outputs, scores_at + buffer * kBlock + 8 * k, v + 128 * k, kOutputs,
-                            n > 0 || k > 0);
-          tensor_commit(&sm.v_free[buffer]);
-          tensor_commit(&sm.added[tile][buffer]);
+            for (int k = 0; k < kBlock / 16; ++k)  // 16 tokens: 8 columns of P, 2 KB of V
+              tensor_mma_from(outputs, scores_at + buffer * kBlock + 8 * k, v + 128 * k, kOutputs,
+                              n > 0 || k > 0);
+            tensor_commit(&sm.added[tile][buffer]);
+            tensor_commit(&sm.v_free[buffer]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        if (block + 2 < blocks) scores(block + 2);
       }
     }
     __syncwarp();
@@ -612,9 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoftmaxWarps + kConvertWarps) {
     // what was issued ends before the shared memory and the tensor memory go
     int none = 0;
-    if (elected()) tensor_commit(&sm.drained[tile]);
+    uint64_t* const drained = &sm.drained[warp - (kSoftmaxWarps + kConvertWarps)];
+    if (elected()) tensor_commit(drained);
     __syncwarp();
-    barrier_wait(&sm.drained[tile], 0, &none);
+    barrier_wait(drained, 0, &none);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
