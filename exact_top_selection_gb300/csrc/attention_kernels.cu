@@ -1261,14 +1261,17 @@ int launch_attention(const CacheArgs& c, const BatchArgs& b, const AttentionArgs
 int launch_attention4(const Cache4Args& c, const BatchArgs& b, const AttentionArgs& a,
                       cudaStream_t stream) {
   if (a.prompt_tokens > 0) {
-    // Two tiles a CTA where there are more tiles than SMs: 16 heads x 1536 tokens (192 tiles) over
-    // 8192 take 158 us against 182 with a tile a CTA, over lists 68 against 72; 1024 tokens (128
-    // tiles) 156 against 154, and over lists 70 against 63.
-    const int64_t tiles = b.num_tokens / a.prompt_tokens * c.heads *
+    // Two tiles a CTA: 16 heads x 448 to 1536 tokens over 8192 take 128 us against 157 with a tile
+    // a CTA, over lists 51 against 56; 64 sequences of 16 tokens (a tile each) over 4096 63 against
+    // 103. Not where sequences have a tile each and those are more than the SMs: 256 of them take 290
+    // against 237, since two CTAs of the other kernel share an SM. Lists: a bit for each token.
+    const int64_t mean = (b.num_tokens + b.num_seqs - 1) / b.num_seqs;
+    const int64_t tiles = (int64_t)b.num_seqs * c.heads *
                           ((a.group + a.prompt_heads - 1) / a.prompt_heads);
-    const bool pair = a.prompt_tokens * 2 <= kPromptTokens &&
-                      tiles > a.workers / attention_ctas_per_sm(a.columns, c.dim) &&
-                      (a.blocks == nullptr || b.width <= kPairListedWidth);
+    const bool apart = mean <= a.prompt_tokens &&
+                       tiles > a.workers / attention_ctas_per_sm(a.columns, c.dim);
+    const bool pair = !apart && (a.blocks == nullptr || (a.prompt_tokens * 2 <= kPromptTokens &&
+                                                         b.width <= kPairListedWidth));
     const int rc = pair ? launch_prompt_pair(c, b, a, stream)
                         : launch_prompt_attention4(c, b, a, stream);
     if (rc != EXACT_TOPK_OK) return rc;

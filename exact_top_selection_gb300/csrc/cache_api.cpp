@@ -221,14 +221,13 @@ int make_plan(int64_t num_tokens, int num_seqs, int single_rows, int q_heads, in
   // 203). Over listed pages it also depends on how many of them neighbours share: 16 heads x 512
   // tokens over 32 pages of 512 each take 54 us against 84 where most are shared, and 198 against
   // 84 where none are; 1024 tokens 55 against 138, 2048 tokens without any shared 248 against 288.
-  // In 4 bits its conversions take longer than those of the other kernel, which skips what it does not
-  // need: it wins from 7168 rows on (5120 rows 155 us against 118, 6144 154 and 136, 8192 153 and
-  // 176), and over lists as in 8 bits (8192 rows 60 against 71 where most are shared, 126 against
-  // 71 where none are; 16384 rows 63 and 123 against 116).
+  // In 4 bits it wins from 6144 rows on (5120 rows 129 us against 116, 5632 129 and 126, 6144 128 and
+  // 135), and over lists as in 8 bits (8192 rows 52 against 68 where most are shared, 132 against
+  // 67 where none are; 16384 rows 51 and 132 against 109).
   const int prompt_heads = group < kPromptRows ? group : kPromptRows;
   const int prompt_tokens =
       kPromptRows / prompt_heads < kPromptTokens ? kPromptRows / prompt_heads : kPromptTokens;
-  const int64_t prompt_rows = num_blocks > 0 ? 16384 : (bits == 4 ? 7168 : 5120);
+  const int64_t prompt_rows = num_blocks > 0 ? 16384 : (bits == 4 ? 6144 : 5120);
   const bool prompt_fits = num_blocks == 0 || table_width <= kPromptListedWidth;
   if (prompt > 0 && !prompt_fits) return EXACT_TOPK_ERR_BAD_PLAN;
   if (prompt > 0 || (prompt < 0 && prompt_fits && !single_rows && mean >= prompt_tokens &&

@@ -60,7 +60,7 @@ def test_cache4_entry_points_refuse_bad_arguments():
     check(-7, which=[3], scale=math.nan)
 
 
-@pytest.mark.parametrize("tokens,blocks,four,eight", [(300, 0, False, False), (320, 0, False, True), (447, 0, False, True), (448, 0, True, True),
+@pytest.mark.parametrize("tokens,blocks,four,eight", [(300, 0, False, False), (320, 0, False, True), (383, 0, False, True), (384, 0, True, True),
                                                       (1023, 32, False, False), (1024, 32, True, True)])
 def test_plans_of_prompts_by_bits(tokens, blocks, four, eight):
     for bits, prompt in ((4, four), (8, eight)):

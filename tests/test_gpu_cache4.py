@@ -520,9 +520,11 @@ def test_rows_whose_offsets_pass_32_bits(dim):
         assert same(x, y)
 
 
-# More tiles of 128 rows than SMs, so that two of them share a CTA: 160, 160, 348, 156, 170 and 510 of them.
+# Two tiles of 128 rows share a CTA, more of them than SMs: 160, 160, 348, 156, 170 and 510 tiles; small groups over the whole
+# cache alone.
 @pytest.mark.parametrize("page,dim,heads,group,dtype", [(16, 64, 10, 8, BF16), (64, 128, 5, 16, FP16), (128, 64, 4, 40, BF16),
-                                                        (32, 128, 6, 12, FP16), (64, 128, 10, 9, BF16), (16, 128, 1, 130, BF16)])
+                                                        (32, 128, 6, 12, FP16), (64, 128, 10, 9, BF16), (16, 128, 1, 130, BF16),
+                                                        (64, 128, 16, 2, BF16), (32, 64, 9, 5, FP16)])
 @pytest.mark.parametrize("listed", [False, True])
 def test_two_tiles_a_cta(page, dim, heads, group, dtype, listed):
     """Sequences that end in a tile's first tokens, in its second half and in a first tile alone; NaN scales; waits that run out."""
@@ -553,6 +555,31 @@ def test_two_tiles_a_cta(page, dim, heads, group, dtype, listed):
             bad = ((got - want).abs() > tol) & fine
             assert not bad.any(), (limit, bad.nonzero()[:4].tolist(), got[bad][:4].tolist(), want[bad][:4].tolist())
             assert not attend.counters.any()
+
+
+@pytest.mark.parametrize("page,dim,dtype", [(64, 128, BF16), (16, 64, FP16)])
+def test_more_sequences_of_a_tile_than_sms(page, dim, dtype):
+    """A tile a CTA: 100 sequences of up to 16 tokens, two heads; NaN scales; waits that run out."""
+    g = torch.Generator().manual_seed(130)
+    new = torch.randint(1, 17, (100,), generator=g).tolist()
+    lens = [n + int(torch.randint(0, 200, (1,), generator=g)) for n in new]
+    tensors, batch = srv.make(131, lens, new, 2, page, dim, dtype)
+    tensors[3].view(torch.uint8)[batch[0][3, 0].long(), 1, 0, 1] = 0x7F
+    q = ref.rows(132, sum(new), 16, dim, dtype, 3.0)
+    want, tol = srv.attention(srv.Cache4(*tensors), batch, q, None, 1 / math.sqrt(dim), MARK)
+    cache, b = device_cache(tensors), device_batch(batch)
+    attend = etk.CacheAttention(cache, 100, sum(new), 16, b.table_width, prompt=1)
+    lib = binding._lib()
+    for limit in (-1, 0, -1):
+        out = torch.full(q.shape, MARK, dtype=dtype, device="cuda")
+        try:
+            assert lib.exact_topk_set_wait_limit(limit) == 0
+            attend(q.cuda(), b, out=out)
+        finally:
+            assert lib.exact_topk_set_wait_limit(-1) == 0
+        got = out.cpu().double()
+        assert torch.equal(got.isnan(), want.isnan()) and want.isnan().any()
+        assert ((got - want).abs() <= tol)[~want.isnan()].all() and not attend.counters.any()
 
 
 def test_two_tiles_a_cta_over_long_caches():
