@@ -60,7 +60,11 @@ def _lib():
 
 
 def _apart(a, b, name):
-    """Rows a and b share no memory. Both may be slices of one wider tensor of tokens."""
+    """Rows a and b share no memory. Both may be slices of one wider tensor of tokens, or of one wider tensor of heads.
+
+    By residues: modulo p, dimensions whose stride is a multiple of p fall together, and an array's bytes lie in one run,
+    as long as its other dimensions span. Runs that are apart are apart in memory too. Each stride is tried as p;
+    those of dimensions of one element mean nothing."""
     if a.is_contiguous() and b.is_contiguous():
         a0, b0 = a.data_ptr(), b.data_ptr()
         if a0 >= b0 + b.nbytes or b0 >= a0 + a.nbytes:
@@ -69,16 +73,12 @@ def _apart(a, b, name):
     if a0 >= b1 or b0 >= a1 or a.numel() == 0 or b.numel() == 0:
         return
     size = a.element_size()
-    token, head = a.stride(0) * size, a.stride(1) * size
-    if a.stride(0) == b.stride(0) and token > 0 and a.shape[0] > 1 and b.shape[0] > 1:
-        (c0, c1), (d0, d1) = _cache._span(a[0]), _cache._span(b[0])
-        at = (d0 - c0) % token  # of b's token behind the start of one of a's
-        if at >= c1 - c0 and at + (d1 - d0) <= token:
+    steps = [[(n - 1, s * size) for n, s in zip(t.shape[:2], t.stride()[:2]) if n > 1] for t in (a, b)]
+    for p in {s for step in steps for _, s in step if s > 0}:
+        run, other = (t.shape[2] * size + sum(n * s for n, s in step if s % p) for t, step in zip((a, b), steps))
+        at = (b0 - a0) % p  # of b's run behind the start of one of a's
+        if at >= run and at + other <= p:
             return
-        if a.stride(1) == b.stride(1) and head > 0 and token % head == 0:
-            at = (b.data_ptr() - a.data_ptr()) % head  # the same of heads
-            if at >= a.shape[2] * size and at + b.shape[2] * size <= head:
-                return
     raise ValueError(f"{name} must not share memory with another row argument")
 
 

@@ -164,6 +164,55 @@ def test_rows_that_interleave_are_apart():
             binding._apart(a, b, "out")
 
 
+def test_rows_of_one_token_or_head_that_interleave_are_apart():
+    """Heads of one projection in turn ([tokens, heads, 3, dim]) and channels side by side, by tokens and by heads, one of either among them."""
+    for tokens in (1, 2, 5):
+        for heads in (1, 2, 4):
+            x = torch.zeros(tokens, heads, 3, 64, dtype=torch.bfloat16)
+            for i, j in ((0, 1), (1, 0), (0, 2), (2, 1)):
+                binding._apart(x[:, :, i], x[:, :, j], "out")
+            wide = torch.zeros(tokens, heads, 128, dtype=torch.bfloat16)
+            binding._apart(wide[..., :64], wide[..., 64:], "out")
+            binding._apart(wide[..., 64:], wide[..., :64], "out")
+            rows = torch.zeros(tokens, 2 * heads + 1, 64, dtype=torch.bfloat16)
+            binding._apart(rows[:, :2 * heads], rows[:, 2 * heads:], "out")
+            binding._apart(rows[:, 2 * heads:], rows[:, :2 * heads], "out")
+            for a, b in ((x[:, :, 1], x[:, :, 1]), (wide[..., :72], wide[..., 64:]), (wide[..., 64:], wide[..., :72]), (rows[:, :heads + 1], rows[:, heads:])):
+                with pytest.raises(ValueError):
+                    binding._apart(a, b, "out")
+    x = torch.zeros(1, 9, 64, dtype=torch.bfloat16)  # a head each of one array between those of the other, and one beside them
+    binding._apart(x[:, ::3], x[:, 1::3], "out")
+    binding._apart(x[:, ::3], x[:, 4:5], "out")
+    for a, b in ((x[:, ::3], x[:, 1:]), (x[:, ::3], x[:, 3:4]), (x[:, ::2], x[:, 1::3])):
+        with pytest.raises(ValueError):
+            binding._apart(a, b, "out")
+
+
+def test_rows_that_are_taken_for_apart_share_no_element():
+    """Random slices of one buffer: where the check passes, no element is in both."""
+    g = torch.Generator().manual_seed(1)
+
+    def pick(lo, hi):
+        return int(torch.randint(lo, hi + 1, (1,), generator=g))
+
+    passed = 0
+    for _ in range(4000):
+        x = torch.arange(pick(1, 4) * 240, dtype=torch.int32)
+        both = []
+        for _ in range(2):
+            shape = pick(1, 3), pick(1, 3), pick(1, 3) * 4
+            strides = pick(0, 12) * 8, pick(0, 12) * 8, 1
+            most = sum((n - 1) * s for n, s in zip(shape, strides)) + 1
+            both.append(x.as_strided(shape, strides, pick(0, (x.numel() - most) // 4) * 4) if most <= x.numel() else x.view(-1, 3, 80)[:, :1])
+        try:
+            binding._apart(*both, "out")
+        except ValueError:
+            continue
+        passed += 1
+        assert not set(both[0].flatten().tolist()) & set(both[1].flatten().tolist())
+    assert passed > 1000
+
+
 # ---- the 64-bit forms ----
 
 def test_reference_values_and_rounding():

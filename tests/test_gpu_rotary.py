@@ -199,3 +199,16 @@ def test_empty_calls_and_overlaps():
         with pytest.raises(ValueError):
             rotary(q, k, positions=positions, out=out)
     rotary(x[:4, :2], x[:4, 2:], positions=positions, out=(x[:4, :2], x[4:, 1:3]))
+
+
+@pytest.mark.parametrize("T", [1, 2])
+def test_in_place_on_heads_that_interleave(T):
+    """Queries, keys and values of a projection [tokens, heads, 3, channels], turned in place: a single token, as a batch of one decodes."""
+    x = ref.rows(10, T, 12, 64, BF16).view(T, 4, 3, 64)
+    wide = x.cuda()
+    rotary = etk.Rotary(64, device="cuda")
+    positions = torch.arange(7, 7 + T, dtype=torch.int32, device="cuda")
+    rotary(wide[:, :, 0], wide[:, :, 1], positions=positions, out=(wide[:, :, 0], wide[:, :, 1]))
+    for i in range(2):
+        close(wide[:, :, i], *srv.rotary(x[:, :, i], range(7, 7 + T), rotary.frequencies, 1.0, False, MARK))
+    assert torch.equal(wide[:, :, 2].cpu(), x[:, :, 2])
