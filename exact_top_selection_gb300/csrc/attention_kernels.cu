@@ -859,10 +859,13 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
 #pragma unroll
           for (int r = 0; r < 4 * ST; ++r) high = fmaxf(high, y[r]);
           if (__any_sync(~0u, high > kMost)) {
-            if constexpr (kBits == 4) {  // the scores themselves are needed here alone
+            if constexpr (kBits == 4) {
+              // The scores themselves are needed here alone. -inf is a masked score or, of an infinite
+              // query, a sum whose sign the factor has yet to give.
 #pragma unroll
               for (int r = 0; r < 4 * ST; ++r)
-                if (x[n][r] != -infinity()) x[n][r] *= r & 1 ? fy : fx;
+                if (!masked || (seen[r >> 2] >> (n * 4 + (r & 3)) & 1u) != 0u)
+                  x[n][r] *= r & 1 ? fy : fx;
             }
             float by[2];
 #pragma unroll

@@ -297,6 +297,26 @@ def test_nan_reaches_the_rows_that_see_it_and_no_other(page, dim, group):
 
 
 @pytest.mark.parametrize("prompt", [0, 1])
+@pytest.mark.parametrize("page,dim,group,dtype", [(64, 128, 4, BF16), (16, 128, 12, FP16), (16, 64, 3, BF16), (32, 64, 20, FP16)])
+def test_infinite_queries_under_every_sign_of_the_scale(page, dim, group, dtype, prompt):
+    """One key stands against all others in the infinite channel, so that a single score is +inf where the others are -inf, or the
+    other way round, in the first step and in a late one; a scale of 0 makes NaN of each."""
+    lens, new, heads = [page * 5 + 3], [3], 2
+    for at in (1, page * 4 + 2):
+        tensors, batch = srv.make(140, lens, new, heads, page, dim, dtype)
+        codes = tensors[0]
+        codes[..., 0] = codes[..., 0] & 0xF0 | 2  # channel 0: +1
+        where = batch[0][0, at // page].long()
+        codes[where, :, at % page, 0] |= 8
+        q = ref.rows(141, 3, heads * group, dim, dtype)
+        q[0, 0, 0], q[2, -1, 0], q[1, group, 0] = math.inf, -math.inf, math.inf
+        for scale in (0.1, -0.1, 0.0):
+            check_attention(tensors, batch, q, scale=scale, prompt=prompt)
+            some = torch.tensor([[0, 1, 4, -1]], dtype=torch.int32).expand(3 * heads, 4).contiguous()
+            check_attention(tensors, batch, q, some, scale=scale, prompt=prompt)
+
+
+@pytest.mark.parametrize("prompt", [0, 1])
 def test_absent_pages_are_not_seen(prompt):
     lens, new = [300, 100, 64], [3, 1, 1]
     tensors, batch = srv.make(49, lens, new, 2, 16, 64, BF16)
