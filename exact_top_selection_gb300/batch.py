@@ -35,7 +35,8 @@ _bound = None
 
 class _Spec(ctypes.Structure):
     _fields_ = [("turns", ctypes.c_void_p), ("amplitude", ctypes.c_float), ("head_dim", ctypes.c_int32),
-                ("rotary_dim", ctypes.c_int32), ("neighbours", ctypes.c_int32), ("type", ctypes.c_int32)]
+                ("rotary_dim", ctypes.c_int32), ("neighbours", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("page_size", ctypes.c_int32)]
 
 
 class _Tables(ctypes.Structure):
@@ -151,20 +152,25 @@ class Rotary:
             _cache._wait_for_buffers()
         self._specs = {}
         for i, dtype in enumerate((torch.bfloat16, torch.float16)):
-            spec = _Spec(self.turns.data_ptr(), self.amplitude, head_dim, rotary_dim, int(self.neighbours), i)
-            self._specs[dtype] = spec, _RowsOf(dev, dtype, head_dim)
+            specs = {page or None: _Spec(self.turns.data_ptr(), self.amplitude, head_dim, rotary_dim, int(self.neighbours), i, page)
+                     for page in (0, *_cache.PAGE_SIZES)}
+            self._specs[dtype] = specs, _RowsOf(dev, dtype, head_dim)
 
-    def __call__(self, q, k=None, batch=None, positions=None, out=None, inverse=False, stream=None):
+    def __call__(self, q, k=None, batch=None, positions=None, out=None, inverse=False, stream=None, page_size=None):
         """q [num_tokens, q_heads, head_dim] turned, and with k [num_tokens, k_heads, head_dim] the pair of both.
 
         batch: rows have the positions of their tokens in it; rows of no sequence are left as they are in
         ``out`` (zeros where it is not given).  positions, int32 [num_tokens], instead: any numbers.  out: rows to write into (a
         pair with k); q and k themselves are turned in place, other rows must not overlap them.  inverse: turns
-        back, which is also the gradient of q and k by that of the outputs."""
+        back, which is also the gradient of q and k by that of the outputs.  page_size: of the batch's tables; a
+        length beyond table_width * page_size is clamped to it, as by the cache's operators (without, lengths are taken as they are)."""
         torch = _cache.torch
         if q.dtype not in self._specs:
             raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-        spec, like = self._specs[q.dtype]
+        specs, like = self._specs[q.dtype]
+        spec = specs.get(page_size)
+        if spec is None:
+            raise ValueError(f"page_size must be None or in {_cache.PAGE_SIZES}, got {page_size}")
         heads = q.shape[1] if q.dim() == 3 else 0
         qr = _cache._rows(q, "q", like, heads)
         if heads < 1:

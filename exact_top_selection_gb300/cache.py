@@ -550,9 +550,9 @@ class SparseAttention:
                 raise ValueError("k, v and q must have the same tokens")
         if self.rotary is not None:
             if k is None:
-                q = self.rotary(q, batch=batch, out=self.turned[0], stream=stream)
+                q = self.rotary(q, batch=batch, out=self.turned[0], stream=stream, page_size=self.cache.page_size)
             else:
-                q, k = self.rotary(q, k, batch=batch, out=self.turned, stream=stream)
+                q, k = self.rotary(q, k, batch=batch, out=self.turned, stream=stream, page_size=self.cache.page_size)
         if k is not None:
             cache_write(self.cache, batch, k, v, stream=stream)
         block_scores(self.cache, batch, q, *self.keep, scores=self.scores, ke=self.ke,

@@ -58,10 +58,17 @@ int exact_topk_rotary(const exact_topk_rotary_spec* spec, const exact_topk_batch
     b.num_tokens = num_tokens;
     b.num_seqs = batch->num_seqs;
     b.width = 1 << 30;  // lengths are clamped to this many tokens
+    if (spec->page_size > 0) {
+      const int64_t most = (int64_t)batch->table_width * spec->page_size;
+      if (batch->table_width < 1 || most > b.width) return EXACT_TOPK_ERR_BAD_BATCH;
+      b.width = (int)most;
+    }
   }
   if (spec->head_dim < 8 || spec->head_dim > 1024 || spec->head_dim % 8 != 0 ||
       spec->rotary_dim < 2 || spec->rotary_dim % 2 != 0 || spec->rotary_dim > spec->head_dim ||
       spec->rotary_dim > EXACT_TOPK_MAX_ROTARY_DIM || !std::isfinite(spec->amplitude) ||
+      !(spec->page_size == 0 || spec->page_size == 16 || spec->page_size == 32 ||
+        spec->page_size == 64 || spec->page_size == 128) ||
       (spec->type != EXACT_TOPK_TYPE_BF16 && spec->type != EXACT_TOPK_TYPE_FP16))
     return EXACT_TOPK_ERR_BAD_SHAPE;
   if (q_heads < 1 || q_heads > 65536 || k_heads < 0 || k_heads > 65536)

@@ -277,7 +277,10 @@ int exact_topk_cache4_attention_run(const exact_topk_attention_plan* plan,
  * p by p * turns[i] / 2^64 turns, modulo one (exact for every position), times amplitude.
  *   turns       device [rotary_dim / 2]
  *   head_dim    a multiple of 8 up to 1024;  rotary_dim even, 2 to head_dim and at most 512
- *   type        of all rows */
+ *   type        of all rows
+ *   page_size   16, 32, 64 or 128: of the batch's tables, to whose table_width * page_size tokens lengths
+ *               are clamped then, as by the cache's operators; 0: there is no table, lengths are taken
+ *               as they are, up to 2^30 */
 typedef struct exact_topk_rotary_spec {
   const uint64_t* turns;
   float amplitude;
@@ -285,13 +288,14 @@ typedef struct exact_topk_rotary_spec {
   int32_t rotary_dim;
   int32_t neighbours;
   int32_t type;
+  int32_t page_size;
 } exact_topk_rotary_spec;
 
 /* Turns q [num_tokens][q_heads][head_dim] into q_out and k [num_tokens][k_heads][head_dim] into
  * k_out; cosines, sines and sums are FP32, rounded once. Each may be its own output (the same data
  * and strides), in no other way may they overlap. k_heads may be 0 (k and k_out are ignored).
- *   batch       the rows' positions are those of their tokens (the page table is not looked at);
- *               rows of no sequence or without a token are left as they were
+ *   batch       the rows' positions are those of their tokens (the page table's entries are not looked
+ *               at); rows of no sequence or without a token are left as they were
  *   positions   device int32 [num_tokens] instead of the batch (one of the two is NULL): any
  *               numbers, negative ones turn back
  *   inverse     nonzero: by the negative angles. That is the gradient of q and k by what comes

@@ -102,6 +102,22 @@ def test_rotary_refuses_bad_arguments():
     assert call(tokens=0) == 0 and call(tokens=0, positions=None, k=None, k_heads=0, q=(None, 0, 0)) == 0
 
 
+def test_rotary_refuses_bad_page_sizes():
+    lib, byref = binding._lib(), ctypes.byref
+
+    def call(page_size, width=1, positions=None):
+        spec = binding._Spec(fake(1), 1.0, 128, 64, 0, 0, page_size)
+        batch = cache_binding._Batch(None, fake(7), fake(8), 4, width, width)
+        rows = byref(cache_binding._Rows(fake(3), 256, 128))
+        return lib.exact_topk_rotary(byref(spec), None if positions else byref(batch), positions, 0, 2, rows, rows, 0, None, None, 0, None)
+
+    for bad in (-1, 1, 8, 48, 256, 2 ** 30):
+        assert call(bad) == -2 and call(bad, positions=fake(2)) == -2, bad
+    assert call(16, 0) == -10 and call(16, -1) == -10 and call(128, (1 << 23) + 1) == -10 and call(16, 2 ** 31 - 1) == -10
+    for good in ((0, 0), (0, 2 ** 31 - 1), (16, 1), (128, 1 << 23)):
+        assert call(*good) == 0, good
+
+
 def test_tables_refuse_bad_arguments():
     lib, byref = binding._lib(), ctypes.byref
     def call(change=fake(20), **fields):

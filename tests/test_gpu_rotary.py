@@ -212,3 +212,43 @@ def test_in_place_on_heads_that_interleave(T):
     for i in range(2):
         close(wide[:, :, i], *srv.rotary(x[:, :, i], range(7, 7 + T), rotary.frequencies, 1.0, False, MARK))
     assert torch.equal(wide[:, :, 2].cpu(), x[:, :, 2])
+
+
+@pytest.mark.parametrize("new", [[3, 1, 2, 5], [1, 1, 1, 1]])
+def test_lengths_beyond_the_table_are_clamped_to_it(new):
+    """As by the cache's operators, where the page size is given; as they are without."""
+    lens, width = [100, 64, 2 ** 31 - 1, 30], 4
+    single = all(n == 1 for n in new)
+    for page_size, most in ((16, 64), (32, 128), (None, 1 << 30)):
+        batch = sequences([min(n, most) for n in lens], new)
+        table = torch.zeros(4, width, dtype=torch.int32, device="cuda")
+        dev = etk.SequenceBatch(table, torch.tensor(lens, dtype=torch.int32, device="cuda"), None if single else batch[2].cuda())
+        q = ref.rows(11, sum(new), 3, 64, BF16)
+        rotary = etk.Rotary(64, device="cuda")
+        got = rotary(q.cuda(), batch=dev, page_size=page_size)
+        close(got, *srv.rotary(q, srv.positions(batch, sum(new), page=1 << 30), rotary.frequencies, 1.0, False, MARK))
+    for bad in (0, 17, 256):
+        with pytest.raises(ValueError, match="page_size"):
+            rotary(q.cuda(), batch=dev, page_size=bad)
+
+
+@pytest.mark.parametrize("make", [etk.KVCache, etk.KVCache4])
+def test_a_step_on_lengths_beyond_the_table_is_one_on_the_clamped_lengths(make):
+    """Angles, the places that are written and the tokens that are attended to go together."""
+    page, dim, width, heads, group, new = 16, 64, 4, 2, 4, [3, 1]
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(2, width)
+    start = torch.tensor([0, 3, 4], dtype=torch.int32, device="cuda")
+    q, k, v = (ref.rows(12 + i, 4, h, dim, BF16).cuda() for i, h in enumerate((heads * group, heads, heads)))
+    old = [ref.rows(15 + i, 2 * width * page, heads, dim, BF16).cuda() for i in range(2)]
+    full = etk.SequenceBatch(table, torch.full((2,), width * page, dtype=torch.int32, device="cuda"),
+                             torch.tensor([0, width * page, 2 * width * page], dtype=torch.int32, device="cuda"))
+    got = []
+    for lens in ([width * page, 50], [100, 50], [2 ** 31 - 1, 50]):
+        cache = make.allocate(8, heads, page, dim, device="cuda")
+        etk.cache_write(cache, full, *old)
+        step = etk.SparseAttention(cache, 2, 4, heads * group, width, 3, 1, 1, rotary=etk.Rotary(dim, device="cuda"))
+        out = step(q, etk.SequenceBatch(table, torch.tensor(lens, dtype=torch.int32, device="cuda"), start), k, v)
+        got.append([out, cache.k.view(torch.uint8), cache.v.view(torch.uint8), step.blocks.sort(-1).values])
+    for other in got[1:]:
+        for x, y in zip(got[0], other):
+            assert torch.equal(x, y)
