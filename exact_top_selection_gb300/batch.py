@@ -162,8 +162,9 @@ class Rotary:
         batch: rows have the positions of their tokens in it; rows of no sequence are left as they are in
         ``out`` (zeros where it is not given).  positions, int32 [num_tokens], instead: any numbers.  out: rows to write into (a
         pair with k); q and k themselves are turned in place, other rows must not overlap them.  inverse: turns
-        back, which is also the gradient of q and k by that of the outputs.  page_size: of the batch's tables; a
-        length beyond table_width * page_size is clamped to it, as by the cache's operators (without, lengths are taken as they are)."""
+        by the negative angles, with the same amplitude: the gradient of q and k by that of the outputs, and the way back
+        where the amplitude is 1 (else it ends at amplitude^2 times the rows).  page_size: of the batch's tables; a length beyond
+        table_width * page_size is clamped to it, as by the cache's operators (without, lengths are taken as they are)."""
         torch = _cache.torch
         if q.dtype not in self._specs:
             raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")

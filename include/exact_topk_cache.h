@@ -298,8 +298,8 @@ typedef struct exact_topk_rotary_spec {
  *               at); rows of no sequence or without a token are left as they were
  *   positions   device int32 [num_tokens] instead of the batch (one of the two is NULL): any
  *               numbers, negative ones turn back
- *   inverse     nonzero: by the negative angles. That is the gradient of q and k by what comes
- *               back for q_out and k_out.
+ *   inverse     nonzero: by the negative angles, with the same amplitude. That is the gradient of q and
+ *               k by what comes back for q_out and k_out; it undoes the call where the amplitude is 1.
  * Errors: NULL_POINTER, BAD_BATCH, BAD_HEADS, BAD_SHAPE (the spec, the amplitude not finite),
  * MISALIGNED, CUDA. */
 int exact_topk_rotary(const exact_topk_rotary_spec* spec, const exact_topk_batch* batch,

@@ -252,3 +252,20 @@ def test_a_step_on_lengths_beyond_the_table_is_one_on_the_clamped_lengths(make):
     for other in got[1:]:
         for x, y in zip(got[0], other):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("amplitude", [1.0, 1.25, -0.5])
+def test_there_and_back_gives_the_amplitudes_square(amplitude):
+    """The way back is off by its own tolerance and by what the way there rounded: turned back, that of a pair's two numbers."""
+    pos, dim, rot = [0, 5, 70000], 64, 48
+    rotary = etk.Rotary(dim, rot, amplitude=amplitude, device="cuda")
+    positions = torch.tensor(pos, dtype=torch.int32, device="cuda")
+    x = ref.rows(20, 3, 2, dim, FP16)
+    there = rotary(x.cuda(), positions=positions)
+    _, tol = srv.rotary(x, pos, rotary.frequencies, amplitude, False, MARK)
+    _, back_tol = srv.rotary(there.cpu(), pos, rotary.frequencies, amplitude, False, MARK, inverse=True)
+    pair = tol[..., :rot // 2] + tol[..., rot // 2:rot]
+    tol = torch.cat([pair, pair, tol[..., rot:]], -1) * abs(amplitude) + back_tol
+    by = torch.ones(dim, dtype=torch.float64)
+    by[:rot] = amplitude ** 2
+    close(rotary(there, positions=positions, inverse=True), x.double() * by, tol)
