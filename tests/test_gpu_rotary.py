@@ -269,3 +269,20 @@ def test_there_and_back_gives_the_amplitudes_square(amplitude):
     by = torch.ones(dim, dtype=torch.float64)
     by[:rot] = amplitude ** 2
     close(rotary(there, positions=positions, inverse=True), x.double() * by, tol)
+
+
+@pytest.mark.parametrize("lens,new", [([300, 5, 40, 129], [130, 0, 40, 2]), ([3, 0, 70], [5, 2, 9]), ([1], [1])])
+def test_outputs_that_the_call_makes(lens, new):
+    """Without `out`: as into tensors of the caller's where a row has a position, zeros elsewhere; without k, as with it."""
+    batch = sequences(lens, new)
+    T = sum(new) + 3  # rows behind the last sequence
+    q, k = ref.rows(30, T, 5, 64, BF16, 3.0), ref.rows(31, T, 2, 64, BF16)
+    q[-3:], k[-3:] = math.nan, math.inf
+    rotary, dev = etk.Rotary(64, 48, device="cuda"), device_batch(batch)
+    there = torch.tensor([p is not None for p in srv.positions(batch, T, page=1 << 30)])
+    assert not there.all() and there.any()
+    into = torch.full_like(q, MARK, device="cuda"), torch.full_like(k, MARK, device="cuda")
+    rotary(q.cuda(), k.cuda(), batch=dev, out=into)
+    for got, want in zip((*rotary(q.cuda(), k.cuda(), batch=dev), rotary(q.cuda(), batch=dev)), (*into, into[0])):
+        assert got.is_contiguous() and torch.equal(got[there], want[there])
+        assert (got[~there] == 0).all() and (want[~there] == MARK).all()
