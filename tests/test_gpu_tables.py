@@ -157,6 +157,81 @@ def test_tables_made_behind_other_work_and_used_on_another_stream():
     assert tables.slots[:45].tolist() == list(range(5)) + list(range(16, 56))
 
 
+@pytest.mark.parametrize("seqs,max_tokens", [(6, 200), (6, 40000), (1500, 3000)])
+def test_nothing_around_the_buffers_is_touched(seqs, max_tokens):
+    """Every buffer lies between marked entries, the tables' rows too: ordinary changes, then contents out of every range."""
+    pages, width, page, margin = 20 * seqs, 7, 16, 37
+    whole = []
+
+    def between(values):
+        x = torch.full((len(values) + 2 * margin,), -9, dtype=torch.int32, device="cuda")
+        x[margin:-margin] = torch.as_tensor(values, dtype=torch.int32)
+        whole.append(x)
+        return x[margin:-margin]
+
+    wide = torch.full((seqs + 2, width + 2 * margin), -9, dtype=torch.int32, device="cuda")
+    tables = etk.PageTables(wide[1:-1, margin:margin + width], between([0] * seqs), between(range(pages)), between([0, pages]), page, max_tokens,
+                            q_start=between([0] * (seqs + 1)), slots=between([0] * max_tokens), positions=between([0] * max_tokens))
+
+    def untouched():
+        assert all(bool((x[:margin] == -9).all()) and bool((x[-margin:] == -9).all()) for x in whole)
+        assert (wide[0] == -9).all() and (wide[-1] == -9).all() and (wide[:, :margin] == -9).all() and (wide[:, margin + width:] == -9).all()
+
+    g = torch.Generator().manual_seed(seqs)
+    for _ in range(4):
+        tables.update(torch.randint(-40, 60, (seqs,), generator=g, dtype=torch.int32).cuda())
+        untouched()
+    assert tables.positions.max() > 0
+    edges = torch.tensor([2 ** 31 - 1, -5, 112, 10 ** 6, 0, -2 ** 31], dtype=torch.int32).repeat(-(-seqs // 6))[:seqs]
+    steps = torch.tensor([-2 ** 31, 16, 1, -1, 2 ** 31 - 1, 5, 0], dtype=torch.int32).repeat(-(-seqs // 7))[:seqs]
+    for lens, where in ((edges, [-7, 2 ** 31 - 1]), (edges.roll(1), [2 ** 31 - 1, -3]), (edges.roll(2), [-2 ** 31, pages]), (edges.roll(3), [pages - 1, pages])):
+        tables.kv_len.copy_(lens)
+        tables.free_range.copy_(torch.tensor(where, dtype=torch.int32))
+        for change in (steps, -1 - steps, steps.roll(3), edges):
+            tables.update(change.cuda())
+            untouched()
+            tables.drop(change.cuda())
+            untouched()
+            assert 0 <= int(tables.kv_len.min()) and int(tables.kv_len.max()) <= width * page
+            assert 0 <= int(tables.free_range[0]) < pages and 0 <= int(tables.free_range[1]) <= pages
+            assert 0 <= int(tables.q_start.min()) and int(tables.q_start.max()) <= max_tokens and not tables.counters.any()
+
+
+def test_more_pages_than_the_ctas_fill_at_once():
+    """Three million tokens in pages of 16: each CTA goes through its units more than once. Checked by tensor arithmetic."""
+    page, width, most = 16, 80000, 3_000_000
+    pages = 240_000
+    tables = etk.PageTables.allocate(pages, 5, width, page, most, device="cuda")
+    ring = torch.randperm(pages, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    tables.free_pages.copy_(ring)
+    lens, head, free = torch.zeros(5, dtype=torch.long), 0, pages
+    held = [torch.zeros(0, dtype=torch.int32, device="cuda") for _ in range(5)]
+    for change in ([700_001, 1_279_999, 16, 0, 1_000_001 - 17], [-650_007, 1, -2 ** 31, 1_240_000, 0], [1_000_000, -1_279_999, 77, -1_240_000, 31]):
+        tables.update(torch.tensor(change, dtype=torch.int32, device="cuda"))
+        want = torch.maximum(torch.tensor(change), -lens)
+        new = lens + want
+        have = [-(-int(n) // page) for n in new]
+        back = [h[n:] for h, n in zip(held, have)]
+        ring_now = torch.cat([ring.roll(-head)[:free], *back])  # the free pages in order, those given back behind them
+        taken, start = 0, 0
+        for b in range(5):
+            held[b], need = held[b][:have[b]], have[b] - len(held[b][:have[b]])
+            held[b] = torch.cat([held[b], ring_now[taken:taken + need]])
+            taken += need
+            assert torch.equal(tables.page_table[b, :have[b]], held[b])
+            got = int(max(want[b], 0))
+            pos = torch.arange(int(lens[b]), int(lens[b]) + got, device="cuda")
+            assert torch.equal(tables.positions[start:start + got].long(), pos)
+            assert torch.equal(tables.slots[start:start + got].long(), held[b][pos // page].long() * page + pos % page)
+            start += got
+            assert int(tables.q_start[b + 1]) == start
+        assert tables.kv_len.tolist() == new.tolist() and tables.applied.tolist() == want.tolist() and not tables.counters.any()
+        lens, free, ring = new, len(ring_now) - taken, tables.free_pages.clone()
+        head = int(tables.free_range[0])
+        assert tables.free_range.tolist()[1] == free and torch.equal(ring.roll(-head)[:free], ring_now[taken:])
+        assert torch.equal(torch.cat([*held, ring_now[taken:]]).sort().values, torch.arange(pages, dtype=torch.int32, device="cuda"))
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_a_step_from_tables_to_attention(bits):
     """Prompts, then tokens one at a time with tokens taken back and a sequence that ends and another that begins, all in
