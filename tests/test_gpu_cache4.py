@@ -617,3 +617,23 @@ def test_two_tiles_a_cta_over_long_caches():
         attend = etk.CacheAttention(cache, 2, 300, heads * group, b.table_width, 0 if blocks is None else 140, prompt=1)
         got = attend(q.cuda(), b, blocks=None if blocks is None else blocks.cuda()).cpu().double()
         assert ((got - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("width", [16384, 16385, 24576])
+def test_prompts_over_lists_of_wide_tables(width, dim):
+    """The widest tables of the kernel of two tiles a CTA and of the one of a tile, and their largest shared memory; the last pages are listed."""
+    page, group, new = 16, 8, 20
+    lens = [width * page - 3]
+    tensors, batch = srv.make(150, lens, [new], 1, page, dim, BF16, width=width)
+    g = torch.Generator().manual_seed(151)
+    some = torch.randint(0, width, (40,), generator=g)  # neighbours share pages
+    blocks = torch.stack([torch.cat([some[torch.randint(0, 40, (9,), generator=g)], torch.tensor([0, width - 1, width - 2 + i % 3])]) for i in range(new)])
+    q = ref.rows(152, new, group, dim, BF16, 3.0)
+    check_attention(tensors, batch, q, blocks.to(torch.int32), prompt=1)
+
+
+def test_prompts_over_lists_of_wider_tables_are_refused():
+    with pytest.raises(etk.ExactTopKError):
+        etk.make_attention_plan(20, 1, 8, 1, 64, 16, 24577, 12, False, prompt=1, bits=4)
+    assert etk.make_attention_plan(4096, 1, 16, 1, 64, 16, 24577, 12, False, bits=4).prompt_tokens == 0
