@@ -463,8 +463,9 @@ class CacheAttention:
     num_blocks=0 attends to every cached token up to the row's own; num_blocks=K to those of the pages
     listed for each token and key head (``blocks`` int32 [num_tokens * kv_heads, K], as ExactTopK selects
     them: a set in any order, -1 and anything outside the pages that the token sees ignored, repeats counted
-    once).  A row that sees nothing gives zeros.  Calls of one object must not overlap on the GPU: graphs
-    that may run at the same time each need an object of their own.  Keep the object until its last call has run."""
+    once).  A row that sees nothing gives zeros, another one with an infinity or a NaN in its query NaN.  Calls of
+    one object must not overlap on the GPU: graphs that may run at the same time each need an object of their
+    own.  Keep the object until its last call has run."""
 
     def __init__(self, cache, num_seqs, num_tokens, q_heads, table_width, num_blocks=0, **overrides):
         self.cache = cache

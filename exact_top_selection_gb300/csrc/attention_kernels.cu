@@ -512,9 +512,14 @@ __global__ void __launch_bounds__(kThreads, attention_ctas_per_sm(NT * 8, D))
         *reinterpret_cast<__half2*>(&sm.q[col][at]) =
             __floats2half2_rn(x[i].x * by, x[i].y * by);
       }
+      // A row with an infinity has the factor NaN: each of its scores is an infinity or NaN, and its
+      // weights are 0 / 0 or NaN, whatever the scores' signs.
       if (lane == 0)
         sm.factor[col] =
-            col < columns ? __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2 : 0.f;
+            col < columns ? __uint_as_float(top == infinity() ? 0x7FFFFFFFu
+                                                              : (uint32_t)(127 - up) << 23) *
+                                a.scale_log2
+                          : 0.f;
     }
     __syncthreads();  // queries and marks are in place
 

@@ -191,9 +191,13 @@ __global__ void __launch_bounds__(kThreads, 2)
           &sm.q[piece / 8][row * 128 + (((piece & 7) ^ (row & 7)) << 4)]) =
           make_uint4(pack2<true>(x[0].x, x[0].y), pack2<true>(x[1].x, x[1].y),
                      pack2<true>(x[2].x, x[2].y), pack2<true>(x[3].x, x[3].y));
+      // NaN where the row has an infinity (see attention_kernels.cu)
       if (piece == 0)
         sm.factor[row] =
-            row < live ? __uint_as_float((uint32_t)(127 - up) << 23) * fabsf(a.scale_log2) : 0.f;
+            row < live ? __uint_as_float(top == infinity() ? 0x7FFFFFFFu
+                                                           : (uint32_t)(127 - up) << 23) *
+                             fabsf(a.scale_log2)
+                       : 0.f;
     }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

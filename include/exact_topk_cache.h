@@ -181,11 +181,13 @@ int exact_topk_make_attention_plan(int64_t num_tokens, int num_seqs, int single_
 
 /* out[t][head] = sum_p softmax_p(scale * q[t][head] . k[p]) v[p] over the tokens p at
  * positions up to t's own: all of them, or those of the pages listed for the row.
- * A row that sees nothing gets zeros. Scores, sums and outputs are FP32, rounded
- * once to the cache's type; the probabilities enter the second product in FP16, off by
- * 2^-11 of themselves and, below 2^-20 of the row's largest, by at most 2^-31 of that.
+ * A row that sees nothing gets zeros, another one with an infinity or a NaN in its query
+ * NaN. Scores, sums and outputs are FP32, rounded once to the cache's type; the
+ * probabilities enter the second product in FP16, off by 2^-11 of themselves and, below
+ * 2^-20 of the row's largest, by at most 2^-31 of that.
  *   q, out      [num_tokens][q_heads][head_dim]; they must not overlap
- *   scale       finite, as is scale * log2(e) (else BAD_PLAN); the scores must be finite in FP32
+ *   scale       finite, as is scale * log2(e) (else BAD_PLAN); the scores of finite queries must be
+ *               finite in FP32
  *   blocks      NULL when plan->num_blocks is 0, else device int32
  *               [num_tokens * kv_heads][num_blocks]: pages by their place in the
  *               sequence, as exact_topk selects them. A list is a set: order does not

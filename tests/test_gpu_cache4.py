@@ -637,3 +637,34 @@ def test_prompts_over_lists_of_wider_tables_are_refused():
     with pytest.raises(etk.ExactTopKError):
         etk.make_attention_plan(20, 1, 8, 1, 64, 16, 24577, 12, False, prompt=1, bits=4)
     assert etk.make_attention_plan(4096, 1, 16, 1, 64, 16, 24577, 12, False, bits=4).prompt_tokens == 0
+
+
+@pytest.mark.parametrize("prompt", [0, 1])
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("page,dim,group,dtype", [(64, 128, 4, BF16), (16, 128, 12, FP16), (16, 64, 3, BF16), (32, 64, 20, FP16)])
+def test_a_query_with_an_infinity_gives_nan(page, dim, group, dtype, bits, prompt):
+    """Every score of such a row is an infinity or NaN: also where all are -inf the weights are 0 / 0. Its neighbours are not touched, and
+    a row that sees nothing gives zeros."""
+    lens, new, heads = [page * 5 + 3, 1], [6, 2], 2
+    if bits == 4:
+        tensors, batch = srv.make(160, lens, new, heads, page, dim, dtype)
+        tensors[0][..., 0] = tensors[0][..., 0] & 0xF0 | 2  # channel 0: +1
+        cache = device_cache(tensors)
+        plain = srv.Cache4(*tensors)
+    else:
+        tensors, batch = ref.make(160, lens, new, heads, page, dim, dtype)
+        codes = tensors[0].view(torch.uint8)
+        codes[..., 0] = torch.where(codes[..., 0] & 0x7F == 0x7F, codes[..., 0], 0x38)
+        cache = etk.KVCache(*(t.cuda() for t in tensors))
+        plain = ref.Cache(*tensors)
+    q = ref.rows(161, 8, heads * group, dim, dtype)
+    q[0, 0, 0], q[2, -1, 0], q[4, group, 0], q[6] = math.inf, -math.inf, -math.inf, math.inf  # row 6 has no token
+    q[3, 1, 5], q[3, 1, 0] = math.inf, 3.0
+    for scale in (0.1, -0.1, 0.0):
+        for blocks in (None, torch.tensor([[0, 1, 4, -1]], dtype=torch.int32).expand(8 * heads, 4).contiguous()):
+            want, tol = ref.attention(plain, batch, q, blocks, scale, MARK)
+            b = device_batch(batch)
+            attend = etk.CacheAttention(cache, 2, 8, heads * group, b.table_width, 0 if blocks is None else 4, prompt=prompt)
+            got = attend(q.cuda(), b, blocks=None if blocks is None else blocks.cuda(), out=torch.full_like(q, MARK, device="cuda"), scale=scale).cpu().double()
+            assert want.isnan().any() and torch.equal(got.isnan(), want.isnan())
+            assert ((got - want).abs() <= tol)[~want.isnan()].all()
