@@ -44,13 +44,17 @@
 // computed. A step takes as many conversions as of 8 bits and a product for each: issue slots (57% used,
 // conversions at half rate) bound it beside HBM.
 //
-// Measured: 64 sequences of 2048 to 65536 tokens, 4 key heads x 8 query heads of 128 channels
-// (2.4 GB): 360 to 370 us from GPU to GPU, 95 to 98% of the rate of a copy. 8 sequences of 512 K
-// tokens, 3 new ones, 2 x 4 heads of 64 channels (1.06 GB): 209 us. 32 listed pages of 64
-// sequences (134 MB): 34 us. In 4 bits: 238 us (1.35 GB, 5.6 TB/s) for the first, 211 for the second
-// (604 MB), 28 for the third. Steps of 16 tokens took 317 us for the first; a fifth CTA an SM
-// changed nothing there (240) and cost 5 us of the third, as asking for all listed pages ahead of their
-// order cost it 3.
+// Measured: 64 sequences of 2048 to 65536 tokens, 4 key heads x 8 query heads of 128 channels (2.4
+// GB): 360 to 370 us from GPU to GPU, 95 to 98% of the rate of a copy. 8 sequences of 512 K tokens,
+// 3 new ones, 2 x 4 heads of 64 channels (1.06 GB): 209 us. 32 listed pages of 64 sequences (134
+// MB): 34 us. In 4 bits: 238 us (1.35 GB, 5.6 TB/s, 83% of the copy rate) for the first. The second
+// is not bound by its bytes: 213 us for 604 MB, 42% of that rate and as long as in 8 bits, since a
+// step's softmax is of 16 columns, of which 12 are live, and its codes are of half as many channels
+// (issue slots 60% used, HBM 27%). The third 28 us, 39%: its lists, page ids and join (9 us) stand
+// before and behind 12 us of products. Pages of 16 tokens of 128 channels take steps of 16: 311 us
+// for the first and 36 for the third, where pages of 32 take 241 and 30, and pages of 128 239 and
+// 28. A fifth CTA an SM changed nothing for the first (240) and cost 5 us of the third, as asking
+// for all listed pages ahead of their order cost it 3.
 
 #include <climits>
 
@@ -144,8 +148,11 @@ __device__ __forceinline__ int page_units(const CacheArgs& c, const SeqRows& s) 
   return pages > 0 ? pages : 1;
 }
 
-// Steps that a warp holds in shared memory, all but one of them on their way: 48 KB of a
-// CTA where four share an SM, more where fewer do.
+// Steps that a warp holds in shared memory, in whole steps; all but the one that is computed are on
+// their way. In 8 bits they are 48 KB of a CTA where four share an SM, more where fewer do. In 4 bits
+// a step of 32 tokens x 128 channels is 4608 bytes, and 2, 3 or 4 of them, 36, 54 or 72 KB of a CTA,
+// are what fits beside 4, 3 or 2 CTAs' other needs: 18 KB of a CTA on their way where four share an
+// SM. Steps of half that size: 5, 7 or 9, 45, 63 or 81 KB; of a quarter twice as many.
 constexpr int ring_steps(int dim, int tiles, int blocks, int bits) {
   const int ctas = attention_ctas_per_sm(tiles * 8, dim);
   // of 128 channels
@@ -1272,7 +1279,10 @@ int launch_attention4(const Cache4Args& c, const BatchArgs& b, const AttentionAr
     // Two tiles a CTA: 16 heads x 448 to 1536 tokens over 8192 take 128 us against 157 with a tile
     // a CTA, over lists 51 against 56; 64 sequences of 16 tokens (a tile each) over 4096 63 against
     // 103. Not where sequences have a tile each and those are more than the SMs: 256 of them take 290
-    // against 237, since two CTAs of the other kernel share an SM. Lists: a bit for each token.
+    // against 237, since two CTAs of the other kernel share an SM. Lists: a bit for each token, so
+    // below 8 heads of a group, whose tiles have more than 16 tokens, a tile a CTA: 4096 tokens x 16
+    // heads over 32 shared pages take 117 us with a group of 16 and 125 with 8; 144 with 7, 152
+    // with 4, 283 with 2 and 503 with 1 (399, 460, 460, 504, 538 and 570 without this kernel).
     const int64_t mean = (b.num_tokens + b.num_seqs - 1) / b.num_seqs;
     const int64_t tiles = (int64_t)b.num_seqs * c.heads *
                           ((a.group + a.prompt_heads - 1) / a.prompt_heads);

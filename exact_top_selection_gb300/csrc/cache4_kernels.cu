@@ -133,10 +133,14 @@ __device__ __forceinline__ bool encode16(const uint32_t (&w)[8], float unit, flo
   return special;
 }
 
-// A thread has 16 channels of a row, which need no other thread; the CTA only joins the keys' bounds.
-// 108 K tokens of 8 heads x 128 channels take 93 us (6.1 TB/s); four rows on their way in each of 32
-// warps an SM: with two 123, and 111 before whole pages went without predicates and a CTA took
-// several heads.
+// A thread has 16 channels of a row, which need no other thread; the CTA only joins the keys'
+// bounds. 108 K tokens of 8 heads x 128 channels in pages of 64 take 92 us (6.2 TB/s); four rows on
+// their way in each of 32 warps an SM: with two 123, and 111 before whole pages went without
+// predicates and a CTA took several heads. It is near HBM's rate where a page gives each thread
+// four rows or more: pages of 32 take 110 us, pages of 16 147, with one row a thread and the join
+// of the bounds behind each. Of 64 channels, 216 K tokens: 242, 152, 112 and 99 in pages of 16 to
+// 128. Pages of 128 of 128 channels take 109: the bound of 64 registers, made for four rows on
+// their way, has eight passes spill (382 bytes a thread, 44 in pages of 64, none in pages of 16).
 template <bool kFp16, int D, int P>
 __global__ void __launch_bounds__(kThreads, 8)
     cache4_write_kernel(Cache4Args c, BatchArgs b, RowArgs krows, RowArgs vrows) {
@@ -376,7 +380,14 @@ __global__ void __launch_bounds__(kThreads) cache4_read_kernel(Cache4Args c, Bat
     steps_of(std::false_type());
 }
 
-// As of the 8-bit cache: heads over CTAs until there are a few waves of them.
+// As of the 8-bit cache: heads over CTAs until there are a few waves of them (4096 CTAs), and as
+// far as a CTA gets `most` numbers then. 108 K tokens of 8 heads x 128 channels in pages of 16, 32,
+// 64 and 128: written in 147, 110, 96 and 109 us with 32768, 160, 125, 105 and 110 with 8192, and
+// 257, 156, 105 and 110 with a head a CTA; read in 90, 90, 92 and 90 with 8192, 156, 157, 91 and 90
+// with 4096, 286, 157, 91 and 90 with a head a CTA. (A cache of one key head has a head a CTA in
+// any case: 258 and 286 us for as many numbers in pages of 16.) Eight sequences of 1000 tokens in
+// pages of 16: written in 17.6 us, read in 14.1, from 1024 CTAs on 17.1 and 10.0, from 16384 on
+// 21.3 and 22.0. (All behind a cold L2.)
 dim3 page_grid(const CacheArgs& c, const BatchArgs& b, int most) {
   const int64_t slots = slot_count(b, c.page, 2);
   int y = c.heads;

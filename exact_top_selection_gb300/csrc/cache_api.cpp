@@ -192,13 +192,22 @@ int make_plan(int64_t num_tokens, int num_seqs, int single_rows, int q_heads, in
   p.page_size = page_size;
   p.table_width = table_width;
   p.num_blocks = num_blocks;
-  // Columns of a tile: 8 as a rule, more only where a key head has more query heads. Wider
-  // tiles share pages between tokens, but are fewer and their products and joins longer. Over
-  // listed pages 8 columns were the fastest or within 4% of it from 1 to 256 tokens of a sequence
-  // (8 tokens of 32 sequences x 16 heads over 32 pages: 50 us, 16 columns 58, 32 columns 56; 32
-  // tokens of one: 17, 21 and 30; 256: 44, 53 and 49; 512: 84, 88 and 75). Over the whole cache
-  // 16 columns win once passes of 8 would read 256 MB (65 MB: 20.5 us with 8, 23.3 with 16; 262 MB:
-  // 43.7 and 44.4; 524 MB: 67.2 and 60.3; 2.1 GB: 230 and 161), and 32 lose to them (94 and 170).
+  // Columns of a tile: 8 as a rule, more only where a key head has more query heads. Wider tiles
+  // share pages between tokens, but are fewer and their products and joins longer. Over listed
+  // pages 8 columns were the fastest or within 4% of it from 1 to 256 tokens of a sequence (8
+  // tokens of 32 sequences x 16 heads over 32 pages: 50 us, 16 columns 58, 32 columns 56; 32 tokens
+  // of one: 17, 21 and 30; 256: 44, 53 and 49; 512: 84, 88 and 75). Over the whole cache 16 columns
+  // win once passes of 8 would read 256 MB (65 MB: 20.5 us with 8, 23.3 with 16; 262 MB: 43.7 and
+  // 44.4; 524 MB: 67.2 and 60.3; 2.1 GB: 230 and 161), and 32 lose to them (94 and 170). The 4-bit
+  // cache goes by the same bytes, of 8 bits, though it reads 9/16 of them (us with 8, 16 and 32
+  // columns of 128 channels, 4 key heads x 8 heads unless said): 32 sequences of 4096 to 16384, 2
+  // tokens 76, 71 and 99, 4 tokens 154, 136 and 145, 8 tokens 279, 239 and 264; 64 of 2048 to
+  // 65536, 2 tokens 490, 401 and 602, 8 tokens 1423, 1192 and 1220; 32 of 1024 to 4096, 2 tokens 34
+  // (the choice), 37 and 48. It does not see that a tile of 16 may be half empty: 3 tokens 108, 122
+  // and 115 in the first, 652, 691 and 638 in the second, 46, 56 and 58 in the third; 5 tokens of 4
+  // heads, 8 key heads, 16 sequences of 2048 to 32768 205, 224 and 216. Over lists 8 columns win:
+  // 64 sequences x 32 pages, 2 tokens 39, 49 and 54, 4 tokens 71, 80 and 72, 8 tokens 117, 125 and
+  // 133.
   const int group = q_heads / kv_heads;
   const int64_t mean = single_rows ? 1 : (num_tokens + num_seqs - 1) / num_seqs;
   const int64_t passes = (mean * group + 7) / 8;
@@ -212,7 +221,10 @@ int make_plan(int64_t num_tokens, int num_seqs, int single_rows, int q_heads, in
   p.workers = info->sm_count * attention_ctas_per_sm(p.columns, head_dim);
   if (p.workers > most_workers(p.columns, head_dim)) p.workers = most_workers(p.columns, head_dim);
   // A CTA's four warps take 32 tokens each at a time; with 128 tokens a CTA its part of the join
-  // outweighs its own work (four short sequences: 21.3 us, 17.0 with 256, 18.0 with 512).
+  // outweighs its own work (four short sequences: 21.3 us, 17.0 with 256, 18.0 with 512). In 4 bits
+  // two sequences of 4000 to 9000 in pages of 16 took 18.8 us, 17.1 with 256 and 17.8 with 512, four
+  // of 1500 to 3000 in pages of 64 17.4, 17.8 and 18.4; shorter ones fare better with fewer: four of
+  // 200 to 900 tokens 10.6, 15.2 and 17.3, 16 of them 19.7, 19.3 and 23.2, and 14.2 with 64.
   p.min_units = 256 / page_size;
   p.counter_bytes = ((uint64_t)p.workers * 4 + 15) / 16 * 16;
   // The prompt's kernel takes 128 rows (tokens x heads) at a time and does not split a tile: it

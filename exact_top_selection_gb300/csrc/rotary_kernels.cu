@@ -231,10 +231,16 @@ int launch_parts(const RotaryArgs& a, const BatchArgs& b, dim3 grid, int tokens,
 template <bool kFp16, bool kNeighbours>
 int launch(const RotaryArgs& a, const BatchArgs& b, cudaStream_t stream) {
   const int heads = a.q_heads + a.k_heads;
-  const int64_t waves = 152 * 8;
+  const int64_t waves = 152 * 8;  // eight CTAs for each of GB300's SMs
+  // Four tokens a CTA (us for 36 heads of 128 channels, with 1, 2 and 4): 4864 tokens 25.4, 19.4
+  // and 18.7, 20000 tokens 98.6, 66.4 and 61.4; 2432 tokens, which get one, 14.1, 11.2 and 11.7,
+  // 1000 7.5, 7.9 and 8.0. (Behind a cold L2, as below.)
   const int tokens = a.num_tokens >= waves * kMostTokens ? kMostTokens : 1;
   const int64_t ctas = (a.num_tokens + tokens - 1) / tokens;
-  // heads apart until there are some waves of CTAs
+  // Heads apart while there are no more CTAs than that. Each works out its token's angles: of 64
+  // tokens x 36 heads 1024 CTAs, with rows for 16 or 24 of their 256 threads, take 6.1 us, where up to
+  // 152 x 1, 2, 4 and 16 CTAs take 3.2, 3.4, 3.6 and 9.2. 16 tokens 3.9 (3.2, 3.6, 3.6, 4.0), 256
+  // tokens 6.0 (3.9, 3.8, 3.8, 9.4), 1000 tokens 7.7 (7.4, 7.7, 7.5, 10.6).
   int split = 1;
   while (split * 2 <= heads && ctas * split * 2 <= waves) split *= 2;
   const dim3 grid((unsigned)ctas, (unsigned)split);

@@ -10,8 +10,10 @@
 // lengths and the ring's place writes the new ones.
 //
 // Little is moved (4 bytes for a page, 8 for a row): a call is bound by its latency, 3.2 us for a
-// decoding step of 64 sequences, 7.4 for 1000 prompts of 1 M tokens in pages of 16. (A CTA that
-// forms the sums ahead of a second kernel that fills in took 11.4.)
+// decoding step of 64 sequences, 7.4 for 1000 prompts of 1 M tokens in pages of 16. Of those 7.4
+// the sums over the sequences are most: 1000 sequences with a token each take 6.6, one sequence
+// 4.0, and 4096 15.6. They are five scans of 64 bits, one behind the other's exchange, in every
+// CTA. (A CTA that forms them ahead of a second kernel that fills in took 11.4.)
 
 #include <climits>
 
@@ -21,9 +23,17 @@
 namespace etk {
 namespace {
 
-constexpr int kAloneThreads = 256;  // one CTA does it all where there are few units
+// One CTA does it all where there are few units, as many as the call may have: it saves the last
+// arrival (64 sequences x 1 token, 129 units, 3.8 us against 4.1), but fills unit by unit what many
+// fill at once. Where all units are in use the two cross at about 300: 64 x 8 tokens, 160 units,
+// 4.4 and 4.6; 256 x 1 token, 528 units, 6.6 and 5.6; 64 x 128 tokens, 640 units, 7.7 and 6.1;
+// beyond the limit 11.6 and 6.2 for 1064 units, 25.8 and 6.9 for 3000. (Device time behind a cold
+// L2.)
+constexpr int kAloneThreads = 256;
 constexpr int kAloneUnits = 1024;
-constexpr int kThreads = 512;       // else
+constexpr int kThreads = 512;
+// Two CTAs an SM: 66 K units 7.8 us (152 CTAs 7.9, 608 7.8), 250 K units 10.1 (12.0, 12.8), a
+// million 25.0 (32.0, 28.1).
 constexpr int kMostCtas = 304;
 constexpr int kOwnRows = 4;         // a unit's rows that its own thread writes
 
